@@ -1,4 +1,5 @@
-"""GB300-native FlashAttention-2 forward pass (sm_103a).
+"""GB300-native FlashAttention-2 forward pass (sm_103a), its backward pass, and
+attention over a paged key/value cache (``paged``).
 
 Python binding of ``libfa2.so`` (C ABI in ``include/fa2.h``).  This module
 only marshals arguments: every step of the attention pass runs in the
@@ -25,6 +26,7 @@ FA2_ERR_MEMORY = 8
 FA2_ERR_DEVICE = 9
 FA2_ERR_SCRATCH = 10
 FA2_ERR_DTYPE = 11
+FA2_ERR_PAGE = 12
 
 FA2_DTYPE_BF16 = 0
 FA2_DTYPE_FP16 = 1
@@ -47,10 +49,43 @@ SIGNATURES = {
     "fa2_backward_workspace_bytes": (_Z, [_I, _I, _I]),
     "fa2_backward": (_I, [_P] * 9 + [_I] * 6 + [ctypes.c_float, _P, _Z, _P]),
     "fa2_backward_typed": (_I, [_P] * 9 + [_I] * 6 + [ctypes.c_float, _I, _P, _Z, _P]),
+    "fa2_forward_paged": (_I, [_P, _P, _LL, _LL, _P, _P, _P, _I, _I, _I, _F, _I, _P, _Z, _P]),
+    "fa2_forward_paged_workspace_bytes": (_Z, [_I] * 6),
+    "fa2_rope": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _LL, _P, _I, _I, _F, _I, _I, _P]),
+    "fa2_append_paged": (_I, [_P] * 9 + [_I, _P, _I, _P, _I, _I, _F, _P]),
+    "fa2_pages_workspace_bytes": (_Z, [_I, _I]),
+    "fa2_pages_reserve": (_I, [_P, _P, _P, _P, _Z, _P]),
+    "fa2_pages_fork": (_I, [_P, _P, _P, _P, _I, _P, _P, _Z, _P]),
+    "fa2_pages_free": (_I, [_P, _P, _I, _P]),
+    "fa2_pages_compact": (_I, [_P, _P, _P, _P, _Z, _P]),
+    "fa2_pages_copy": (_I, [_P, _P, _P, _I, _P, _Z, _P]),
     "fa2_status_string": (ctypes.c_char_p, [_I]),
     "fa2_device_status": (_I, [_P, _I]),
     "fa2_check_wait_timeout": (_I, [ctypes.c_ulonglong, _P]),
 }
+
+
+
+class PagedCacheArgs(ctypes.Structure):
+    """fa2_paged_cache of the C header."""
+
+    _fields_ = [("k_pages", _P), ("v_pages", _P), ("num_pages", _I), ("kv_heads", _I), ("page_size", _I),
+                ("d", _I), ("page_stride", _LL), ("head_stride", _LL), ("slot_stride", _LL), ("dtype", _I),
+                ("page_table", _P), ("table_stride", _LL), ("table_width", _I), ("B", _I), ("kv_lens", _P)]
+
+
+class PageTablesArgs(ctypes.Structure):
+    """fa2_page_tables of the C header."""
+
+    _fields_ = [("page_table", _P), ("table_stride", _LL), ("table_width", _I), ("B", _I), ("lens", _P),
+                ("refs", _P), ("num_pages", _I), ("page_size", _I)]
+
+
+class PagePoolsArgs(ctypes.Structure):
+    """fa2_page_pools of the C header (``planes``: an array of device pointers)."""
+
+    _fields_ = [("planes", _P), ("num_planes", _I), ("num_pages", _I), ("page_stride", _LL), ("page_bytes", _LL)]
+
 
 _lib = None
 
@@ -400,3 +435,7 @@ def backward(q, k, v, o, lse, do, causal: bool = False, scale: float | None = No
     if rc != FA2_OK:
         raise FA2Error(rc, "fa2_backward_typed")
     return dq, dk, dv
+
+
+from .paged import (append_paged, forward_paged, pages_compact, pages_copy, pages_fork, pages_free,  # noqa: E402
+                    pages_reserve, rope, rope_backward, rope_inv_freq)

@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "fa2.h"
+#include "fa2_host.h"
 #include "fa2_launch.h"
 
 namespace {
@@ -71,7 +72,8 @@ int device_ready() {
         fa2host::prepare_tc_d64_f16() != cudaSuccess || fa2host::prepare_tc_d128_f16() != cudaSuccess ||
         fa2host::prepare_tc_d256_bf16() != cudaSuccess || fa2host::prepare_tc_d256_f16() != cudaSuccess ||
         fa2host::prepare_tc_pair_d128() != cudaSuccess || fa2host::prepare_simt() != cudaSuccess ||
-        fa2host::prepare_bwd() != cudaSuccess || fa2host::prepare_bwd2() != cudaSuccess)
+        fa2host::prepare_bwd() != cudaSuccess || fa2host::prepare_bwd2() != cudaSuccess ||
+        fa2host::prepare_paged_bf16() != cudaSuccess || fa2host::prepare_paged_f16() != cudaSuccess)
       return;
     st.usable = true;
   });
@@ -215,6 +217,33 @@ bool encode_map_out(CUtensorMap* map, const void* base, int d, int Nq, long long
   return r == CUDA_SUCCESS;
 }
 
+}  // namespace
+
+// What the other host units share with this one.
+namespace fa2host {
+
+int require_device() { return device_ready(); }
+int device_sms() { return sm_count(); }
+bool device_memory_ok(const void* p, size_t bytes) { return device_range_ok(p, bytes); }
+int* device_status_word() { return status_word(); }
+unsigned long long wait_timeout_ns() { return kWaitTimeoutNs; }
+
+bool encode_tiled(CUtensorMap* map, bool f16, int rank, const void* base, const unsigned long long* dims,
+                  const unsigned long long* strides, const unsigned* box) {
+  cuuint64_t d[5], st[4];
+  cuuint32_t b[5], estr[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    estr[i] = 1;
+    if (i + 1 < rank) st[i] = strides[i];
+  }
+  return driver().encode(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                         static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, st, b, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Multiplier and shift of fa2dev::fast_div for a divisor d >= 1.
 fa2dev::FastDiv make_fast_div(int d) {
   int l = 0;
@@ -225,6 +254,12 @@ fa2dev::FastDiv make_fast_div(int d) {
   f.s = 31 + l;
   return f;
 }
+
+}  // namespace fa2host
+
+namespace {
+
+using fa2host::make_fast_div;
 
 // Head dimensions of the tensor-core forward kernels (and of the merge).
 bool forward_head_dim(int d) { return d == 64 || d == 128 || d == 256; }
@@ -691,6 +726,7 @@ extern "C" const char* fa2_status_string(int status) {
     case FA2_ERR_DEVICE: return "no usable sm_103 device is current";
     case FA2_ERR_SCRATCH: return "the problem needs more split-KV scratch than the library's 32 MiB static buffer";
     case FA2_ERR_DTYPE: return "unsupported element types (Q/K/V bf16 or fp16; O fp32 or the Q/K/V type)";
+    case FA2_ERR_PAGE: return "a page number, length or offset read on the device lies outside the cache";
     default: return "unknown status";
   }
 }
@@ -730,7 +766,8 @@ extern "C" int fa2_device_status(fa2_stream_t stream, int reset) {
     const int z = 0;
     if (cudaMemcpyToSymbol(g_device_status, &z, sizeof z) != cudaSuccess) return FA2_ERR_LAUNCH;
   }
-  return v ? FA2_ERR_TIMEOUT : FA2_OK;
+  if (v & fa2dev::kDevErrTimeout) return FA2_ERR_TIMEOUT;
+  return v ? FA2_ERR_PAGE : FA2_OK;
 }
 
 // ---------------------------------------------------------------------------

@@ -10,6 +10,7 @@
 #include "fa2_fwd_simt.cuh"
 #include "fa2_fwd_pair_sm103.cuh"
 #include "fa2_fwd_sm103.cuh"
+#include "fa2_paged_sm103.cuh"
 
 namespace fa2host {
 
@@ -66,5 +67,15 @@ cudaError_t prepare_bwd2();
 cudaError_t launch_bwd2(bool causal, bool f16, const CUtensorMap& mq64, const CUtensorMap& mk,
                         const CUtensorMap& mv, const CUtensorMap& mdo64, const CUtensorMap& mdq32,
                         const fa2dev::BwdParams& p, unsigned grid, cudaStream_t s);
+
+// Attention over a paged cache (fa2_paged_bf16.cu, fa2_paged_f16.cu): the
+// partial or final results, then the merge of items cut into key ranges
+// (merge_grid = 0: no item can be cut).
+cudaError_t prepare_paged_bf16();
+cudaError_t prepare_paged_f16();
+cudaError_t launch_paged_bf16(int d, int subs, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                              const fa2dev::PagedParams& p, unsigned grid, unsigned merge_grid, cudaStream_t s);
+cudaError_t launch_paged_f16(int d, int subs, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                             const fa2dev::PagedParams& p, unsigned grid, unsigned merge_grid, cudaStream_t s);
 
 }  // namespace fa2host

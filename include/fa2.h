@@ -69,7 +69,8 @@ typedef enum {
   FA2_ERR_MEMORY = 8,   /* a pointer is not device memory, or its buffer is too small */
   FA2_ERR_DEVICE = 9,   /* no usable sm_103 device is current */
   FA2_ERR_SCRATCH = 10, /* split-KV scratch needed exceeds the library's static buffer */
-  FA2_ERR_DTYPE = 11    /* unsupported element type combination */
+  FA2_ERR_DTYPE = 11,   /* unsupported element type combination */
+  FA2_ERR_PAGE = 12     /* a page number, length or offset read on the device lies outside the cache */
 } fa2_status;
 
 /* Element types for fa2_forward_typed. */
@@ -293,14 +294,193 @@ int fa2_backward_typed(const void *Q, const void *K, const void *V, const float 
                        int Nk, int d, int causal, float scale, int qkv_dtype, void *workspace,
                        size_t workspace_size, fa2_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * A paged key/value cache: rotary positions, writing new tokens, attention of
+ * new tokens over the cache, and the pages' management.
+ *
+ * A cache is two arrays of pages, K and V, each [num_pages, kv_heads,
+ * page_size, d] of bf16 or fp16 with any strides whose last dimension is dense
+ * (a [num_pages, page_size, kv_heads, d] layout is the same with the strides
+ * exchanged; K and V have the same strides).  Sequence b's token t lies in slot
+ * t % page_size of page page_table[b][t / page_size].  kv_lens[b] counts the
+ * sequence's tokens, the new ones of the call among them: c_b new tokens are
+ * its positions kv_lens[b] - c_b .. kv_lens[b] - 1.  New tokens are packed:
+ * sequence b's are rows cu_q[b] .. cu_q[b+1]-1 of [T, heads, d] arrays (cu_q
+ * ascending, cu_q[B] <= T; rows from cu_q[B] on belong to nobody and are
+ * neither read nor written), or row b alone when cu_q is NULL (T = B: one new
+ * token per sequence).
+ *
+ * Page tables, lengths and offsets are device memory that the kernels read when
+ * they run, so a captured launch may be replayed after they changed.  What they
+ * hold cannot be checked on the host: a page number outside [0, num_pages), a
+ * length that is negative or longer than the table row (table_width *
+ * page_size) and offsets outside [0, T] never make a kernel read or write out
+ * of range; it reads zeros or writes nothing there, and the device status word
+ * then reports FA2_ERR_PAGE (fa2_device_status).  Table entries behind a
+ * sequence's last page are not read, slots behind its last token may hold
+ * anything.
+ */
+typedef struct {
+  void *k_pages, *v_pages;   /* 16-byte aligned */
+  int num_pages, kv_heads;
+  int page_size;             /* a power of two, 16 .. 1024 */
+  int d;                     /* 64, 128 or 256 */
+  /* in elements, multiples of 8, at least d; ignored for a dimension of size 1 */
+  long long page_stride, head_stride, slot_stride;
+  int dtype;                 /* FA2_DTYPE_BF16 or FA2_DTYPE_FP16 */
+  const int *page_table;     /* [B, table_width], rows table_stride apart */
+  long long table_stride;
+  int table_width;           /* table_width * page_size <= 2^30 */
+  int B;
+  const int *kv_lens;        /* [B] */
+} fa2_paged_cache;
+
+/*
+ * Attention of the new tokens over the cache.  Query heads share key/value
+ * heads in groups of Hq / kv_heads (at most 128): head h reads key/value head
+ * h / (Hq / kv_heads).  For new token i of sequence b (position p = kv_lens[b]
+ * - c_b + i): over the keys j < kv_lens[b], j <= p when causal,
+ *     O_i = sum_j softmax_j(scale q_i . k_j) v_j,  LSE_i = log sum_j exp(scale q_i . k_j)
+ * A row without keys (kv_lens[b] = 0, or p < 0 under the causal mask) gets
+ * O = 0 and LSE = -inf.
+ *   Q          [T, Hq, d] of the cache's type, 16-byte aligned; token and head
+ *              strides in elements, multiples of 8, at least d
+ *   O          dense [T, Hq, d], fp32 or the cache's type (o_dtype)
+ *   LSE        dense fp32 [T, Hq]
+ *   workspace  256-byte aligned device memory of at least
+ *              fa2_forward_paged_workspace_bytes bytes; its contents do not
+ *              matter, on entry or afterwards.  Calls that may run at the same
+ *              time (streams, graphs) need one each.
+ * P is rounded to the cache's type for the P V product; sums are fp32.  The
+ * result does not depend on timing: repeated calls give the same bits.
+ * T = 0, Hq = 0 or B = 0 is a valid empty problem.  Errors as fa2_forward.
+ */
+int fa2_forward_paged(const fa2_paged_cache *cache, const void *Q, long long q_token_stride,
+                      long long q_head_stride, void *O, float *LSE, const int *cu_q, int T, int Hq,
+                      int causal, float scale, int o_dtype, void *workspace, size_t workspace_size,
+                      fa2_stream_t stream);
+
+/* Workspace of fa2_forward_paged on the current device; 0 for invalid arguments or an empty problem. */
+size_t fa2_forward_paged_workspace_bytes(int B, int T, int Hq, int kv_heads, int d, int has_cu_q);
+
+/*
+ * Rotary positions.  Pair i of the first rotary_dim columns of the row at
+ * position t -- columns (i, i + rotary_dim / 2), or (2i, 2i + 1) when
+ * interleaved -- becomes
+ *     (a, b) -> mscale (a cos(t f_i) - b sin(t f_i), b cos(t f_i) + a sin(t f_i)),
+ * f_i = inv_freq[i] radians per position (device memory, 64-bit; scaling for
+ * long contexts is a matter of these numbers and of mscale).  The other columns
+ * are copied.  transposed != 0 applies the transposed rotation: the gradient.
+ * Angles are exact to 2^-25 turns for any position below 2^31 in magnitude; products are fp32 and
+ * rounded once.
+ *   X, Y       [B, H, N, d], strides {batch, head, token} in elements; Y = X
+ *              (same strides) works in place, other overlaps are refused
+ *              (FA2_ERR_MEMORY).  d is even, at most 1024.  Interleaved
+ *              pairs must be aligned to two elements.
+ *   positions  int32, or int64 (positions_int64), [N] or [B, N]
+ *              (positions_batch_stride 0 or N)
+ *   dtype      of X and Y: bf16, fp16 or fp32
+ */
+int fa2_rope(const void *X, const long long *x_strides, void *Y, const long long *y_strides, int B,
+             int H, int N, int d, const void *positions, int positions_int64,
+             long long positions_batch_stride, const double *inv_freq, int rotary_dim,
+             int interleaved, float mscale, int transposed, int dtype, fa2_stream_t stream);
+
+/*
+ * Writes the new tokens' keys and values into their pages, the keys rotated at
+ * their positions (rotary_dim = 0: as they are); in the same launch rotates the
+ * queries Q [T, Hq, d] into Q_out (Hq = 0: none; Q_out = Q works in place).
+ * K, V [T, kv_heads, d]; strides {token, head} in elements, multiples of 8.
+ * Tokens at negative positions (c_b > kv_lens[b]) are not written.  The pages
+ * written must not be shared by sequences.
+ */
+int fa2_append_paged(const fa2_paged_cache *cache, const void *K, const long long *k_strides,
+                     const void *V, const long long *v_strides, const void *Q,
+                     const long long *q_strides, void *Q_out, const long long *q_out_strides, int Hq,
+                     const int *cu_q, int T, const double *inv_freq, int rotary_dim, int interleaved,
+                     float mscale, fa2_stream_t stream);
+
+/*
+ * The tables that the page functions manage: page_table [B, table_width] (-1:
+ * no page), lens [B] (tokens of each sequence) and refs [num_pages] (how many
+ * table entries name the page; 0: free).  All int32 on the device; start with
+ * -1, 0 and 0.  A page that several sequences share is full.  num_pages is at
+ * most 2^21 - 1.  Entries that contradict each other (a page number outside the
+ * pool, a freed page freed again, a sequence index outside [0, B)) are skipped
+ * and reported as FA2_ERR_PAGE by the device status word.
+ */
+typedef struct {
+  int *page_table;
+  long long table_stride;
+  int table_width, B;
+  int *lens, *refs;
+  int num_pages, page_size;
+} fa2_page_tables;
+
+/*
+ * The page data that moves with the tables: num_planes (0 .. 256) arrays of
+ * num_pages pages of page_bytes dense bytes (a multiple of 16), page_stride
+ * bytes apart; `planes` is a host array of device pointers.
+ */
+typedef struct {
+  void *const *planes;
+  int num_planes, num_pages;
+  long long page_stride, page_bytes;
+} fa2_page_pools;
+
+/* Workspace of any of the functions below for this pool and n pairs. */
+size_t fa2_pages_workspace_bytes(int num_pages, int n);
+
+/*
+ * lens[b] += add[b] (add[b] <= 0: nothing) and the pages that takes, the free
+ * pages of the lowest numbers in the order of the sequences.  All or nothing:
+ * *missing (device) becomes 0, or the number of pages that lack, or -1 where a
+ * table row is too short, and then nothing has changed.
+ */
+int fa2_pages_reserve(const fa2_page_tables *tables, const int *add, int *missing, void *workspace,
+                      size_t workspace_size, fa2_stream_t stream);
+
+/*
+ * For each of n pairs the empty sequence dst[i] becomes a copy of src[i]: its
+ * full pages are shared, its last page, when partly filled, is copied to a free
+ * one (lowest numbers first, in the order of the pairs).  A destination that is
+ * not empty, or named by an earlier pair, is skipped (FA2_ERR_PAGE).  Sources
+ * count as they were before the call.  *missing as in fa2_pages_reserve.
+ */
+int fa2_pages_fork(const fa2_page_tables *tables, const fa2_page_pools *pools, const int *src,
+                   const int *dst, int n, int *missing, void *workspace, size_t workspace_size,
+                   fa2_stream_t stream);
+
+/* Empties the n listed sequences (one listed twice: once) and frees pages that nobody names any more. */
+int fa2_pages_free(const fa2_page_tables *tables, const int *seqs, int n, fa2_stream_t stream);
+
+/*
+ * Moves the pages in use to the lowest numbers: with `used` of them, those of
+ * number >= used go, in ascending order, to the free numbers below it; tables
+ * and counts follow.  moved[p] (device, [num_pages]) is where page p went, p
+ * itself for one that stayed, -1 for a free one.
+ */
+int fa2_pages_compact(const fa2_page_tables *tables, const fa2_page_pools *pools, int *moved,
+                      void *workspace, size_t workspace_size, fa2_stream_t stream);
+
+/*
+ * Copies page src[i] to page dst[i], i < n (device lists).  Of several pairs
+ * with one destination the last counts.  A pair whose source is another pair's
+ * destination, or with a number outside the pool, is skipped (FA2_ERR_PAGE).
+ */
+int fa2_pages_copy(const fa2_page_pools *pools, const int *src, const int *dst, int n,
+                   void *workspace, size_t workspace_size, fa2_stream_t stream);
+
 /* Static description of a status code (never NULL). */
 const char *fa2_status_string(int status);
 
 /*
  * Synchronises `stream`, then reports whether any kernel of this library on
  * the current device has set its device status word since the last reset:
- * FA2_OK, FA2_ERR_TIMEOUT, or FA2_ERR_LAUNCH if the synchronisation itself
- * failed.  reset != 0 clears the word afterwards.
+ * FA2_OK, FA2_ERR_TIMEOUT, FA2_ERR_PAGE (see the paged-cache functions; a
+ * timeout is reported before it), or FA2_ERR_LAUNCH if the synchronisation
+ * itself failed.  reset != 0 clears the word afterwards.
  */
 int fa2_device_status(fa2_stream_t stream, int reset);
 
