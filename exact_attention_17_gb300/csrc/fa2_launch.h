@@ -14,6 +14,22 @@
 
 namespace fa2host {
 
+// Launches a kernel that may start while the one before it on the stream still
+// runs; it waits for that one (griddepcontrol.wait) before it reads its results.
+template <typename Kernel, typename Params>
+cudaError_t launch_behind(Kernel kernel, dim3 grid, int threads, cudaStream_t s, const Params& p) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 // Raise the dynamic shared-memory limit of every kernel in the unit (current device).
 cudaError_t prepare_tc_d64_bf16();
 cudaError_t prepare_tc_d128_bf16();
@@ -70,12 +86,12 @@ cudaError_t launch_bwd2(bool causal, bool f16, const CUtensorMap& mq64, const CU
 
 // Attention over a paged cache (fa2_paged_bf16.cu, fa2_paged_f16.cu): the
 // partial or final results, then the merge of items cut into key ranges
-// (merge_grid = 0: no item can be cut).
+// (merge_grid.x = 0: no item can be cut).
 cudaError_t prepare_paged_bf16();
 cudaError_t prepare_paged_f16();
 cudaError_t launch_paged_bf16(int d, int subs, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                              const fa2dev::PagedParams& p, unsigned grid, unsigned merge_grid, cudaStream_t s);
+                              const fa2dev::PagedParams& p, unsigned grid, dim3 merge_grid, cudaStream_t s);
 cudaError_t launch_paged_f16(int d, int subs, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                             const fa2dev::PagedParams& p, unsigned grid, unsigned merge_grid, cudaStream_t s);
+                             const fa2dev::PagedParams& p, unsigned grid, dim3 merge_grid, cudaStream_t s);
 
 }  // namespace fa2host

@@ -97,35 +97,43 @@ bool rows_in_memory(const void* p, long long token, long long head, long long T,
 // How a call of fa2_forward_paged is laid out; depends on sizes alone.
 struct PagedPlan {
   int G, subs, sub_tokens, box_tokens, part_rows;
-  int target_units, slots;
+  bool narrow;            // blocks of at most 32 rows (single tokens)
+  bool even;              // equal ranges of key tiles, one per CTA of a single wave
+  int ctas, slots;
   long long items;        // most (sequence, block, head) items there can be
   size_t bytes;           // workspace
 };
 
 int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 
+// Blocks of queries that fill this many waves of CTAs are taken one item per CTA.
+constexpr int kItemWaves = 4;
+// Least key tiles of a range.
+constexpr int kMinTiles = 2;
+
 // Sub-tiles per CTA: two (256 rows on one K/V stream) where the sequences'
-// average chunk fills more than one sub-tile, else one with two CTAs per SM.
+// average chunk fills more than one sub-tile, else one with two CTAs per SM, of
+// at most 32 rows where the average chunk has no more.
 PagedPlan plan_paged(int B, int T, int Hq, int Hkv, int d, bool has_cu, int sms) {
   PagedPlan q;
   q.G = Hq / Hkv;
   q.subs = has_cu && d != 256 && static_cast<long long>(T) * q.G > 128ll * B ? 2 : 1;
   // Q boxes start on whole 1024-byte swizzle atoms (8 rows): the tokens per
   // box are the fewest that fill whole atoms, where 128 rows hold that many.
-  const int most = 128 / q.G, unit = 8 / gcd(q.G, 8);
+  q.narrow = q.G <= 32 && (!has_cu || static_cast<long long>(T) * q.G <= 32ll * B);
+  const int most = (q.narrow ? 32 : 128) / q.G, unit = 8 / gcd(q.G, 8);
   q.box_tokens = most >= unit ? unit : most;
   q.sub_tokens = most / q.box_tokens * q.box_tokens;
   const int block = q.sub_tokens * q.subs;
   q.items = (has_cu ? T / block + static_cast<long long>(B < T ? B : T) : B) * Hkv;
-  q.target_units = sms * (q.subs == 2 || d == 256 ? 1 : 2) * 2;
-  q.slots = 2 * q.target_units;
+  q.ctas = sms * (q.subs == 2 || d == 256 ? 1 : 2);
+  q.even = !has_cu || T / block * static_cast<long long>(Hkv) < kItemWaves * static_cast<long long>(q.ctas);
+  q.slots = 2 * q.ctas;
   const long long rows = static_cast<long long>(has_cu ? (T < block ? T : block) : 1) * q.G;
   q.part_rows = static_cast<int>(rows);
   q.bytes = align256(static_cast<size_t>(q.slots) * rows * d * 4) + align256(static_cast<size_t>(q.slots) * rows * 4);
   return q;
 }
-
-constexpr int kMinTilesPerUnit = 2;
 
 }  // namespace
 
@@ -166,7 +174,7 @@ extern "C" int fa2_forward_paged(const fa2_paged_cache* cache, const void* Q, lo
       !range_ok(LSE, rows, 4) || (cu_q && !range_ok(cu_q, c.B + 1ll, 4)) || workspace_size < plan.bytes ||
       !fa2host::device_memory_ok(workspace, plan.bytes))
     return FA2_ERR_MEMORY;
-  const long long grid = plan.items + plan.target_units;
+  const long long grid = plan.even ? plan.ctas : plan.items + plan.ctas;
   if (grid > 0x7fffffffll) return FA2_ERR_SHAPE;
 
   using ull = unsigned long long;
@@ -209,18 +217,24 @@ extern "C" int fa2_forward_paged(const fa2_paged_cache* cache, const void* Q, lo
   p.table_width = c.table_width;
   p.table_stride = c.table_stride;
   p.max_len = c.table_width << p.page_log2;
-  p.target_units = plan.target_units;
-  p.min_tiles = kMinTilesPerUnit;
+  p.even = plan.even ? 1 : 0;
+  p.ctas = plan.ctas;
+  p.inv_ctas = 1.0 / plan.ctas;
+  p.min_tiles = kMinTiles;
   p.causal = causal != 0;
   p.o_half = half_out ? 1 : 0;
+  p.narrow = plan.narrow ? 1 : 0;
   p.scale_log2 = scale * kLog2e;
   p.status = fa2host::device_status_word();
   p.timeout_ns = fa2host::wait_timeout_ns();
   if (p.status == nullptr) return FA2_ERR_LAUNCH;
-  const long long merge = plan.items < plan.target_units ? plan.items : plan.target_units;
+  // columns: items that may be cut; rows: warps for their rows
+  constexpr int kMergeRows = fa2dev::kPagedMergeWarps * fa2dev::kPagedMergeRows;
+  dim3 merge(static_cast<unsigned>(plan.even ? plan.ctas - 1 : plan.ctas),
+             static_cast<unsigned>((plan.part_rows + kMergeRows - 1) / kMergeRows));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const auto launch = f16 ? fa2host::launch_paged_f16 : fa2host::launch_paged_bf16;
-  return launch(c.d, plan.subs, mq, mk, mv, p, static_cast<unsigned>(grid), static_cast<unsigned>(merge), s) ==
+  return launch(c.d, plan.subs, mq, mk, mv, p, static_cast<unsigned>(grid), merge, s) ==
                  cudaSuccess
              ? FA2_OK
              : FA2_ERR_LAUNCH;
@@ -236,9 +250,9 @@ int check_rotary(const double* inv_freq, int rotary_dim, int d, float mscale) {
   return FA2_OK;
 }
 
-// 16-byte vectors fill the rotated columns (their halves, unless interleaved) and the rest.
+// Whole vectors fill the rotated columns (their halves, unless interleaved) and the rest.
 bool wide_rotary(int d, int r, bool interleaved, int elem) {
-  const int w = 16 / elem;
+  const int w = fa2host::rope_width(elem, interleaved);
   return d % w == 0 && (interleaved ? r % w == 0 : r % (2 * w) == 0);
 }
 
@@ -258,14 +272,15 @@ extern "C" int fa2_rope(const void* X, const long long* x_strides, void* Y, cons
   const int elem = dtype == FA2_DTYPE_FP32 ? 4 : 2;
   const long long sizes[3] = {B, H, N};
   long long xs[3], ys[3];
-  bool wide = wide_rotary(d, rotary_dim, interleaved != 0, elem) && !misaligned(X, 15) && !misaligned(Y, 15);
+  const int vec = fa2host::rope_width(elem, interleaved != 0) * elem;   // bytes
+  bool wide = wide_rotary(d, rotary_dim, interleaved != 0, elem) && !misaligned(X, vec - 1) && !misaligned(Y, vec - 1);
   bool pairs = !misaligned(X, 2 * elem - 1) && !misaligned(Y, 2 * elem - 1);
   for (int i = 0; i < 3; ++i) {
     xs[i] = sizes[i] > 1 ? x_strides[i] : 0;
     ys[i] = sizes[i] > 1 ? y_strides[i] : 0;
     // reading the same row twice is fine, writing it twice is not
     if (xs[i] < 0 || xs[i] > kMaxStride || (sizes[i] > 1 && (ys[i] < d || ys[i] > kMaxStride))) return FA2_ERR_SHAPE;
-    wide = wide && xs[i] * elem % 16 == 0 && ys[i] * elem % 16 == 0;
+    wide = wide && xs[i] * elem % vec == 0 && ys[i] * elem % vec == 0;
     pairs = pairs && xs[i] % 2 == 0 && ys[i] % 2 == 0;
   }
   if (misaligned(X, elem - 1) || misaligned(Y, elem - 1) || misaligned(positions, positions_int64 ? 7 : 3) ||

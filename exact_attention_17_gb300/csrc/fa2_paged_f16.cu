@@ -1,5 +1,5 @@
 // Attention over a paged cache: f16 inputs (head dimensions 64, 128, 256; one
-// or two query sub-tiles per CTA).
+// or two query sub-tiles per CTA, or one of at most 32 rows).
 #include "fa2_launch.h"
 
 namespace fa2host {
@@ -7,39 +7,40 @@ namespace fa2host {
 namespace {
 constexpr bool kF16 = true;
 
-template <int D, int SUBS>
+template <int D, int SUBS, bool NARROW>
 cudaError_t set_limits() {
-  return cudaFuncSetAttribute(fa2dev::fa2_paged_tc_kernel<D, kF16, SUBS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              fa2dev::FwdConfig<D, SUBS>::kSmemBytes);
+  return cudaFuncSetAttribute(fa2dev::fa2_paged_tc_kernel<D, kF16, SUBS, NARROW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              fa2dev::PagedConfig<D, SUBS>::kSmemBytes);
 }
 
-template <int D, int SUBS>
+template <int D, int SUBS, bool NARROW>
 cudaError_t run(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const fa2dev::PagedParams& p,
-                unsigned grid, unsigned merge_grid, cudaStream_t s) {
-  fa2dev::fa2_paged_tc_kernel<D, kF16, SUBS>
-      <<<grid, fa2dev::FwdShape<SUBS>::kThreads, fa2dev::FwdConfig<D, SUBS>::kSmemBytes, s>>>(mq, mk, mv, p);
+                unsigned grid, dim3 merge_grid, cudaStream_t s) {
+  fa2dev::fa2_paged_tc_kernel<D, kF16, SUBS, NARROW>
+      <<<grid, fa2dev::FwdShape<SUBS>::kThreads, fa2dev::PagedConfig<D, SUBS>::kSmemBytes, s>>>(mq, mk, mv, p);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || merge_grid == 0) return e;
-  fa2dev::fa2_paged_merge_kernel<D, kF16, SUBS><<<merge_grid, fa2dev::kPagedMergeWarps * 32, 0, s>>>(p);
-  return cudaGetLastError();
+  if (e != cudaSuccess || merge_grid.x == 0) return e;
+  return launch_behind(fa2dev::fa2_paged_merge_kernel<D, kF16, SUBS>, merge_grid, fa2dev::kPagedMergeWarps * 32, s, p);
 }
 }  // namespace
 
 cudaError_t prepare_paged_f16() {
   cudaError_t e;
-  if ((e = set_limits<64, 1>()) != cudaSuccess || (e = set_limits<64, 2>()) != cudaSuccess ||
-      (e = set_limits<128, 1>()) != cudaSuccess || (e = set_limits<128, 2>()) != cudaSuccess)
+  if ((e = set_limits<64, 1, false>()) != cudaSuccess || (e = set_limits<64, 2, false>()) != cudaSuccess ||
+      (e = set_limits<128, 1, false>()) != cudaSuccess || (e = set_limits<128, 2, false>()) != cudaSuccess ||
+      (e = set_limits<256, 1, false>()) != cudaSuccess || (e = set_limits<64, 1, true>()) != cudaSuccess ||
+      (e = set_limits<128, 1, true>()) != cudaSuccess)
     return e;
-  return set_limits<256, 1>();
+  return set_limits<256, 1, true>();
 }
 
 cudaError_t launch_paged_f16(int d, int subs, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                              const fa2dev::PagedParams& p, unsigned grid, unsigned merge_grid, cudaStream_t s) {
-  if (d == 64)
-    return subs == 1 ? run<64, 1>(mq, mk, mv, p, grid, merge_grid, s) : run<64, 2>(mq, mk, mv, p, grid, merge_grid, s);
-  if (d == 128)
-    return subs == 1 ? run<128, 1>(mq, mk, mv, p, grid, merge_grid, s) : run<128, 2>(mq, mk, mv, p, grid, merge_grid, s);
-  return run<256, 1>(mq, mk, mv, p, grid, merge_grid, s);
+                              const fa2dev::PagedParams& p, unsigned grid, dim3 merge_grid, cudaStream_t s) {
+  const auto f = p.narrow ? (d == 64 ? run<64, 1, true> : d == 128 ? run<128, 1, true> : run<256, 1, true>)
+                 : d == 64 ? (subs == 1 ? run<64, 1, false> : run<64, 2, false>)
+                 : d == 128 ? (subs == 1 ? run<128, 1, false> : run<128, 2, false>)
+                            : run<256, 1, false>;
+  return f(mq, mk, mv, p, grid, merge_grid, s);
 }
 
 }  // namespace fa2host

@@ -15,6 +15,12 @@
 //    rows of the MMA instead of one, and K/V is read once per group.  Rows past
 //    the block's tokens compute on whatever the buffer holds (rows do not
 //    mix) and are not stored; a warp without a live row skips its softmax.
+//  * Few rows.  One warp's softmax of a tile costs the same for one live row as
+//    for 32, and as much as the tile's MMAs.  So a block of at most 32 rows
+//    (NARROW: single tokens) loads its queries four times, into each warp's 32
+//    rows of the tile, and warp w takes the keys 32 w .. 32 w + 31 of every tile:
+//    its P is zero elsewhere, so its rows of O hold the share of those keys.
+//    The four shares are merged at the end like parts of an item.
 //  * Pages.  A 128-key tile is read through a 4-D tensor map (column, slot,
 //    head, page), one box per page and 64 columns, page numbers from the table
 //    (32 entries at a time in the producer warp's lanes).  Any strides that TMA
@@ -25,12 +31,20 @@
 //    (0 * NaN is NaN in the MMA) are overwritten with zeros in shared memory
 //    by the softmax threads before they announce P.
 //  * Schedule.  Lengths live on the device and may change between replays of a
-//    captured launch, so each CTA finds its work unit itself: the tiles of all
-//    (sequence, query block, head) items are counted, L = ceil(tiles / target)
-//    key tiles make one unit, and a warp scan over the sequences finds unit
-//    blockIdx.x.  An item of more than L tiles is cut into several units, whose
-//    normalised O and LSE go to the workspace and are merged by a second kernel
-//    (the merge of fa2_combine.cu, in range order, so results do not vary).
+//    captured launch, so the kernel finds its work itself.  An item is a
+//    (sequence, block of tokens, key/value head), its cost its keys and a fixed
+//    part.  With `even` the list of all items is cut into ranges of equal cost,
+//    one per CTA of a single wave: a CTA walks its range segment by segment, at
+//    most its first and last segment being parts of an item.
+//    Without it (many items, the host's choice) a CTA takes one item, in an
+//    order that keeps a group of heads in L2, items of more than an even share
+//    of the tiles being cut.  A part's normalised O and LSE go to the workspace,
+//    and a second kernel merges them (as fa2_combine.cu, in the order of the
+//    keys: results do not depend on timing).
+//  * Segments.  The producer warp runs ahead: it loads the next segment's Q and
+//    first tiles while the current one finishes.  One named barrier per segment,
+//    which every role passes for every segment, also after an abort, hands over
+//    the segment's description.
 #pragma once
 
 #include "fa2_fwd_sm103.cuh"
@@ -46,7 +60,7 @@ struct PagedParams {
   const int* cu_q;         // [B + 1], or null: one token per sequence
   void* O;                 // [T, Hq, D] fp32, or the input type (o_half)
   float* LSE;              // [T, Hq]
-  float* O_part;           // [slots][part_rows][D]
+  float* O_part;           // [slots][D / 4][part_rows][4]: a warp's rows write 512 neighbouring bytes
   float* LSE_part;         // [slots][part_rows]
   int slots;
   int part_rows;
@@ -58,26 +72,29 @@ struct PagedParams {
   int table_width;
   long long table_stride;
   int max_len;             // table_width << page_log2, at most 2^30
-  int target_units;
-  int min_tiles;           // least key tiles per unit
+  int even;                // equal ranges of the work, one per CTA (else one item per CTA)
+  int ctas;                // even: ranges; else the number of equal shares above which an item is cut
+  double inv_ctas;
+  int min_tiles;           // least key tiles per range
   int causal;
   int o_half;
+  int narrow;              // blocks of at most 32 rows
   float scale_log2;
   int* status;
   unsigned long long timeout_ns;
 };
 
-// One work unit: key tiles [t_begin, t_end) of a block of tokens and a head.
+// Key tiles [t_begin, t_end) of an item.
 struct PagedUnit {
   int valid;
-  int b, head;
+  int head;
   int row0;       // first token of the block in the packed queries
   int tok0;       // the same within its sequence
   int ntok;       // tokens of the block
   int q_len, kv_len;
   int t_begin, t_end;
-  int splits, split;
-  int slot;       // workspace slot of split 0 is slot - split (splits > 1)
+  int slot;       // workspace slot of this part, -1: the whole item
+  long long table;   // offset of the sequence's row in the page table
 };
 
 // Keys that the token `tok` of a sequence keeps: [0, kept).
@@ -85,132 +102,412 @@ __device__ __forceinline__ int paged_kept(int causal, int kv_len, int q_len, int
   return causal ? max(0, min(kv_len, kv_len - q_len + tok + 1)) : kv_len;
 }
 
+__device__ __forceinline__ int key_tiles_of(int keys) { return (keys + kKeysPerTile - 1) / kKeysPerTile; }
+
+// Sequence b's new tokens and keys.
+struct PagedSeq {
+  int q0, q_len, kv_len, blocks;
+};
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b, int block) {
+  PagedSeq s;
+  s.q0 = s.q_len = s.kv_len = 0;
+  if (b < p.B) {
+    const int begin = p.cu_q ? p.cu_q[b] : b;
+    const int end = p.cu_q ? p.cu_q[b + 1] : b + 1;
+    const int kv = p.kv_lens[b];
+    s.q0 = min(max(begin, 0), p.T);
+    s.q_len = max(0, min(end, p.T) - s.q0);
+    s.kv_len = min(max(kv, 0), p.max_len);
+    if (blockIdx.x == 0 && (begin < 0 || end < begin || end > p.T || kv < 0 || kv > p.max_len))
+      atomicOr(p.status, kDevErrPage);
+  }
+  s.blocks = (s.q_len + block - 1) / block;
+  return s;
+}
+
+// Cost of an item: kKeysPerItem for its start and end, then its keys, at least
+// one (a lone sub-tile takes about as long as two, whose MMAs and softmax
+// overlap).  Sums of costs over a sequence's blocks are closed forms in keys,
+// which tiles would not be; a position x inside an item stands for tile ceil((x
+// - kKeysPerItem) / 128), cut to the item's tiles.
+constexpr int kKeysPerItem = 256;
+
+__device__ __forceinline__ int block_keys(const PagedParams& p, const PagedSeq& s, int block, int i) {
+  return max(1, paged_kept(p.causal, s.kv_len, s.q_len, min((i + 1) * block, s.q_len) - 1));
+}
+
+// Cost of the blocks 0 .. i-1 of a sequence (0 <= i <= blocks).
+template <int SUBS>
+__device__ __forceinline__ long long cost_before(const PagedParams& p, const PagedSeq& s, int i) {
+  if (i == 0) return 0;
+  const int block = p.sub_tokens * SUBS;
+  // all but the last block are full: block k keeps kv_len - q_len + (k + 1) block keys when causal
+  const int full = i == s.blocks ? i - 1 : i;
+  long long keys;
+  if (p.causal) {
+    const long long lead = static_cast<long long>(s.kv_len) - s.q_len;
+    const int none = lead >= 0 ? 0 : min(full, static_cast<int>(-lead) / block);   // blocks without a key count one
+    const long long n = full - none;
+    keys = none + n * (lead + none * static_cast<long long>(block)) + block * (n * (n + 1) / 2);
+  } else {
+    keys = static_cast<long long>(full) * max(1, s.kv_len);
+  }
+  keys += static_cast<long long>(i) * kKeysPerItem;
+  if (i == s.blocks) keys += max(1, s.kv_len);
+  return keys;
+}
+
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+__device__ __forceinline__ long long warp_scan(long long v) {   // inclusive
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long a = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += a;
+  }
+  return v;
+}
+
+__device__ __forceinline__ PagedSeq seq_from(const PagedSeq& s, int src) {
+  PagedSeq r;
+  r.q0 = __shfl_sync(0xffffffffu, s.q0, src);
+  r.q_len = __shfl_sync(0xffffffffu, s.q_len, src);
+  r.kv_len = __shfl_sync(0xffffffffu, s.kv_len, src);
+  r.blocks = __shfl_sync(0xffffffffu, s.blocks, src);
+  return r;
+}
+
+// An item in the list of all items (sequences, their heads, their blocks) and
+// the cost of all items before it.
+struct PagedPlace {
+  int b, head, i;
+  int tiles;
+  long long start, cost;
+  PagedSeq s;
+
+  // the item's tile at position `pos` of the list
+  __device__ __forceinline__ int tile(long long pos) const {
+    const long long x = pos - start - kKeysPerItem;
+    if (x <= 0) return 0;
+    if (pos >= start + cost) return tiles;
+    return min(tiles, key_tiles_of(static_cast<int>(x)));
+  }
+  template <int SUBS>
+  __device__ __forceinline__ void measure(const PagedParams& p) {
+    const int keys = block_keys(p, s, p.sub_tokens * SUBS, i);
+    tiles = key_tiles_of(keys);
+    cost = kKeysPerItem + keys;
+  }
+};
+
+// Whole warp: the length of one of p.ctas equal ranges of the list, at least an
+// item's fixed cost and one tile, so that an item's inner ranges all have tiles;
+// and the length of the list.
+template <int SUBS>
+__device__ __forceinline__ long long paged_share(const PagedParams& p, long long* total) {
+  long long sum = 0;
+  for (int b = threadIdx.x & 31; b < p.B; b += 32) {
+    const PagedSeq s = paged_seq(p, b, p.sub_tokens * SUBS);
+    sum += cost_before<SUBS>(p, s, s.blocks);
+  }
+  sum = warp_sum(sum) * p.Hkv;
+  *total = sum;
+  // total / ctas rounded up (the 64-bit product is off by less than one), so that the ranges cover the list
+  const long long share = static_cast<long long>(static_cast<double>(sum) * p.inv_ctas) + 2;
+  return max(share, static_cast<long long>(p.min_tiles) * kKeysPerTile + kKeysPerItem);
+}
+
+// Whole warp: the item that position `pos` (below the list's length) lies in.
+template <int SUBS>
+__device__ __forceinline__ PagedPlace paged_find(const PagedParams& p, long long pos) {
+  const int lane = threadIdx.x & 31;
+  PagedPlace w = {};
+  long long before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const PagedSeq s = paged_seq(p, b0 + lane, p.sub_tokens * SUBS);
+    const long long per_head = cost_before<SUBS>(p, s, s.blocks);
+    const long long mine = per_head * p.Hkv, sum = warp_scan(mine) + before;
+    const unsigned here = __ballot_sync(0xffffffffu, pos >= sum - mine && pos < sum);
+    if (here == 0) {
+      before = __shfl_sync(0xffffffffu, sum, 31);
+      continue;
+    }
+    const int src = __ffs(here) - 1;
+    w.start = __shfl_sync(0xffffffffu, sum - mine, src);
+    const long long each = __shfl_sync(0xffffffffu, per_head, src);
+    w.b = b0 + src;
+    w.s = seq_from(s, src);
+    // heads and blocks that start at or before pos, 32 candidates at a time
+    for (int h0 = 0; h0 < p.Hkv; h0 += 32) {
+      const unsigned some =
+          __ballot_sync(0xffffffffu, h0 + lane < p.Hkv && w.start + (h0 + lane) * each <= pos);
+      if (some == 0) break;
+      w.head = h0 + 31 - __clz(some);
+    }
+    w.start += w.head * each;
+    int lo = 0, n = w.s.blocks;
+    while (n > 1) {
+      const int step = (n + 31) / 32;
+      const bool below =
+          lane * step < n && w.start + cost_before<SUBS>(p, w.s, lo + min(lane * step, n)) <= pos;
+      const int last = 31 - __clz(__ballot_sync(0xffffffffu, below));
+      n = min(step, n - last * step);
+      lo += last * step;
+    }
+    w.i = lo;
+    w.start += cost_before<SUBS>(p, w.s, lo);
+    w.measure<SUBS>(p);
+    return w;
+  }
+  return w;
+}
+
+__device__ __forceinline__ PagedUnit paged_unit(const PagedParams& p, const PagedSeq& s, int b, int head, int block,
+                                                int i) {
+  PagedUnit u;
+  u.valid = 1;
+  u.head = head;
+  u.q_len = s.q_len;
+  u.kv_len = s.kv_len;
+  u.tok0 = i * block;
+  u.ntok = min(block, s.q_len - u.tok0);
+  u.row0 = s.q0 + u.tok0;
+  u.table = b * p.table_stride;
+  u.t_begin = u.t_end = 0;
+  u.slot = -1;
+  return u;
+}
+
+// Whole warp: walks the segments of range `cta`.  A part that begins inside an
+// item goes to slot 2 cta, one that begins it and does not end it to slot 2 cta
+// + 1: a range has at most one of each.
+struct PagedWalk {
+  PagedPlace at;
+  long long lo, hi;   // the range
+  int cta;
+
+  template <int SUBS>
+  __device__ __forceinline__ PagedUnit next(const PagedParams& p) {
+    const int lane = threadIdx.x & 31;
+    PagedUnit u;
+    u.valid = 0;
+    while (lo < hi && !u.valid) {
+      const int from = at.tile(lo), to = at.tile(hi);
+      if (from < to) {
+        u = paged_unit(p, at.s, at.b, at.head, p.sub_tokens * SUBS, at.i);
+        u.t_begin = from;
+        u.t_end = to;
+        if (from > 0)
+          u.slot = 2 * cta;
+        else if (to < at.tiles)
+          u.slot = 2 * cta + 1;
+      }
+      at.start += at.cost;
+      lo = max(lo, at.start);
+      if (lo >= hi) break;
+      // the next block, head or sequence with new tokens
+      if (++at.i == at.s.blocks) {
+        at.i = 0;
+        if (++at.head == p.Hkv) {
+          at.head = 0;
+          int b0 = at.b + 1;
+          for (; b0 < p.B; b0 += 32) {
+            const PagedSeq s = paged_seq(p, b0 + lane, p.sub_tokens * SUBS);
+            const unsigned some = __ballot_sync(0xffffffffu, s.blocks > 0);
+            if (some != 0) {
+              const int src = __ffs(some) - 1;
+              at.s = seq_from(s, src);
+              at.b = b0 + src;
+              break;
+            }
+          }
+          if (b0 >= p.B) {
+            lo = hi;
+            break;
+          }
+        }
+      }
+      at.measure<SUBS>(p);
+    }
+    return u;
+  }
+};
+
+template <int SUBS>
+__device__ __forceinline__ PagedWalk paged_walk(const PagedParams& p, int cta) {
+  PagedWalk w;
+  long long total;
+  const long long share = paged_share<SUBS>(p, &total);
+  w.cta = cta;
+  w.lo = cta * share;
+  w.hi = cta < p.ctas ? min(w.lo + share, total) : w.lo;
+  if (w.lo < w.hi) w.at = paged_find<SUBS>(p, w.lo);
+  return w;
+}
+
+// Parts of an item that the merge reads: the first in slot `first`, the others
+// in `rest`, `rest` + step, ...
+struct PagedParts {
+  PagedUnit u;
+  int parts, first, rest, step;
+};
+
+// Whole warp: the item that the boundary between the ranges `index` and `index`
+// + 1 cuts, when it is the first boundary to do so; otherwise u.valid = 0.
+template <int SUBS>
+__device__ __forceinline__ PagedParts paged_parts_even(const PagedParams& p, int index) {
+  PagedParts r;
+  r.u.valid = 0;
+  long long total;
+  const long long share = paged_share<SUBS>(p, &total);
+  const long long pos = (index + 1ll) * share;
+  if (index + 1 >= p.ctas || pos >= total) return r;
+  const PagedPlace w = paged_find<SUBS>(p, pos);
+  const int t = w.tile(pos);
+  if (t == 0 || t == w.tiles || w.tile(pos - share) > 0) return r;
+  r.u = paged_unit(p, w.s, w.b, w.head, p.sub_tokens * SUBS, w.i);
+  r.first = 2 * index + 1;
+  r.rest = 2 * (index + 1);
+  r.step = 2;
+  r.parts = 2;
+  for (long long next = pos + share; next < total && w.tile(next) < w.tiles; next += share) ++r.parts;
+  return r;
+}
+
 // Bytes of one head's K and V that a group of heads may hold in L2 together.
 constexpr long long kPagedL2Bytes = 64ll << 20;
 
-// Whole warp: unit `index` (items = false), or the item of rank `index` among
-// those cut into several units (items = true; split 0 of it is returned).
+// Whole warp, one item per CTA: unit `index` (items = false), or the item of
+// rank `index` among those cut into several units (items = true; its parts are
+// in slots first, first + 1, ...).
 template <int SUBS>
-__device__ __forceinline__ PagedUnit paged_locate(const PagedParams& p, int index, bool items, int D) {
+__device__ __forceinline__ PagedParts paged_item(const PagedParams& p, int index, bool items, int D) {
   const int lane = threadIdx.x & 31;
   const int block = p.sub_tokens * SUBS;
-  auto lengths = [&](int b, int& q0, int& nq, int& tiles, int& q_len, int& kv_len) {
-    q0 = 0;
-    q_len = kv_len = 0;
-    if (b < p.B) {
-      const int begin = p.cu_q ? p.cu_q[b] : b;
-      const int end = p.cu_q ? p.cu_q[b + 1] : b + 1;
-      const int kv = p.kv_lens[b];
-      q0 = min(max(begin, 0), p.T);
-      q_len = max(0, min(end, p.T) - q0);
-      kv_len = min(max(kv, 0), p.max_len);
-      if (blockIdx.x == 0 && (begin < 0 || end < begin || end > p.T || kv < 0 || kv > p.max_len))
-        atomicOr(p.status, kDevErrPage);
-    }
-    nq = (q_len + block - 1) / block;
-    tiles = (kv_len + kKeysPerTile - 1) / kKeysPerTile;
-  };
-  int q0, nq, tiles, q_len, kv_len;
   long long total = 0;
   for (int b = lane; b < p.B; b += 32) {
-    lengths(b, q0, nq, tiles, q_len, kv_len);
-    total += static_cast<long long>(nq) * tiles;
+    const PagedSeq s = paged_seq(p, b, block);
+    total += static_cast<long long>(s.blocks) * key_tiles_of(s.kv_len);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  total *= p.Hkv;
-  const long long want = (total + p.target_units - 1) / p.target_units;
-  const int per_unit = static_cast<int>(max(want, static_cast<long long>(p.min_tiles)));
+  total = warp_sum(total) * p.Hkv;
+  const int per_unit =
+      static_cast<int>(max((total + p.ctas - 1) / p.ctas, static_cast<long long>(p.min_tiles)));
 
-  PagedUnit u;
-  u.valid = 0;
+  PagedParts r;
+  r.u.valid = 0;
+  r.step = 1;
   int before = 0, slots_before = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    lengths(b0 + lane, q0, nq, tiles, q_len, kv_len);
+    const PagedSeq q = paged_seq(p, b0 + lane, block);
+    const int tiles = key_tiles_of(q.kv_len);
     const int s = max(1, (tiles + per_unit - 1) / per_unit);
-    const int blocks = nq * p.Hkv;
+    const int blocks = q.blocks * p.Hkv;
     const int slots = s > 1 ? blocks * s : 0;
     const int count = items ? (s > 1 ? blocks : 0) : blocks * s;
-    int sum = count, slot_sum = slots;   // inclusive scans
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, sum, o);
-      const int c = __shfl_up_sync(0xffffffffu, slot_sum, o);
-      if (lane >= o) {
-        sum += a;
-        slot_sum += c;
-      }
-    }
+    const int sum = static_cast<int>(warp_scan(count)), slot_sum = static_cast<int>(warp_scan(slots));
     const int at = index - before;
     const unsigned here = __ballot_sync(0xffffffffu, at >= sum - count && at < sum);
     if (here != 0) {
       const int src = __ffs(here) - 1;
       auto get = [&](int v) { return __shfl_sync(0xffffffffu, v, src); };
-      const int splits = get(s), n_blocks = get(nq), all_tiles = get(tiles);
+      const int splits = get(s), all_tiles = get(tiles);
+      const PagedSeq seq = seq_from(q, src);
       int in = at - get(sum - count);
       if (items) in *= splits;
-      const int slot0 = slots_before + get(slot_sum - slots);
-      u.valid = 1;
-      u.b = b0 + src;
-      u.q_len = get(q_len);
-      u.kv_len = get(kv_len);
-      u.splits = splits;
-      u.slot = slot0 + in;
+      const int slot = slots_before + get(slot_sum - slots) + in;
       // Units of a sequence: groups of heads whose K and V fit in L2 together;
       // within a group the last query blocks (the longest under the causal
       // mask) first, all heads of the group for one block, then the next.
-      const long long kv_bytes = static_cast<long long>(max(u.kv_len, 1)) * D * 4;
+      const long long kv_bytes = static_cast<long long>(max(seq.kv_len, 1)) * D * 4;
       const int hg = static_cast<int>(min(max(kPagedL2Bytes / kv_bytes, 1ll), static_cast<long long>(p.Hkv)));
-      const int per_group = hg * n_blocks * splits;
+      const int per_group = hg * seq.blocks * splits;
       const int group = in / per_group;
       in -= group * per_group;
       const int per_block = min(hg, p.Hkv - group * hg) * splits;
       const int rank = in / per_block;
       in -= rank * per_block;
-      const int h = in / splits;
-      u.split = in - h * splits;
-      u.head = group * hg + h;
-      u.tok0 = (n_blocks - 1 - rank) * block;
-      u.ntok = min(block, u.q_len - u.tok0);
-      u.row0 = get(q0) + u.tok0;
-      u.t_begin = u.split * per_unit;
-      u.t_end = min(all_tiles, u.t_begin + per_unit);
-      return u;
+      const int h = in / splits, split = in - h * splits;
+      r.u = paged_unit(p, seq, b0 + src, group * hg + h, block, seq.blocks - 1 - rank);
+      r.u.t_begin = split * per_unit;
+      r.u.t_end = min(all_tiles, r.u.t_begin + per_unit);
+      if (splits > 1) r.u.slot = slot;
+      r.parts = splits;
+      r.first = slot;
+      r.rest = slot + 1;
+      return r;
     }
     before += __shfl_sync(0xffffffffu, sum, 31);
     slots_before += __shfl_sync(0xffffffffu, slot_sum, 31);
   }
-  return u;
+  return r;
 }
+
+// Named barrier of the segments (kBarP0 and kBarP1 are the dense kernel's).
+constexpr int kBarSegment = 3;
+constexpr int kBarShares = 4;   // the softmax warps, while they merge their shares
+
+template <int D, int SUBS>
+struct PagedConfig : FwdConfig<D, SUBS> {
+  using Base = FwdConfig<D, SUBS>;
+  // Epilogue staging: 64 bytes of each of a warp's 32 rows (Q's buffer already
+  // takes the next segment's queries by then).
+  static constexpr uint32_t kStageBytes = 32 * 64;
+  static constexpr uint32_t kSmemStage = Base::kSmemData;
+  static constexpr uint32_t kSmemBars = Base::kSmemData + 4 * SUBS * kStageBytes;
+  static constexpr uint32_t kSmemBytes = kSmemBars + 1024 /*align*/ + 2048 /*barriers, shares*/;
+  static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+  static_assert(SUBS == 2 || D == 256 || 2 * (kSmemBytes + 1024) <= 233472, "two CTAs per SM");
+  // Registers per thread after the start: the producer warp walks the schedule
+  // in 64 bits and needs more than the dense kernel's.
+  static constexpr int kSoftmax = SUBS == 2 ? 216 : 184;
+  static constexpr int kProducer = 72;
+  static_assert(SUBS * 128 * kSoftmax + 128 * kProducer <= FwdShape<SUBS>::kLaunch * FwdShape<SUBS>::kThreads,
+                "register rebalancing exceeds the launch allocation");
+  // every role: softmax, producer and MMA warps, and the watcher where there is one
+  static constexpr int kSegmentThreads = SUBS * 128 + 64 + (Base::kNamedP ? 32 : 0);
+};
 
 template <int STAGES>
 struct alignas(8) PagedShared {
   FwdBarriers<STAGES> bars;
-  PagedUnit unit;
+  uint64_t q_empty;
+  PagedUnit unit[2];   // segment k in unit[k % 2]
+  float2 shares[4][32];   // NARROW: (m, l) of the warps' rows
 };
 
 // F16: Q, K, V (and P) are fp16 instead of bf16.  SUBS: sub-tiles per CTA, as
 // in the dense kernel (2: one CTA per SM, for blocks of more than 128 rows).
-template <int D, bool F16, int SUBS>
+//
+// Counters that run on over a CTA's segments: `base` K/V copies (two per key
+// tile, in order K, V), `done[sub]` tiles of a sub-tile, `loads` segments that
+// loaded Q.  A barrier's phase is taken from them.
+template <int D, bool F16, int SUBS, bool NARROW>
 __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCtasPerSm)
     fa2_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                        const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
-  using Cfg = FwdConfig<D, SUBS>;
-  using Shape = FwdShape<SUBS>;
+                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedParams p) {
+  using Cfg = PagedConfig<D, SUBS>;
   constexpr int kWarpProducer = 4 * SUBS;      // schedule and TMA warp
   constexpr int kWarpMma = 4 * SUBS + 1;       // MMA warp, owns the TMEM allocation
+  constexpr int kWarpWatch = 4 * SUBS + 2;     // K/V watcher (named-barrier variants)
   constexpr int STAGES = Cfg::kStages;
   constexpr uint32_t TILE = Cfg::kTileBytes;
   constexpr int NCH = Cfg::kChunks;
   constexpr uint32_t kChunkBytes = kRowsPerSub * 128;  // one 64-column chunk of a 128-row tile
-  static_assert(sizeof(PagedShared<STAGES>) <= 1024, "barrier page");
+  static_assert(sizeof(PagedShared<STAGES>) <= 2048, "barrier page");
+  static_assert(!NARROW || SUBS == 1, "narrow blocks have one sub-tile");
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sQ = smem;                  // SUBS sub-tiles
   uint8_t* sKV = smem + SUBS * TILE;   // STAGES tiles
-  auto* shared = reinterpret_cast<PagedShared<STAGES>*>(smem + Cfg::kSmemData);
+  auto* shared = reinterpret_cast<PagedShared<STAGES>*>(smem + Cfg::kSmemBars);
   auto* bars = &shared->bars;
   volatile int* abort = &bars->abort;
 
@@ -223,97 +520,27 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
     if (first >= w.ntok) return 0;
     const int last = min(first + p.sub_tokens, w.ntok) - 1;
     const int kept = paged_kept(p.causal, w.kv_len, w.q_len, w.tok0 + last);
-    return max(0, min(w.t_end, (kept + kKeysPerTile - 1) / kKeysPerTile) - w.t_begin);
+    return max(0, min(w.t_end, key_tiles_of(kept)) - w.t_begin);
   };
 
-  // State of the producer warp: table entries [chunk0, chunk0 + 32) of the
-  // sequence in `pages`, the next 32 in `pages_next`, one per lane.
-  const int slots_log2 = min(p.page_log2, 7);           // slots of a page that one tile reads
-  const int tile_pages = kKeysPerTile >> slots_log2;    // pages (boxes per 64 columns) of a tile
-  int pages = 0, pages_next = 0, chunk0 = 0;
-  const int* table = nullptr;
-  int live_pages = 0;                                   // table entries that hold keys
-  auto fetch = [&](int first) {
-    const int i = first + lane;
-    int id = 0;
-    if (i < live_pages) {
-      id = table[i];
-      if (id < 0 || id >= p.num_pages) atomicOr(p.status, kDevErrPage);
+  if (warp == kWarpProducer && lane == 0) {
+    bar_init(&bars->q_full, 1);
+    bar_init(&shared->q_empty, 1);
+    for (int s = 0; s < STAGES; ++s) {
+      bar_init(&bars->kv_full[s], 1);
+      bar_init(&bars->kv_empty[s], 1);
     }
-    return id;
-  };
-  // whole warp: K (kind 0) or V (kind 1) tile `tile` into ring slot `slot`
-  auto load_tile = [&](const PagedUnit& w, int tile, int kind, int slot) {
-    const int first = (tile << 7) >> p.page_log2;       // table entry of the tile's first page
-    if (first >= chunk0 + 32) {
-      chunk0 += 32;
-      pages = pages_next;
-      pages_next = fetch(chunk0 + 32);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&bars->s_full[i], 1);
+      bar_init(&bars->p_ready[i], kRowsPerSub);
+      bar_init(&bars->o_done[i], 1);
     }
-    const int n = min(tile_pages, live_pages - first);
-    const int id = __shfl_sync(0xffffffffu, pages, (first - chunk0 + lane) & 31);
-    if (lane == 0) bar_arrive_expect_tx(&bars->kv_full[slot], static_cast<uint32_t>(n) * NCH * (128u << slots_log2));
-    __syncwarp();
-    if (lane < n) {
-      const CUtensorMap* map = kind == 0 ? &tm_k : &tm_v;
-      const int row = p.page_log2 > 7 ? (tile << 7) & ((1 << p.page_log2) - 1) : 0;
-      uint8_t* dst = sKV + slot * TILE + (static_cast<uint32_t>(lane) << slots_log2) * 128;
-#pragma unroll
-      for (int c = 0; c < NCH; ++c)
-        tma_load_4d(dst + c * kChunkBytes, map, &bars->kv_full[slot], c * 64, row, w.head, id);
-    }
-    __syncwarp();
-  };
-
-  if (warp == kWarpProducer) {
-    if (lane == 0) {
-      bar_init(&bars->q_full, 1);
-      for (int s = 0; s < STAGES; ++s) {
-        bar_init(&bars->kv_full[s], 1);
-        bar_init(&bars->kv_empty[s], 1);
-      }
-      for (int i = 0; i < 2; ++i) {
-        bar_init(&bars->s_full[i], 1);
-        bar_init(&bars->p_ready[i], kRowsPerSub);
-        bar_init(&bars->o_done[i], 1);
-      }
-      bar_init(&bars->mma_drain, 1);
-      bars->abort = 0;
-      fence_barrier_init();
-      prefetch_tmap(&tm_q);
-      prefetch_tmap(&tm_k);
-      prefetch_tmap(&tm_v);
-    }
-    const PagedUnit w = paged_locate<SUBS>(p, static_cast<int>(blockIdx.x), false, D);
-    if (lane == 0) shared->unit = w;
-    __syncwarp();
-    if (w.valid) {
-      const int n0 = tiles_for(w, 0), n1 = SUBS == 2 ? tiles_for(w, 1) : 0;
-      const int nmax = max(n0, n1);
-      if (nmax > 0) {
-        table = p.page_table + static_cast<long long>(w.b) * p.table_stride;
-        live_pages = (w.kv_len + (1 << p.page_log2) - 1) >> p.page_log2;
-        chunk0 = (w.t_begin << 7) >> p.page_log2;
-        pages = fetch(chunk0);
-        pages_next = fetch(chunk0 + 32);
-        // Q boxes of the live tokens: lane i loads box i of each sub-tile
-        const uint32_t box_bytes = static_cast<uint32_t>(p.box_tokens) * p.G * 128;
-        const int per_sub = p.sub_tokens / p.box_tokens;
-        const int boxes = (w.ntok + p.box_tokens - 1) / p.box_tokens;
-        if (lane == 0) bar_arrive_expect_tx(&bars->q_full, static_cast<uint32_t>(boxes) * NCH * box_bytes);
-        __syncwarp();
-        for (int i = lane; i < boxes; i += 32) {
-          const int sub = i / per_sub;
-          uint8_t* dst = sQ + sub * TILE + (i - sub * per_sub) * box_bytes;
-          for (int c = 0; c < NCH; ++c)
-            tma_load_3d(dst + c * kChunkBytes, &tm_q, &bars->q_full, c * 64, w.head * p.G,
-                        w.row0 + i * p.box_tokens);
-        }
-        __syncwarp();
-        const int primed = min(STAGES, 2 * nmax);
-        for (int g = 0; g < primed; ++g) load_tile(w, w.t_begin + g / 2, g & 1, g);
-      }
-    }
+    bar_init(&bars->mma_drain, 1);
+    bars->abort = 0;
+    fence_barrier_init();
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
   }
   if (warp == kWarpMma) {
     tmem_alloc(&bars->tmem_base, Cfg::kTmemCols);
@@ -323,49 +550,156 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = bars->tmem_base;
-  const PagedUnit w = shared->unit;
-  const int n0 = w.valid ? tiles_for(w, 0) : 0;
-  const int n1 = w.valid && SUBS == 2 ? tiles_for(w, 1) : 0;
-  const int nmax = max(n0, n1);
+
+  // the merge may start (it finds its items and then waits for this grid to end)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp >= kWarpProducer) {
-    regs_decrease<Shape::kProducer>();
+    regs_decrease<Cfg::kProducer>();
     if (warp == kWarpProducer) {
-      // ------------------------------------------------------------ TMA producer
-      int issued = min(STAGES, 2 * nmax);
+      // ------------------------------------------------------------ schedule and TMA producer
+      const int slots_log2 = min(p.page_log2, 7);           // slots of a page that one tile reads
+      const int tile_pages = kKeysPerTile >> slots_log2;    // pages (boxes per 64 columns) of a tile
+      PagedWalk walk;
+      PagedUnit w;
+      if (p.even) {
+        walk = paged_walk<SUBS>(p, static_cast<int>(blockIdx.x));
+        w = walk.next<SUBS>(p);
+      } else {
+        w = paged_item<SUBS>(p, static_cast<int>(blockIdx.x), false, D).u;
+      }
+      int issued = 0, loads = 0;
       bool ok = true;
-      for (; issued < 2 * nmax && ok; ++issued) {
-        const int slot = issued % STAGES;
-        const int lap = issued / STAGES;
-        if (lane == 0) ok = wait_bar(&bars->kv_empty[slot], (lap - 1) & 1, abort, p.timeout_ns);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) {
-          if (lane == 0) raise_abort(abort, p.status);
-          break;
+      for (int k = 0;; ++k) {
+        if (lane == 0) shared->unit[k & 1] = w;
+        __syncwarp();
+        int n = 0;
+        if (w.valid) {
+          n = tiles_for(w, 0);
+          if (SUBS == 2) n = max(n, tiles_for(w, 1));
         }
-        load_tile(w, w.t_begin + issued / 2, issued & 1, slot);
+        // table entries [chunk0, chunk0 + 32) of the sequence in `pages`, the next 32 in `pages_next`
+        const int* table = p.page_table + (n > 0 ? w.table : 0);
+        const int live_pages = n > 0 ? (w.kv_len + (1 << p.page_log2) - 1) >> p.page_log2 : 0;
+        int chunk0 = n > 0 ? (w.t_begin << 7) >> p.page_log2 : 0;
+        auto fetch = [&](int first) {
+          const int i = first + lane;
+          int id = 0;
+          if (i < live_pages) {
+            id = table[i];
+            if (id < 0 || id >= p.num_pages) atomicOr(p.status, kDevErrPage);
+          }
+          return id;
+        };
+        int pages = fetch(chunk0), pages_next = fetch(chunk0 + 32);
+        // copy i of this segment: K (even i) or V of tile i / 2
+        auto load = [&](int i) {
+          const int slot = issued % STAGES, lap = issued / STAGES;
+          if (ok && lap > 0) {
+            if (lane == 0) {
+              ok = wait_bar(&bars->kv_empty[slot], (lap - 1) & 1, abort, p.timeout_ns);
+              if (!ok) raise_abort(abort, p.status);
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+          }
+          if (!ok) return;
+          const int tile = w.t_begin + (i >> 1);
+          const int first = (tile << 7) >> p.page_log2;       // table entry of the tile's first page
+          if (first >= chunk0 + 32) {
+            chunk0 += 32;
+            pages = pages_next;
+            pages_next = fetch(chunk0 + 32);
+          }
+          const int count = min(tile_pages, live_pages - first);
+          const int id = __shfl_sync(0xffffffffu, pages, (first - chunk0 + lane) & 31);
+          if (lane == 0)
+            bar_arrive_expect_tx(&bars->kv_full[slot], static_cast<uint32_t>(count) * NCH * (128u << slots_log2));
+          __syncwarp();
+          if (lane < count) {
+            const CUtensorMap* map = (i & 1) == 0 ? &tm_k : &tm_v;
+            const int row = p.page_log2 > 7 ? (tile << 7) & ((1 << p.page_log2) - 1) : 0;
+            uint8_t* dst = sKV + slot * TILE + (static_cast<uint32_t>(lane) << slots_log2) * 128;
+#pragma unroll
+            for (int c = 0; c < NCH; ++c)
+              tma_load_4d(dst + c * kChunkBytes, map, &bars->kv_full[slot], c * 64, row, w.head, id);
+          }
+          __syncwarp();
+          ++issued;
+        };
+        // Ahead of the hand-over: the first copies, which do not wait for the
+        // last V of the segment before (its slot comes STAGES - 1 copies
+        // later), and Q, once the last S of the segment before is complete.
+        const int early = min(STAGES - 1, 2 * n);
+        for (int i = 0; i < early; ++i) {
+          load(i);
+          if (i == 0 && ok) {
+            if (loads > 0) {
+              if (lane == 0) {
+                ok = wait_bar(&shared->q_empty, (loads - 1) & 1, abort, p.timeout_ns);
+                if (!ok) raise_abort(abort, p.status);
+              }
+              ok = __shfl_sync(0xffffffffu, ok, 0);
+            }
+            if (ok) {
+              // Q boxes of the live tokens, a box per lane
+              const uint32_t box_bytes = static_cast<uint32_t>(p.box_tokens) * p.G * 128;
+              const int per_sub = p.sub_tokens / p.box_tokens;
+              const int boxes = (w.ntok + p.box_tokens - 1) / p.box_tokens;
+              constexpr int kCopies = NARROW ? 4 : 1;   // one in each warp's rows
+              if (lane == 0)
+                bar_arrive_expect_tx(&bars->q_full, static_cast<uint32_t>(boxes) * kCopies * NCH * box_bytes);
+              __syncwarp();
+              for (int y = lane; y < boxes * kCopies; y += 32) {
+                const int x = y / kCopies, copy = y % kCopies;
+                const int sub = x / per_sub;
+                uint8_t* dst = sQ + sub * TILE + (x - sub * per_sub) * box_bytes + copy * (32 * 128);
+                for (int c = 0; c < NCH; ++c)
+                  tma_load_3d(dst + c * kChunkBytes, &tm_q, &bars->q_full, c * 64, w.head * p.G,
+                              w.row0 + x * p.box_tokens);
+              }
+              __syncwarp();
+              ++loads;
+            }
+          }
+        }
+        named_sync(kBarSegment, Cfg::kSegmentThreads);
+        if (!w.valid) break;
+        for (int i = early; i < 2 * n; ++i) load(i);
+        if (p.even)
+          w = walk.next<SUBS>(p);
+        else
+          w.valid = 0;
       }
       // Before the CTA may exit, every copy it started must have landed.
-      if (lane == 0 && nmax > 0) {
+      if (lane == 0) {
         volatile int never = 0;
-        wait_bar(&bars->q_full, 0, &never, p.timeout_ns);
-        for (int k = max(0, issued - STAGES); k < issued; ++k)
-          wait_bar(&bars->kv_full[k % STAGES], (k / STAGES) & 1, &never, p.timeout_ns);
+        if (loads > 0) wait_bar(&bars->q_full, (loads - 1) & 1, &never, p.timeout_ns);
+        for (int i = max(0, issued - STAGES); i < issued; ++i)
+          wait_bar(&bars->kv_full[i % STAGES], (i / STAGES) & 1, &never, p.timeout_ns);
       }
       __syncwarp();
-    } else if (warp == kWarpMma + 1 && Cfg::kNamedP) {
+    } else if (warp == kWarpWatch && Cfg::kNamedP) {
       // ------------------------------------------------------------ K/V watcher
+      // After an abort the waits are skipped, not the phases.
       bool ok = true;
-      for (int j = 0; j < nmax; ++j) {
-        if (lane == 0 && ok) {
-          const int iv = 2 * j + 1, ik = 2 * j + 2;
-          ok = wait_bar(&bars->kv_full[iv % STAGES], (iv / STAGES) & 1, abort, p.timeout_ns);
-          if (ok && j + 1 < nmax)
-            ok = wait_bar(&bars->kv_full[ik % STAGES], (ik / STAGES) & 1, abort, p.timeout_ns);
-          if (!ok) raise_abort(abort, p.status);
+      int base = 0;
+      for (int k = 0;; ++k) {
+        named_sync(kBarSegment, Cfg::kSegmentThreads);
+        const PagedUnit& w = shared->unit[k & 1];
+        if (!w.valid) break;
+        const int n0 = tiles_for(w, 0), nmax = SUBS == 2 ? max(n0, tiles_for(w, 1)) : n0;
+        for (int j = 0; j < nmax; ++j) {
+          if (lane == 0 && ok) {
+            const int iv = base + 2 * j + 1, ik = iv + 1;
+            ok = wait_bar(&bars->kv_full[iv % STAGES], (iv / STAGES) & 1, abort, p.timeout_ns);
+            if (ok && j + 1 < nmax)
+              ok = wait_bar(&bars->kv_full[ik % STAGES], (ik / STAGES) & 1, abort, p.timeout_ns);
+            if (!ok) raise_abort(abort, p.status);
+          }
+          __syncwarp();
+          named_sync(kBarP0, j < n0 ? kBarP0Count : kBarP0Idle);
         }
-        __syncwarp();
-        named_sync(kBarP0, j < n0 ? kBarP0Count : kBarP0Idle);
+        base += 2 * nmax;
       }
     } else if (warp == kWarpMma) {
       // ------------------------------------------------------------ MMA issuer
@@ -403,90 +737,107 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
         }
       };
       bool ok = true;
-      if (lane == 0 && nmax > 0) {
-        ok = wait_bar(&bars->q_full, 0, abort, p.timeout_ns) &&
-             wait_bar(&bars->kv_full[0], 0, abort, p.timeout_ns);
-        if (!ok) raise_abort(abort, p.status);
-        tc_fence_after_sync();
-        if (ok || Cfg::kNamedP) {
-          if (n0 > 0) { issue_s(0, 0, 0); mma_commit(&bars->s_full[0]); }
-          if (n1 > 0) { issue_s(1, 0, 1); mma_commit(&bars->s_full[1]); }
-          if (!Cfg::kSoftmaxRelease) mma_commit(&bars->kv_empty[0]);
+      int base = 0, done0 = 0, loads = 0;
+      for (int k = 0;; ++k) {
+        named_sync(kBarSegment, Cfg::kSegmentThreads);
+        const PagedUnit& w = shared->unit[k & 1];
+        if (!w.valid) break;
+        const int n0 = tiles_for(w, 0), n1 = SUBS == 2 ? tiles_for(w, 1) : 0, nmax = max(n0, n1);
+        if (nmax == 0) continue;
+        if (lane == 0 && ok) {
+          ok = wait_bar(&bars->q_full, loads & 1, abort, p.timeout_ns) &&
+               wait_bar(&bars->kv_full[base % STAGES], (base / STAGES) & 1, abort, p.timeout_ns);
+          if (!ok) raise_abort(abort, p.status);
         }
-      }
-      __syncwarp();
-      if constexpr (Cfg::kNamedP) {
-        // named barriers: every phase is passed, also after an abort
-        for (int j = 0; j < nmax; ++j) {
-          const int slot_v = (2 * j + 1) % STAGES, slot_k = (2 * j + 2) % STAGES;
-          named_sync(kBarP0, j < n0 ? kBarP0Count : kBarP0Idle);
-          if (lane == 0) {
-            tc_fence_after_sync();
-            if (j < n0) {
-              issue_pv(0, slot_v, j > 0, 0);
-              if (j + 1 == n0) mma_commit(&bars->o_done[0]);
-            }
-            if (j + 1 < n0) { issue_s(0, slot_k, 0); mma_commit(&bars->s_full[0]); }
+        ++loads;
+        if (lane == 0 && (ok || Cfg::kNamedP)) {
+          tc_fence_after_sync();
+          if (n0 > 0) {
+            const int buf = Cfg::kDoubleS ? done0 & 1 : 0;
+            issue_s(0, base % STAGES, buf);
+            mma_commit(&bars->s_full[buf]);
           }
-          __syncwarp();
-          if (j < n1) {
-            named_sync(kBarP1, kBarP1Count);
+          if (n1 > 0) { issue_s(1, base % STAGES, 1); mma_commit(&bars->s_full[1]); }
+          if (!Cfg::kSoftmaxRelease) mma_commit(&bars->kv_empty[base % STAGES]);
+          if (nmax == 1) mma_commit(&shared->q_empty);
+        }
+        __syncwarp();
+        if constexpr (Cfg::kNamedP) {
+          // Named barriers: every phase is passed, also after an abort (the
+          // MMAs then still go out, on whatever the buffers hold).
+          for (int j = 0; j < nmax; ++j) {
+            const int slot_v = (base + 2 * j + 1) % STAGES, slot_k = (base + 2 * j + 2) % STAGES;
+            named_sync(kBarP0, j < n0 ? kBarP0Count : kBarP0Idle);   // P_0(j); V_j, K_(j+1) landed
             if (lane == 0) {
               tc_fence_after_sync();
-              issue_pv(1, slot_v, j > 0, 1);
-              if (j + 1 == n1) mma_commit(&bars->o_done[1]);
-              if (j + 1 < n1) { issue_s(1, slot_k, 1); mma_commit(&bars->s_full[1]); }
+              if (j < n0) {
+                issue_pv(0, slot_v, j > 0, 0);
+                if (j + 1 == n0) mma_commit(&bars->o_done[0]);
+              }
+              if (j + 1 < n0) { issue_s(0, slot_k, 0); mma_commit(&bars->s_full[0]); }
             }
             __syncwarp();
-          }
-        }
-      } else if (lane == 0 && nmax > 0) {
-        if constexpr (Cfg::kDoubleS) {
-          for (int j = 0; j < n0 && ok; ++j) {
-            const int iv = 2 * j + 1, ik = 2 * j + 2;
-            const int slot_v = iv % STAGES, slot_k = ik % STAGES;
-            if (j + 1 < n0) {
-              if (!wait_bar(&bars->kv_full[slot_k], (ik / STAGES) & 1, abort, p.timeout_ns)) { ok = false; break; }
-              tc_fence_after_sync();
-              issue_s(0, slot_k, (j + 1) & 1);
-              mma_commit(&bars->s_full[(j + 1) & 1]);
-              mma_commit(&bars->kv_empty[slot_k]);
+            if (j < n1) {
+              named_sync(kBarP1, kBarP1Count);                      // P_1(j)
+              if (lane == 0) {
+                tc_fence_after_sync();
+                issue_pv(1, slot_v, j > 0, 1);
+                if (j + 1 == n1) mma_commit(&bars->o_done[1]);
+                if (j + 1 < n1) { issue_s(1, slot_k, 1); mma_commit(&bars->s_full[1]); }
+              }
             }
-            uint64_t* bv = &bars->kv_full[slot_v];
-            const uint32_t pv = (iv / STAGES) & 1;
-            if (!wait_bar3(bv, pv, &bars->p_ready[j & 1], (j >> 1) & 1, bv, pv, abort, p.timeout_ns)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after_sync();
-            issue_pv(0, slot_v, j > 0, j & 1);
-            mma_commit(&bars->o_done[0]);
-            mma_commit(&bars->kv_empty[slot_v]);
+            if (lane == 0 && j + 2 == nmax) mma_commit(&shared->q_empty);   // after the last S
+            __syncwarp();
           }
-        } else {
-          static_assert(Cfg::kNamedP || Cfg::kDoubleS || SUBS == 1, "polled order: one sub-tile");
-          for (int j = 0; j < n0 && ok; ++j) {
-            const int iv = 2 * j + 1, ik = 2 * j + 2;
+        } else if (lane == 0 && ok) {
+          static_assert(Cfg::kNamedP || SUBS == 1, "polled order: one sub-tile");
+          for (int j = 0; j < n0; ++j) {
+            const int g = done0 + j;   // tile count over all segments
+            const int iv = base + 2 * j + 1, ik = iv + 1;
             const int slot_v = iv % STAGES, slot_k = ik % STAGES;
             uint64_t* bv = &bars->kv_full[slot_v];
             const uint32_t pv = (iv / STAGES) & 1;
-            if (!wait_bar3(bv, pv, &bars->p_ready[0], j & 1, bv, pv, abort, p.timeout_ns)) { ok = false; break; }
-            tc_fence_after_sync();
-            issue_pv(0, slot_v, j > 0, 0);
-            if (j + 1 == n0) mma_commit(&bars->o_done[0]);
-            mma_commit(&bars->kv_empty[slot_v]);
-            if (j + 1 < n0) {
-              if (!wait_bar(&bars->kv_full[slot_k], (ik / STAGES) & 1, abort, p.timeout_ns)) { ok = false; break; }
+            if constexpr (Cfg::kDoubleS) {
+              // S(j+1) into the other buffer ahead of P(j) V
+              if (j + 1 < n0) {
+                if (!wait_bar(&bars->kv_full[slot_k], (ik / STAGES) & 1, abort, p.timeout_ns)) { ok = false; break; }
+                tc_fence_after_sync();
+                issue_s(0, slot_k, (g + 1) & 1);
+                mma_commit(&bars->s_full[(g + 1) & 1]);
+                mma_commit(&bars->kv_empty[slot_k]);
+                if (j + 2 == n0) mma_commit(&shared->q_empty);
+              }
+              if (!wait_bar3(bv, pv, &bars->p_ready[g & 1], (g >> 1) & 1, bv, pv, abort, p.timeout_ns)) {
+                ok = false;
+                break;
+              }
               tc_fence_after_sync();
-              issue_s(0, slot_k, 0);
-              mma_commit(&bars->s_full[0]);
-              mma_commit(&bars->kv_empty[slot_k]);
+              issue_pv(0, slot_v, j > 0, g & 1);
+              mma_commit(&bars->o_done[0]);
+              mma_commit(&bars->kv_empty[slot_v]);
+            } else {
+              if (!wait_bar3(bv, pv, &bars->p_ready[0], g & 1, bv, pv, abort, p.timeout_ns)) { ok = false; break; }
+              tc_fence_after_sync();
+              issue_pv(0, slot_v, j > 0, 0);
+              if (j + 1 == n0) mma_commit(&bars->o_done[0]);
+              mma_commit(&bars->kv_empty[slot_v]);
+              if (j + 1 < n0) {
+                if (!wait_bar(&bars->kv_full[slot_k], (ik / STAGES) & 1, abort, p.timeout_ns)) { ok = false; break; }
+                tc_fence_after_sync();
+                issue_s(0, slot_k, 0);
+                mma_commit(&bars->s_full[0]);
+                mma_commit(&bars->kv_empty[slot_k]);
+                if (j + 2 == n0) mma_commit(&shared->q_empty);
+              }
             }
           }
+          if (!ok) raise_abort(abort, p.status);
         }
-        if (!ok) raise_abort(abort, p.status);
+        __syncwarp();
+        base += 2 * nmax;
+        done0 += n0;
       }
-      if (lane == 0 && nmax > 0) {
+      if (lane == 0) {
         // Every MMA must be complete before TMEM is released.
         mma_commit(&bars->mma_drain);
         volatile int never = 0;
@@ -495,256 +846,372 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
       __syncwarp();
     }
   } else {
-    regs_increase<Shape::kSoftmax>();
+    regs_increase<Cfg::kSoftmax>();
     // ------------------------------------------------------------ softmax
     const int sub = warp >> 2;
-    const int n_tiles = sub == 0 ? n0 : n1;
     const int wq = warp & 3;
-    const int row = wq * 32 + lane;                       // TMEM lane = row of the sub-tile
-    const int sub_tok0 = w.valid ? sub * p.sub_tokens : 0;
-    const int rows = w.valid ? max(0, min(p.sub_tokens, w.ntok - sub_tok0)) * p.G : 0;   // live rows
-    const bool live = row < rows;
-    const bool warp_live = wq * 32 < rows;
+    // TMEM lane wq * 32 + lane is row `row` of the sub-tile
+    const int row = NARROW ? lane : wq * 32 + lane;
+    const int sub_tok0 = sub * p.sub_tokens;
     const int tok = row / p.G;                            // token of the sub-tile
-    const int lim = live ? paged_kept(p.causal, w.kv_len, w.q_len, w.tok0 + sub_tok0 + tok) : 0;
-    // every live row keeps at least the first token's keys
-    const int lim_min = w.valid ? paged_kept(p.causal, w.kv_len, w.q_len, w.tok0 + sub_tok0) : 0;
     const uint32_t lane_bits = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tS0 = tmem + lane_bits + sub * 128;
     const uint32_t tO = tmem + lane_bits + (sub == 0 ? Cfg::kColsO0 : Cfg::kColsO1);
     const float sl2 = p.scale_log2;
-
-    // One thread of the sub-tile that visits every key tile releases the ring slots.
-    const bool releaser = (threadIdx.x & (kRowsPerSub - 1)) == 0 && n_tiles == nmax &&
-                          (sub == SUBS - 1 || n1 == 0);
-    float m = -INFINITY;
-    float l = 0.f;
     bool ok = true;
-    int announced = 0;
-    for (int j = 0; j < n_tiles; ++j) {
-      uint64_t* sbar = &bars->s_full[Cfg::kDoubleS ? (j & 1) : sub];
-      const uint32_t s_phase = Cfg::kDoubleS ? (j >> 1) & 1 : j & 1;
-      const uint32_t tS = Cfg::kDoubleS ? tS0 + (j & 1) * 128 : tS0;
-      if (!__all_sync(0xffffffffu, wait_bar(sbar, s_phase, abort, p.timeout_ns))) {
-        ok = false;
-        break;
-      }
-      tc_fence_after_sync();
-      if (Cfg::kSoftmaxRelease && releaser) {
-        if (j > 0) bar_arrive(&bars->kv_empty[(2 * j - 1) % STAGES]);
-        bar_arrive(&bars->kv_empty[(2 * j) % STAGES]);
-      }
-      const int key0 = (w.t_begin + j) * kKeysPerTile;
-      // V rows behind the last key: zeros, written by the first sub-tile that reads them
-      if (key0 + kKeysPerTile > w.kv_len && (sub == 0 || j >= n0)) {
-        const int iv = 2 * j + 1;
-        if (!__all_sync(0xffffffffu, wait_bar(&bars->kv_full[iv % STAGES], (iv / STAGES) & 1, abort, p.timeout_ns))) {
+    int base = 0, done = 0, outs = 0;   // outs: segments in which this sub-tile had tiles
+    for (int k = 0;; ++k) {
+      named_sync(kBarSegment, Cfg::kSegmentThreads);
+      const PagedUnit& w = shared->unit[k & 1];
+      if (!w.valid) break;
+      const int n0 = tiles_for(w, 0), n1 = SUBS == 2 ? tiles_for(w, 1) : 0, nmax = max(n0, n1);
+      const int n_tiles = sub == 0 ? n0 : n1;
+      const int rows = max(0, min(p.sub_tokens, w.ntok - sub_tok0)) * p.G;   // live rows
+      const bool live = row < rows;
+      const bool warp_live = NARROW || wq * 32 < rows;
+      const int kv_len = w.kv_len, t_begin = w.t_begin;
+      const int lim = live ? paged_kept(p.causal, kv_len, w.q_len, w.tok0 + sub_tok0 + tok) : 0;
+      // every live row keeps at least the first token's keys
+      const int lim_min = paged_kept(p.causal, kv_len, w.q_len, w.tok0 + sub_tok0);
+
+      // One thread of the sub-tile that visits every key tile releases the ring slots.
+      const bool releaser = (threadIdx.x & (kRowsPerSub - 1)) == 0 && n_tiles == nmax && n_tiles > 0 &&
+                            (sub == SUBS - 1 || n1 == 0);
+      float m = -INFINITY;
+      float l = 0.f;
+      int announced = 0;
+      for (int j = 0; j < n_tiles && ok; ++j) {
+        const int g = done + j;
+        uint64_t* sbar = &bars->s_full[Cfg::kDoubleS ? (g & 1) : sub];
+        const uint32_t s_phase = Cfg::kDoubleS ? (g >> 1) & 1 : g & 1;
+        const uint32_t tS = Cfg::kDoubleS ? tS0 + (g & 1) * 128 : tS0;
+        if (!__all_sync(0xffffffffu, wait_bar(sbar, s_phase, abort, p.timeout_ns))) {
           ok = false;
           break;
         }
-        const uint32_t v_addr = smem_addr(sKV + (iv % STAGES) * TILE);
-        const uint32_t keep_bytes = static_cast<uint32_t>(w.kv_len - key0) * 128;
-#pragma unroll
-        for (int c = 0; c < NCH; ++c)
-          for (uint32_t at = keep_bytes + row * 16; at < kChunkBytes; at += kRowsPerSub * 16)
-            st_shared_v4(v_addr + c * kChunkBytes + at, 0u, 0u, 0u, 0u);
-        fence_proxy_async_shared();
-      }
-      if (warp_live) {
-        uint32_t s[4][32];
-        const bool masked = key0 + kKeysPerTile > lim_min;
-        auto load_s = [&]() {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, s[c]);
-          tmem_ld_wait(s[0]);
-#pragma unroll
-          for (int c = 1; c < 4; ++c) regs_after_wait(s[c]);
-          if (masked) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (key0 + c * 32 + e >= lim) s[c][e] = __float_as_uint(-INFINITY);
+        tc_fence_after_sync();
+        if (Cfg::kSoftmaxRelease && releaser) {
+          if (j > 0) bar_arrive(&bars->kv_empty[(base + 2 * j - 1) % STAGES]);
+          bar_arrive(&bars->kv_empty[(base + 2 * j) % STAGES]);
+        }
+        const int key0 = (t_begin + j) * kKeysPerTile;
+        // V rows behind the last key: zeros, written by the first sub-tile that reads them
+        if (key0 + kKeysPerTile > kv_len && (sub == 0 || j >= n0)) {
+          const int iv = base + 2 * j + 1;
+          if (!__all_sync(0xffffffffu, wait_bar(&bars->kv_full[iv % STAGES], (iv / STAGES) & 1, abort, p.timeout_ns))) {
+            ok = false;
+            break;
           }
-        };
-        // the row max, and the offset moved to it when it exceeds it by more than kRescaleLog2
-        float m_new = m;
-        float alpha = 1.f;
-        auto decide = [&]() {
+          const uint32_t v_addr = smem_addr(sKV + (iv % STAGES) * TILE);
+          const uint32_t keep_bytes = static_cast<uint32_t>(kv_len - key0) * 128;
+#pragma unroll
+          for (int c = 0; c < NCH; ++c)
+            for (uint32_t at = keep_bytes + (wq * 32 + lane) * 16; at < kChunkBytes; at += kRowsPerSub * 16)
+              st_shared_v4(v_addr + c * kChunkBytes + at, 0u, 0u, 0u, 0u);
+          fence_proxy_async_shared();
+        }
+        if (warp_live) {
+          constexpr int kChunks = NARROW ? 1 : 4;   // of 32 keys of the tile that this warp takes
+          const int first = key0 + (NARROW ? wq * 32 : 0);
+          const uint32_t tMine = tS + (NARROW ? wq * 32 : 0);
+          uint32_t s[kChunks][32];
+          const bool masked = key0 + kKeysPerTile > lim_min;
+          auto load_s = [&]() {
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) tmem_ld32(tMine + c * 32, s[c]);
+            tmem_ld_wait(s[0]);
+#pragma unroll
+            for (int c = 1; c < kChunks; ++c) regs_after_wait(s[c]);
+            if (masked) {
+#pragma unroll
+              for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (first + c * 32 + e >= lim) s[c][e] = __float_as_uint(-INFINITY);
+            }
+          };
+          // the row max, and the offset moved to it when it exceeds it by more than kRescaleLog2
+          float m_new = m;
+          float alpha = 1.f;
+          auto decide = [&]() {
 #define FA2_S(f) __uint_as_float(s[(f) >> 5][(f) & 31])
-          float mx8[8];
+            float mx8[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) mx8[k] = FA2_S(k);
+            for (int k = 0; k < 8; ++k) mx8[k] = FA2_S(k);
 #pragma unroll
-          for (int f = 8; f < 120; f += 16)
+            for (int f = 8; f < kChunks * 32 - 8; f += 16)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) mx8[k] = fmax3(mx8[k], FA2_S(f + k), FA2_S(f + 8 + k));
+              for (int k = 0; k < 8; ++k) mx8[k] = fmax3(mx8[k], FA2_S(f + k), FA2_S(f + 8 + k));
 #pragma unroll
-          for (int k = 0; k < 8; ++k) mx8[k] = fmaxf(mx8[k], FA2_S(120 + k));
+            for (int k = 0; k < 8; ++k) mx8[k] = fmaxf(mx8[k], FA2_S(kChunks * 32 - 8 + k));
 #undef FA2_S
-          const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
-                                 fmaxf(mx8[6], mx8[7]));
-          const float m_cand = fmaxf(m, mx * sl2);
-          const bool move = m == -INFINITY || m_cand > m + kRescaleLog2;
-          m_new = move ? m_cand : m;
-          alpha = !move ? 1.f : (m == -INFINITY ? 0.f : ex2_approx(m - m_new));
-        };
-        uint32_t pk[2][32];
-        float rs;
-        auto exps = [&]() {
-          const float off = m_new == -INFINITY ? 0.f : m_new;
-          const float2 c2 = make_float2(sl2, sl2);
-          const float2 o2 = make_float2(-off, -off);
-          float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                           make_float2(0.f, 0.f)};
+            const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
+                                   fmaxf(mx8[6], mx8[7]));
+            const float m_cand = fmaxf(m, mx * sl2);
+            const bool move = m == -INFINITY || m_cand > m + kRescaleLog2;
+            m_new = move ? m_cand : m;
+            alpha = !move ? 1.f : (m == -INFINITY ? 0.f : ex2_approx(m - m_new));
+          };
+          uint32_t pk[kChunks][16];
+          float rs;
+          auto exps = [&]() {
+            const float off = m_new == -INFINITY ? 0.f : m_new;
+            const float2 c2 = make_float2(sl2, sl2);
+            const float2 o2 = make_float2(-off, -off);
+            float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                             make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < kChunks; ++c) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 t = __ffma2_rn(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), c2, o2);
-              const float2 pe = make_float2(ex2_approx(t.x), ex2_approx(t.y));
-              acc[(e >> 1) & 3] = __fadd2_rn(acc[(e >> 1) & 3], pe);
-              pk[c >> 1][(c & 1) * 16 + (e >> 1)] = pack_x2<F16>(pe.x, pe.y);
+              for (int e = 0; e < 32; e += 2) {
+                const float2 t = __ffma2_rn(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), c2, o2);
+                const float2 pe = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+                acc[(e >> 1) & 3] = __fadd2_rn(acc[(e >> 1) & 3], pe);
+                pk[c][e >> 1] = pack_x2<F16>(pe.x, pe.y);
+              }
+            }
+            const float2 a01 = __fadd2_rn(acc[0], acc[1]);
+            const float2 a23 = __fadd2_rn(acc[2], acc[3]);
+            const float2 a = __fadd2_rn(a01, a23);
+            rs = a.x + a.y;
+          };
+          // Once the offset is finite the exponentials come first, with the
+          // offset as it stands (see the dense kernel); one loop, so that the
+          // code, which every cold launch has to fetch, is there once.
+          bool decided = __any_sync(0xffffffffu, live && m == -INFINITY);   // take the row max first
+          for (;;) {
+            load_s();
+            if (decided) decide();
+            exps();
+            if (decided || !__any_sync(0xffffffffu, live && rs > kRescaleBound)) break;
+            decided = true;
+          }
+          if constexpr (NARROW) {
+            // P: my keys, zeros for the other warps' (S covers all of P's columns);
+            // all loads of S by this warp are complete, the others read other rows
+            const uint32_t none[16] = {};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              if (c == wq)
+                tmem_st16(tS + c * 16, pk[0]);
+              else
+                tmem_st16(tS + c * 16, none);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) tmem_st16(tS + c * 16, pk[c]);
+          }
+          l = l * alpha + rs;
+          m = m_new;
+          const bool rescale = decided && j > 0 && __any_sync(0xffffffffu, live && alpha != 1.f);
+          if (!Cfg::kOutDoneLast && j > 0 && (rescale || j == n_tiles - 1) &&
+              !__all_sync(0xffffffffu, wait_bar(&bars->o_done[sub], (g - 1) & 1, abort, p.timeout_ns))) {
+            ok = false;
+          }
+          if (rescale && ok) {
+            tc_fence_after_sync();
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tO + c * 32, o);
+              tmem_ld_wait(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st32(tO + c * 32, o);
             }
           }
-          const float2 a01 = __fadd2_rn(acc[0], acc[1]);
-          const float2 a23 = __fadd2_rn(acc[2], acc[3]);
-          const float2 a = __fadd2_rn(a01, a23);
-          rs = a.x + a.y;
-        };
-        load_s();
-        const bool max_first = __any_sync(0xffffffffu, live && m == -INFINITY);
-        bool decided = max_first;
-        if (max_first) decide();
-        exps();
-        if (!max_first && __any_sync(0xffffffffu, live && rs > kRescaleBound)) {
-          load_s();
-          decide();
-          exps();
-          decided = true;
+          tmem_st_wait();
         }
-        tmem_st32(tS, pk[0]);
-        tmem_st32(tS + 32, pk[1]);
-        l = l * alpha + rs;
-        m = m_new;
-        const bool rescale = decided && j > 0 && __any_sync(0xffffffffu, live && alpha != 1.f);
-        if (!Cfg::kOutDoneLast && j > 0 && (rescale || j == n_tiles - 1) &&
-            !__all_sync(0xffffffffu, wait_bar(&bars->o_done[sub], (j - 1) & 1, abort, p.timeout_ns))) {
-          ok = false;
+        tc_fence_before_sync();
+        if constexpr (Cfg::kNamedP) {
+          __syncwarp();
+          named_sync(sub == 0 ? kBarP0 : kBarP1, sub == 0 ? kBarP0Count : kBarP1Count);
+        } else {
+          bar_arrive(&bars->p_ready[Cfg::kDoubleS ? (g & 1) : sub]);
         }
-        if (rescale && ok) {
+        announced = j + 1;
+      }
+      if constexpr (Cfg::kNamedP) {
+        // after an abort: the remaining phases, in step with the issuing warp
+        __syncwarp();
+        for (int j = announced; j < n_tiles; ++j)
+          named_sync(sub == 0 ? kBarP0 : kBarP1, sub == 0 ? kBarP0Count : kBarP1Count);
+      }
+
+      // Outputs: the item's rows, or this part's rows in its workspace slot.
+      const bool part = w.slot >= 0;
+      const bool fits = w.slot < p.slots;   // always, but for offsets that contradict each other
+      const bool store = live && fits;
+      const int in_token = row - tok * p.G;
+      const long long prow =
+          part ? static_cast<long long>(w.slot) * p.part_rows + sub_tok0 * p.G + row
+               : static_cast<long long>(w.row0 + sub_tok0 + tok) * p.Hq + w.head * p.G + in_token;
+      float* lse_out = (part ? p.LSE_part : p.LSE) + prow;
+      const bool half_out = p.o_half != 0 && !part;
+      if (!fits && threadIdx.x == 0) atomicOr(p.status, kDevErrPage);
+      if (n_tiles == 0 && store && ok && (!NARROW || wq == 0)) {
+        // no kept key: O = 0 and LSE = -inf (a part: LSE alone, the merge skips its O)
+        *lse_out = -INFINITY;
+        if (!part) {
+          uint8_t* o = static_cast<uint8_t*>(p.O) + prow * (half_out ? D * 2 : D * 4);
+          for (int c = 0; c < (half_out ? D * 2 : D * 4); c += 16)
+            *reinterpret_cast<uint4*>(o + c) = make_uint4(0, 0, 0, 0);
+        }
+      }
+      const uint32_t o_phase = Cfg::kOutDoneLast ? outs & 1 : (done + n_tiles - 1) & 1;
+      if constexpr (NARROW) {
+        // The four warps' shares of the rows: O = sum_w e_w O_w / sum_w e_w l_w, e_w =
+        // 2^(m_w - max m).  32 columns of 16 rows at a time through the staging
+        // rows.  Every warp passes every barrier, also after an abort.
+        if (n_tiles > 0) {
+          if (ok) ok = __all_sync(0xffffffffu, wait_bar(&bars->o_done[0], o_phase, abort, p.timeout_ns));
           tc_fence_after_sync();
+          if (ok && Cfg::kSoftmaxRelease && releaser) bar_arrive(&bars->kv_empty[(base + 2 * nmax - 1) % STAGES]);
+          shared->shares[wq][lane] = make_float2(m, l);
+          named_sync(kBarShares, kRowsPerSub);
+          float top = -INFINITY, sum = 0.f;
 #pragma unroll
+          for (int x = 0; x < 4; ++x) top = fmaxf(top, shared->shares[x][lane].x);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float2 ml = shared->shares[x][lane];
+            sum += ml.y == 0.f ? 0.f : ex2_approx(ml.x - top) * ml.y;   // (a warp without keys has m = -inf, l = 0)
+          }
+          const float mine = l == 0.f ? 0.f : ex2_approx(m - top) / sum;
+          if (store && ok && wq == 0) *lse_out = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;
+          const uint32_t stage = smem_addr(smem + Cfg::kSmemStage);   // [4][16 rows][128 bytes]
+          const int out_row = threadIdx.x >> 3, unit = threadIdx.x & 7;   // what I add up and store
+#pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
             tmem_ld32(tO + c * 32, o);
             tmem_ld_wait(o);
+#pragma unroll 1
+            for (int r0 = 0; r0 < rows; r0 += 16) {
+              if (lane >= r0 && lane < r0 + 16) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st32(tO + c * 32, o);
-          }
-        }
-        tmem_st_wait();
-      }
-      tc_fence_before_sync();
-      if constexpr (Cfg::kNamedP) {
-        __syncwarp();
-        named_sync(sub == 0 ? kBarP0 : kBarP1, sub == 0 ? kBarP0Count : kBarP1Count);
-      } else {
-        bar_arrive(&bars->p_ready[Cfg::kDoubleS ? (j & 1) : sub]);
-      }
-      announced = j + 1;
-      if (!ok) break;
-    }
-    if constexpr (Cfg::kNamedP) {
-      // after an abort: the remaining phases, in step with the issuing warp
-      __syncwarp();
-      for (int j = announced; j < n_tiles; ++j)
-        named_sync(sub == 0 ? kBarP0 : kBarP1, sub == 0 ? kBarP0Count : kBarP1Count);
-    }
-
-    // Outputs: the final rows, or this key range's rows in its workspace slot.
-    const bool part = w.valid && w.splits > 1;
-    const bool fits = !part || (w.slot >= 0 && w.slot < p.slots);   // always, for lengths within the launch's bounds
-    const bool store = live && fits;
-    const long long prow = part ? static_cast<long long>(w.slot) * p.part_rows + sub_tok0 * p.G + row
-                                : static_cast<long long>(w.row0 + sub_tok0 + tok) * p.Hq + w.head * p.G + (row - tok * p.G);
-    float* lse_out = (part ? p.LSE_part : p.LSE) + prow;
-    const bool half_out = p.o_half != 0 && !part;
-    if (w.valid && !fits && threadIdx.x == 0) atomicOr(p.status, kDevErrPage);
-    if (n_tiles == 0 && store) {
-      // no kept key: O = 0 and LSE = -inf (a key range: LSE alone, the merge skips its O)
-      *lse_out = -INFINITY;
-      if (!part) {
-        uint8_t* o = static_cast<uint8_t*>(p.O) + prow * (half_out ? D * 2 : D * 4);
-        for (int c = 0; c < (half_out ? D * 2 : D * 4); c += 16) *reinterpret_cast<uint4*>(o + c) = make_uint4(0, 0, 0, 0);
-      }
-    }
-    if (n_tiles > 0 && ok) {
-      if (store) *lse_out = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
-      if (!__all_sync(0xffffffffu,
-                      wait_bar(&bars->o_done[sub], Cfg::kOutDoneLast ? 0u : (n_tiles - 1) & 1, abort, p.timeout_ns))) {
-        ok = false;
-      } else if (warp_live) {
-        tc_fence_after_sync();
-        // O / l goes through this warp's quarter of its sub-tile's Q buffer
-        // (every S MMA that read it has completed) so that the global stores
-        // are whole rows: D * 2 bytes a row and round (fp32 O: two rounds).
-        const float inv_l = l == 0.f ? 0.f : 1.f / l;
-        constexpr int kUnits = D / 8;               // 16-byte units of a staged row
-        const uint32_t stage = smem_addr(sQ + sub * TILE) + wq * (TILE / 4);
-        const uint32_t mine = stage + lane * (D * 2);
-        const long long row_bytes = half_out ? D * 2 : D * 4;
-        uint8_t* base = static_cast<uint8_t*>(part ? static_cast<void*>(p.O_part) : p.O);
-        const long long my_off = store ? prow * row_bytes : -1;
-        const int parts = half_out ? 1 : 2;
-        for (int r = 0; r < parts; ++r) {
-          if (r > 0) __syncwarp();
+                for (int u = 0; u < 8; ++u)
+                  st_shared_v4(stage + wq * 2048 + (lane & 15) * 128 + ((u ^ (lane & 7)) << 4),
+                               __float_as_uint(__uint_as_float(o[4 * u]) * mine),
+                               __float_as_uint(__uint_as_float(o[4 * u + 1]) * mine),
+                               __float_as_uint(__uint_as_float(o[4 * u + 2]) * mine),
+                               __float_as_uint(__uint_as_float(o[4 * u + 3]) * mine));
+              }
+              named_sync(kBarShares, kRowsPerSub);
+              const int r = r0 + out_row;
+              if (r < rows && fits && ok) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int b = 0; b < D / 64; ++b) {
-            if (!half_out) {
-              uint32_t o[32];
-              tmem_ld32(tO + r * (D / 2) + 32 * b, o);
-              tmem_ld_wait(o);
-#pragma unroll
-              for (int u = 0; u < 8; ++u)
-                st_shared_v4(mine + (((b * 8 + u) ^ (lane & 7)) << 4), __float_as_uint(__uint_as_float(o[4 * u]) * inv_l),
-                             __float_as_uint(__uint_as_float(o[4 * u + 1]) * inv_l),
-                             __float_as_uint(__uint_as_float(o[4 * u + 2]) * inv_l),
-                             __float_as_uint(__uint_as_float(o[4 * u + 3]) * inv_l));
-            } else {
-              uint32_t o[2][32];
-              tmem_ld32(tO + 64 * b, o[0]);
-              tmem_ld32(tO + 64 * b + 32, o[1]);
-              tmem_ld_wait(o[0]);
-              tmem_ld_wait(o[1]);
-              uint32_t h[32];
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                h[e] = pack_x2<F16>(__uint_as_float(o[e >> 4][(2 * e) & 31]) * inv_l,
-                                    __uint_as_float(o[e >> 4][(2 * e + 1) & 31]) * inv_l);
-#pragma unroll
-              for (int u = 0; u < 8; ++u)
-                st_shared_v4(mine + (((b * 8 + u) ^ (lane & 7)) << 4), h[4 * u], h[4 * u + 1], h[4 * u + 2], h[4 * u + 3]);
+                for (int x = 0; x < 4; ++x) {
+                  float4 y;
+                  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                               : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w)
+                               : "r"(stage + x * 2048 + out_row * 128 + ((unit ^ (out_row & 7)) << 4))
+                               : "memory");
+                  v.x += y.x;
+                  v.y += y.y;
+                  v.z += y.z;
+                  v.w += y.w;
+                }
+                const int column = c * 32 + unit * 4, t = r / p.G;
+                const long long o_row = static_cast<long long>(w.row0 + t) * p.Hq + w.head * p.G + (r - t * p.G);
+                if (part)
+                  *reinterpret_cast<float4*>(p.O_part + static_cast<long long>(w.slot) * p.part_rows * D +
+                                             (static_cast<long long>(column / 4) * p.part_rows + r) * 4) = v;
+                else if (half_out)
+                  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) + o_row * D + column) =
+                      make_uint2(pack_x2<F16>(v.x, v.y), pack_x2<F16>(v.z, v.w));
+                else
+                  *reinterpret_cast<float4*>(static_cast<float*>(p.O) + o_row * D + column) = v;
+              }
+              named_sync(kBarShares, kRowsPerSub);
             }
           }
-          __syncwarp();
-          constexpr int kRowsPer = 32 / kUnits > 0 ? 32 / kUnits : 1;   // rows written by one warp store
-#pragma unroll 4
-          for (int i = 0; i < 32; i += kRowsPer) {
-            const int rr = i + lane / kUnits, unit = lane % kUnits;
-            const long long off = __shfl_sync(0xffffffffu, my_off, rr);
-            uint32_t v[4];
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                         : "r"(stage + rr * (D * 2) + ((unit ^ (rr & 7)) << 4)));
-            if (off >= 0)
-              *reinterpret_cast<uint4*>(base + off + r * (D * 2) + unit * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+          tc_fence_before_sync();
+        }
+      } else if (n_tiles > 0 && ok) {
+        if (store) *lse_out = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
+        if (!__all_sync(0xffffffffu, wait_bar(&bars->o_done[sub], o_phase, abort, p.timeout_ns))) {
+          ok = false;
+        } else {
+          tc_fence_after_sync();
+          // the last V of the segment: every MMA that reads it is complete
+          if (Cfg::kSoftmaxRelease && releaser) bar_arrive(&bars->kv_empty[(base + 2 * nmax - 1) % STAGES]);
+          const float inv_l = l == 0.f ? 0.f : 1.f / l;
+          if (part && warp_live) {
+            float* dst = p.O_part + static_cast<long long>(w.slot) * p.part_rows * D + (sub_tok0 * p.G + row) * 4;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tO + c * 32, o);
+              tmem_ld_wait(o);
+              if (store) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                  *reinterpret_cast<float4*>(dst + static_cast<long long>(c * 8 + e / 4) * p.part_rows * 4) =
+                      make_float4(__uint_as_float(o[e]) * inv_l, __uint_as_float(o[e + 1]) * inv_l,
+                                  __uint_as_float(o[e + 2]) * inv_l, __uint_as_float(o[e + 3]) * inv_l);
+              }
+            }
+          } else if (warp_live) {
+            // O / l, 64 bytes of each row at a time through this warp's staging
+            // rows (16-byte units exchanged so that writes touch every bank),
+            // so that four lanes store 64 neighbouring bytes of a row.
+            const uint32_t stage = smem_addr(smem + Cfg::kSmemStage) + warp * Cfg::kStageBytes;
+            const uint32_t mine = stage + lane * 64;
+            const int turn = (lane >> 1) & 3;
+            uint8_t* out = static_cast<uint8_t*>(p.O);
+            const long long my_off = store ? prow * (half_out ? D * 2 : D * 4) : -1;
+            const int warp_rows = min(32, rows - wq * 32);
+            auto put = [&](int column_bytes, const uint32_t (&v)[16]) {   // 64 bytes of my row
+              __syncwarp();
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                st_shared_v4(mine + ((u ^ turn) << 4), v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 32; i += 8) {
+                if (i >= warp_rows) break;
+                const int rr = i + (lane >> 2), unit = lane & 3;
+                const long long off = __shfl_sync(0xffffffffu, my_off, rr);
+                uint32_t x[4];
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                             : "r"(stage + rr * 64 + ((unit ^ ((rr >> 1) & 3)) << 4))
+                             : "memory");
+                if (off >= 0)
+                  *reinterpret_cast<uint4*>(out + off + column_bytes + unit * 16) = make_uint4(x[0], x[1], x[2], x[3]);
+              }
+            };
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tO + c * 32, o);
+              tmem_ld_wait(o);
+              uint32_t v[16];
+              if (half_out) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  v[e] = pack_x2<F16>(__uint_as_float(o[2 * e]) * inv_l, __uint_as_float(o[2 * e + 1]) * inv_l);
+                put(c * 64, v);
+              } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(o[16 * h + e]) * inv_l);
+                  put(c * 128 + h * 64, v);
+                }
+              }
+            }
           }
+          tc_fence_before_sync();
         }
       }
+      if (n_tiles > 0) ++outs;
+      done += n_tiles;
+      base += 2 * nmax;
+      if (!ok) raise_abort(abort, p.status);
     }
-    if (!ok) raise_abort(abort, p.status);
   }
 
   // ------------------------------------------------------------ teardown
@@ -756,49 +1223,96 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
   }
 }
 
-constexpr int kPagedMergeWarps = 8;
+constexpr int kPagedMergeWarps = 4;
+constexpr int kPagedMergeRows = 8;    // rows of a warp
+constexpr int kPagedMergeMany = 6;    // parts from which the warps of a block share one row group's parts
 
-// Merge of the key ranges of one item: one CTA per item that was cut, a warp
-// per row.  With m = max_s L_s and w_s = exp(L_s - m): O = sum_s w_s O_s / sum
-// w_s, LSE = m + log sum w_s; ranges with L_s = -inf are skipped unread.
+// Merge of the parts of cut items: blockIdx.x names an item, the blocks of a
+// column share its rows, eight rows a warp: lane = (row, 4 of 16 columns), so
+// that reads are 128 and writes 32 neighbouring bytes at least.  With m = max_s
+// L_s and w_s = exp(L_s - m): O = sum_s w_s O_s / sum w_s, LSE = m + log sum w_s;
+// parts with L_s = -inf have w_s = 0 and their O is not read.  An item of many
+// parts has few rows (it was cut because there were few items): its block's
+// warps take every fourth part each and add up through shared memory.
 template <int D, bool F16, int SUBS>
-__global__ void __launch_bounds__(kPagedMergeWarps * 32) fa2_paged_merge_kernel(const PagedParams p) {
-  constexpr int V = D / 32;
-  const PagedUnit w = paged_locate<SUBS>(p, static_cast<int>(blockIdx.x), true, D);
-  if (!w.valid || w.slot < 0 || w.slot + w.splits > p.slots) return;
-  const int lane = threadIdx.x & 31;
-  for (int row = threadIdx.x >> 5; row < w.ntok * p.G; row += kPagedMergeWarps) {
-    const float* L = p.LSE_part + static_cast<long long>(w.slot) * p.part_rows + row;
+__global__ void __launch_bounds__(kPagedMergeWarps * 32) fa2_paged_merge_kernel(const __grid_constant__ PagedParams p) {
+  __shared__ float4 sums[kPagedMergeWarps - 1][D / 16][32];
+  __shared__ float weights[kPagedMergeWarps - 1][32];
+  const int index = static_cast<int>(blockIdx.x);
+  const PagedParts w = p.even ? paged_parts_even<SUBS>(p, index) : paged_item<SUBS>(p, index, true, D);
+  // launched while the partial results are computed: they are complete from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!w.u.valid || w.first < 0 || w.first >= p.slots || w.rest + (w.parts - 2) * w.step >= p.slots) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rows = w.u.ntok * p.G;
+  const bool share = w.parts >= kPagedMergeMany;
+  const int first = share ? warp : 0, step = share ? kPagedMergeWarps : 1;
+  const int groups = share ? 1 : kPagedMergeWarps;   // row groups of the block
+  for (int g0 = blockIdx.y * groups; g0 * kPagedMergeRows < rows; g0 += groups * gridDim.y) {
+    const int row = (g0 + (share ? 0 : warp)) * kPagedMergeRows + (lane & 7), group = lane >> 3;
+    const bool live = row < rows;
+    auto slot = [&](int s) { return static_cast<long long>(s == 0 ? w.first : w.rest + (s - 1) * w.step); };
+    const float* L = p.LSE_part + (live ? row : 0);
     float mx = -INFINITY;
-    for (int s = lane; s < w.splits; s += 32) mx = fmaxf(mx, L[static_cast<long long>(s) * p.part_rows]);
+#pragma unroll 4
+    for (int s = 0; s < w.parts; ++s) mx = fmaxf(mx, L[slot(s) * p.part_rows]);
+    float4 acc[D / 16];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    float acc[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+    for (int c = 0; c < D / 16; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
-    for (int s = 0; s < w.splits; ++s) {
-      const float ls = L[static_cast<long long>(s) * p.part_rows];
-      if (ls == -INFINITY) continue;
+#pragma unroll 2
+    for (int s = first; s < w.parts; s += step) {
+      const float ls = L[slot(s) * p.part_rows];
+      if (!live || ls == -INFINITY) continue;
       const float e = expf(ls - mx);
       sum += e;
-      const float* src = p.O_part + ((static_cast<long long>(w.slot) + s) * p.part_rows + row) * D + lane * V;
+      const float* src = p.O_part + (slot(s) * (D / 4) + group) * p.part_rows * 4 + row * 4;
 #pragma unroll
-      for (int c = 0; c < V; ++c) acc[c] = fmaf(e, src[c], acc[c]);
+      for (int c = 0; c < D / 16; ++c) {
+        const float4 x = *reinterpret_cast<const float4*>(src + static_cast<long long>(c) * 16 * p.part_rows);
+        acc[c].x = fmaf(e, x.x, acc[c].x);
+        acc[c].y = fmaf(e, x.y, acc[c].y);
+        acc[c].z = fmaf(e, x.z, acc[c].z);
+        acc[c].w = fmaf(e, x.w, acc[c].w);
+      }
     }
-    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+    if (share) {
+      __syncthreads();   // the last row group's sums are read
+      if (warp > 0) {
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) sums[warp - 1][c][lane] = acc[c];
+        weights[warp - 1][lane] = sum;
+      }
+      __syncthreads();
+      if (warp > 0) continue;
+#pragma unroll
+      for (int x = 0; x < kPagedMergeWarps - 1; ++x) {
+        sum += weights[x][lane];
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          const float4 y = sums[x][c][lane];
+          acc[c].x += y.x;
+          acc[c].y += y.y;
+          acc[c].z += y.z;
+          acc[c].w += y.w;
+        }
+      }
+    }
+    if (!live) continue;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int tok = row / p.G;
-    const long long out = static_cast<long long>(w.row0 + tok) * p.Hq + w.head * p.G + (row - tok * p.G);
-    if (p.o_half) {
-      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.O) + out * D + lane * V);
+    const long long out = static_cast<long long>(w.u.row0 + tok) * p.Hq + w.u.head * p.G + (row - tok * p.G);
 #pragma unroll
-      for (int c = 0; c < V; c += 2) dst[c / 2] = pack_x2<F16>(acc[c] * inv, acc[c + 1] * inv);
-    } else {
-      float* dst = static_cast<float*>(p.O) + out * D + lane * V;
-#pragma unroll
-      for (int c = 0; c < V; ++c) dst[c] = acc[c] * inv;
+    for (int c = 0; c < D / 16; ++c) {
+      const long long at = out * D + c * 16 + group * 4;
+      const float4 x = make_float4(acc[c].x * inv, acc[c].y * inv, acc[c].z * inv, acc[c].w * inv);
+      if (p.o_half)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.O) + at) =
+            make_uint2(pack_x2<F16>(x.x, x.y), pack_x2<F16>(x.z, x.w));
+      else
+        *reinterpret_cast<float4*>(static_cast<float*>(p.O) + at) = x;
     }
-    if (lane == 0) p.LSE[out] = sum == 0.f ? -INFINITY : mx + logf(sum);
+    if (group == 0) p.LSE[out] = sum == 0.f ? -INFINITY : mx + logf(sum);
   }
 }
 

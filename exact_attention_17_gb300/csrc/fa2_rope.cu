@@ -11,14 +11,17 @@
 // Angles.  t f in 32 bits is off by whole turns at far positions, and 64-bit
 // floating point is slow here.  f / (2 pi) is turned into a 64-bit fixed-point
 // fraction of a turn with one 64 x 64-bit multiplication; times t modulo 2^64 it
-// is the exact angle of the rounded frequency (error below |t| 2^-63 turns), and
-// its top 32 bits, rounded to fp32, go to sincospif: the angle is within 2^-25
-// turns for every 32-bit position.
+// is the exact angle of the rounded frequency (error below |t| 2^-63 turns).  Its
+// top 32 bits give the quadrant and a remainder of at most an eighth turn, whose
+// sine and cosine are Taylor polynomials (degree 9 and 10: remainders below
+// 2e-9 and 2e-10): about 30 instructions a pair, a third of a library call.
 //
-// Bound: bytes (each row read and written once).  A block takes `tokens` x
-// `rows` head rows; each thread first loads its vectors (up to four pairs of 16
-// bytes), then the block computes the sines of its tokens once for all heads in
-// shared memory, then rotates and stores: the arithmetic overlaps the loads.
+// Bound: bytes (each row read and written once).  A thread keeps one unit of the
+// head (two 8-byte vectors of 16-bit elements whose columns are rotated against
+// each other, or one 16-byte vector of neighbouring pairs) at one token: it
+// computes the unit's four sines once, in registers, and then runs over the
+// heads, four at a time.  Nothing goes through shared memory but, for the cache,
+// where the block's tokens lie.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -28,6 +31,7 @@
 namespace fa2dev {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeUnroll = 4;   // heads whose loads a thread has in flight
 
 // 2^64 times the fraction of a turn that f radians are, modulo 2^64.
 // |f| = mant 2^(e-1075); kTurn = 2^66 / (2 pi) rounded, so |f| / (2 pi) 2^64 =
@@ -51,10 +55,24 @@ __device__ __forceinline__ unsigned long long turns_of(double f) {
 // (cos, sin) times m of `pos` steps of f radians
 __device__ __forceinline__ float2 rotation(double f, long long pos, float m, bool transposed) {
   const unsigned long long t = turns_of(f) * static_cast<unsigned long long>(pos);
-  const int top = static_cast<int>(static_cast<long long>(t) >> 32);   // turns * 2^32, in [-1/2, 1/2)
-  float s, c;
-  sincospif(static_cast<float>(top) * 0x1p-31f, &s, &c);
-  return make_float2(c * m, transposed ? -s * m : s * m);
+  const uint32_t top = static_cast<uint32_t>(t >> 32);   // turns * 2^32
+  const uint32_t quadrant = (top + 0x20000000u) >> 30;
+  const float y = static_cast<float>(static_cast<int>(top - (quadrant << 30))) * 1.4629180792671596e-9f;   // 2 pi / 2^32
+  const float z = y * y;
+  float s = 2.7557319e-6f, c = -2.7557319e-7f;   // 1 / 9!, -1 / 10!
+  s = fmaf(s, z, -1.9841270e-4f);                // 1 / 7!
+  s = fmaf(s, z, 8.3333333e-3f);
+  s = fmaf(s, z, -1.6666667e-1f);
+  s = fmaf(s * z, y, y);
+  c = fmaf(c, z, 2.4801587e-5f);                 // 1 / 8!
+  c = fmaf(c, z, -1.3888889e-3f);
+  c = fmaf(c, z, 4.1666667e-2f);
+  c = fmaf(c, z, -0.5f);
+  c = fmaf(c, z, 1.0f);
+  const float a = (quadrant & 1) ? s : c, b = (quadrant & 1) ? c : s;
+  const float mc = (quadrant == 1 || quadrant == 2) ? -m : m;
+  const float ms = ((quadrant >= 2) != transposed) ? -m : m;
+  return make_float2(a * mc, b * ms);
 }
 
 template <typename T> __device__ __forceinline__ float to_float(T x);
@@ -72,175 +90,168 @@ struct alignas(sizeof(T) * W) Vec {
   T v[W];
 };
 
-// Where a block's tokens go.
+// Where a new token of a cache goes.
 struct RopeToken {
-  long long src;     // element offset of the token in x (or its index in the packed tensors)
-  long long dst;     // the same in the output (append: offset of its slot in the pages, -1: not written)
+  long long dst;     // element offset of its slot in the pages, -1: not written
   long long pos;
   int live;          // 0: nothing is written for this token
 };
 
-// A block's rows: `tokens` consecutive tokens times `rows` consecutive head
-// rows.  Work is numbered (token, row, unit); unit u of a row is the pair of
-// vectors (u, u + half) when HALF, else the vector u.  Rows of W elements:
-// the rotated vectors first, then the copied ones two at a time (HALF) or one.
-template <typename T, int W, bool HALF, bool APPEND, int ITEMS>
-__global__ void __launch_bounds__(kRopeThreads) fa2_rope_kernel(const RopeParams p) {
-  extern __shared__ float2 cs[];   // [tokens][r / 2]
-  __shared__ RopeToken toks[kRopeMaxTokens];
-  using V = Vec<T, W>;
-  const int tile = fast_div(static_cast<int>(blockIdx.x), p.div_row_tiles);
-  const int row0 = (static_cast<int>(blockIdx.x) - tile * p.row_tiles) * p.rows;
-  const long long tok0 = static_cast<long long>(tile) * p.tokens;
-  const int n_tok = static_cast<int>(min(static_cast<long long>(p.tokens), p.total_tokens - tok0));
-  const int n_row = min(p.rows, p.total_rows - row0);
-  const int half = p.r / 2;
-
-  // ---- the block's tokens
-  if constexpr (APPEND) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int k = warp; k < n_tok; k += kRopeThreads / 32) {
-      const int t = static_cast<int>(tok0) + k;
-      int b = t, begin = t, end = t + 1;
-      if (p.cu_q != nullptr) {
-        int c = 0;   // sequences that end at or before t
-        for (int i = lane + 1; i <= p.B; i += 32) c += p.cu_q[i] <= t ? 1 : 0;
-        b = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(c)));
-        begin = b < p.B ? p.cu_q[b] : 0;
-        end = b < p.B ? p.cu_q[b + 1] : 0;
-      }
-      if (lane == 0) {
-        RopeToken& o = toks[k];
-        o.src = t;
-        o.dst = -1;
-        o.live = b < p.B && begin <= t && t < end;
-        o.pos = 0;
-        if (o.live) {
-          const int len = p.kv_lens[b];
-          const long long pos = static_cast<long long>(len) - end + t;
-          o.pos = pos;
-          if (len > p.max_len) {
+// Whole block: positions and slots of `n_tok` tokens from tok0 on, a warp per token.
+__device__ __forceinline__ void append_tokens(const RopeParams& p, int tok0, int n_tok, RopeToken* toks) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int k = warp; k < n_tok; k += kRopeThreads / 32) {
+    const int t = tok0 + k;
+    int b = t, begin = t, end = t + 1;
+    if (p.cu_q != nullptr) {
+      int c = 0;   // sequences that end at or before t
+      for (int i = lane + 1; i <= p.B; i += 32) c += p.cu_q[i] <= t ? 1 : 0;
+      b = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(c)));
+      begin = b < p.B ? p.cu_q[b] : 0;
+      end = b < p.B ? p.cu_q[b + 1] : 0;
+    }
+    if (lane == 0) {
+      RopeToken o;
+      o.dst = -1;
+      o.pos = 0;
+      o.live = b < p.B && begin <= t && t < end;
+      if (o.live) {
+        const int len = p.kv_lens[b];
+        const long long pos = static_cast<long long>(len) - end + t;
+        o.pos = pos;
+        if (len > p.max_len) {
+          atomicOr(p.status, kDevErrPage);
+        } else if (pos >= 0) {
+          const int page = p.page_table[b * p.table_stride + (pos >> p.page_log2)];
+          if (page < 0 || page >= p.num_pages)
             atomicOr(p.status, kDevErrPage);
-          } else if (pos >= 0) {
-            const int page = p.page_table[b * p.table_stride + (pos >> p.page_log2)];
-            if (page < 0 || page >= p.num_pages)
-              atomicOr(p.status, kDevErrPage);
-            else
-              o.dst = page * p.page_stride + (pos & ((1 << p.page_log2) - 1)) * p.slot_stride;
-          }
+          else
+            o.dst = page * p.page_stride + (pos & ((1 << p.page_log2) - 1)) * p.slot_stride;
         }
       }
-    }
-  } else {
-    for (int k = threadIdx.x; k < n_tok; k += kRopeThreads) {
-      const long long t = tok0 + k;
-      const long long b = t / p.N, n = t - b * p.N;
-      RopeToken& o = toks[k];
-      o.src = b * p.x_batch + n * p.x_token;
-      o.dst = b * p.y_batch + n * p.y_token;
-      const long long at = b * p.pos_batch + n;
-      o.pos = p.pos64 ? static_cast<const long long*>(p.positions)[at] : static_cast<const int*>(p.positions)[at];
-      o.live = 1;
+      toks[k] = o;
     }
   }
-  __syncthreads();
+}
 
-  // ---- loads
-  constexpr int PAIR = HALF ? 2 : 1;                 // vectors per unit
-  const int rot_units = p.r / (W * PAIR);            // units that rotate
-  const int units = p.units;
-  const int total = n_tok * n_row * units;
-  V a[ITEMS], b2[ITEMS];
-  T* to[ITEMS];
-  T* to2[ITEMS];
-  int how[ITEMS];   // index of the token's first sine of this unit, or -1: copy, -2: nothing
-  for (int base = 0; base < total; base += kRopeThreads * ITEMS) {
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const int item = base + i * kRopeThreads + threadIdx.x;
-      how[i] = -2;
-      to[i] = to2[i] = nullptr;
-      if (item >= total) continue;
-      const int rr = fast_div(item, p.div_units);
-      const int u = item - rr * units;
-      const int k = n_row == p.rows ? fast_div(rr, p.div_rows) : rr / n_row;
-      int row = row0 + (rr - k * n_row);
-      const RopeToken tk = toks[k];
-      if (!tk.live) continue;
+// Unit u of a head row is the pair of vectors (u, u + half) when HALF, else the
+// vector u; behind the rotated units come the copied ones, two vectors at a
+// time (HALF) or one.
+template <typename T, int W, bool HALF, bool APPEND>
+__global__ void __launch_bounds__(kRopeThreads, 3) fa2_rope_kernel(const __grid_constant__ RopeParams p) {
+  using V = Vec<T, W>;
+  constexpr int PAIRS = HALF ? W : W / 2;
+  __shared__ RopeToken toks[APPEND ? kRopeThreads : 1];
+  const long long tok0 = static_cast<long long>(blockIdx.x) * p.tokens;
+  const int n_tok = static_cast<int>(min(static_cast<long long>(p.tokens), p.total_tokens - tok0));
+  const int row0 = blockIdx.y * p.rows, row1 = min(row0 + p.rows, p.total_rows);
+  const int rot_units = p.r / (HALF ? 2 * W : W);
+
+  for (int base = 0; base < n_tok * p.units; base += kRopeThreads) {   // once, but for rows of more than 256 units
+    const int id = base + threadIdx.x;
+    const bool active = id < n_tok * p.units;
+    const int k = active ? fast_div(id, p.div_units) : 0;
+    const int u = active ? id - k * p.units : 0;
+    const long long t = tok0 + k;
+    long long batch = 0, n = t;
+    if (!APPEND && p.N < p.total_tokens) {
+      batch = t < 0x7fffffff ? static_cast<long long>(fast_div(static_cast<int>(t), p.div_n)) : t / p.N;
+      n = t - batch * p.N;
+    }
+    // columns of the unit's vectors: c and, when `two`, c + second
+    const bool rotate = u < rot_units;
+    int c = u * W, second = p.r / 2;
+    bool two = HALF;
+    if (HALF && !rotate) {
+      c = p.r + (u - rot_units) * 2 * W;
+      second = W;
+      two = c + W < p.d;
+    }
+    // where row `row` of the token is read
+    auto from = [&](int row) {
       const T* x;
-      T* y;
-      bool rotate = u < rot_units;
-      if constexpr (APPEND) {
-        if (row < p.Hq) {
-          x = static_cast<const T*>(p.q) + tk.src * p.q_token + row * p.q_head;
-          y = static_cast<T*>(p.q_out) + tk.src * p.qo_token + row * p.qo_head;
-        } else {
-          if (tk.dst < 0) continue;
-          row -= p.Hq;
-          const bool value = row >= p.Hkv;
-          if (value) row -= p.Hkv;
-          x = value ? static_cast<const T*>(p.v) + tk.src * p.v_token + row * p.v_head
-                    : static_cast<const T*>(p.k) + tk.src * p.k_token + row * p.k_head;
-          y = static_cast<T*>(value ? p.v_pages : p.k_pages) + tk.dst + row * p.page_head;
-          if (value) rotate = false;
-        }
+      if constexpr (APPEND) {   // the queries' heads, the keys', the values'
+        if (row < p.Hq) x = static_cast<const T*>(p.q) + t * p.q_token + row * p.q_head;
+        else if (row < p.Hq + p.Hkv) x = static_cast<const T*>(p.k) + t * p.k_token + (row - p.Hq) * p.k_head;
+        else x = static_cast<const T*>(p.v) + t * p.v_token + (row - p.Hq - p.Hkv) * p.v_head;
       } else {
-        x = static_cast<const T*>(p.x) + tk.src + row * p.x_head;
-        y = static_cast<T*>(p.y) + tk.dst + row * p.y_head;
+        x = static_cast<const T*>(p.x) + batch * p.x_batch + n * p.x_token + row * p.x_head;
       }
-      // columns of the unit's vectors: (c, c2), c2 < 0: one vector
-      int c, c2 = -1;
-      if constexpr (HALF) {
-        if (u < rot_units) {
-          c = u * W;
-          c2 = c + half;
-        } else {
-          c = p.r + (u - rot_units) * 2 * W;
-          c2 = c + W < p.d ? c + W : -1;
-        }
-      } else {
-        c = u * W;
-      }
-      a[i] = *reinterpret_cast<const V*>(x + c);
-      to[i] = y + c;
-      if (HALF && c2 >= 0) {
-        b2[i] = *reinterpret_cast<const V*>(x + c2);
-        to2[i] = y + c2;
-      }
-      how[i] = rotate ? k * half + (HALF ? u * W : u * W / 2) : -1;
-    }
-    // ---- sines, once per block, while the first loads are in flight
-    if (base == 0 && half > 0) {
-      for (int e = threadIdx.x; e < n_tok * half; e += kRopeThreads) {
-        const int k = fast_div(e, p.div_half);
-        cs[e] = rotation(p.inv_freq[e - k * half], toks[k].pos, p.mscale, p.transposed != 0);
-      }
-      __syncthreads();
-    }
+      return x + c;
+    };
+    V a[kRopeUnroll], b[kRopeUnroll];
+    auto load = [&](int row) {
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      if (how[i] >= 0) {
-        const float2* t = cs + how[i];
-        if constexpr (HALF) {
+      for (int i = 0; i < kRopeUnroll; ++i) {
+        if (!active || row + i >= row1) continue;
+        const T* x = from(row + i);
+        a[i] = *reinterpret_cast<const V*>(x);
+        if (HALF && two) b[i] = *reinterpret_cast<const V*>(x + second);
+      }
+    };
+    // the first heads, the frequencies and the positions are all on their way at once
+    load(row0);
+    double f[PAIRS];
+    if (rotate) {
 #pragma unroll
-          for (int e = 0; e < W; ++e) {
-            const float x0 = to_float(a[i].v[e]), x1 = to_float(b2[i].v[e]);
-            const float2 w = t[e];
-            a[i].v[e] = from_float<T>(x0 * w.x - x1 * w.y);
-            b2[i].v[e] = from_float<T>(x1 * w.x + x0 * w.y);
+      for (int e = 0; e < PAIRS; ++e) f[e] = p.inv_freq[HALF ? c + e : c / 2 + e];
+    }
+    long long pos, slot = -1;
+    bool live = active;
+    if constexpr (APPEND) {
+      if (base == 0) {
+        append_tokens(p, static_cast<int>(tok0), n_tok, toks);
+        __syncthreads();
+      }
+      pos = toks[k].pos;
+      slot = toks[k].dst;
+      live = active && toks[k].live;
+    } else {
+      const long long at = batch * p.pos_batch + n;
+      pos = p.pos64 ? static_cast<const long long*>(p.positions)[at] : static_cast<const int*>(p.positions)[at];
+    }
+    if (!live) continue;   // (no barrier follows but in rows of more than 256 units, which are of one token)
+    float2 w[PAIRS];
+    if (rotate) {
+#pragma unroll
+      for (int e = 0; e < PAIRS; ++e) w[e] = rotation(f[e], pos, p.mscale, p.transposed != 0);
+    }
+    for (int row = row0;;) {
+#pragma unroll
+      for (int i = 0; i < kRopeUnroll; ++i) {
+        const int r = row + i;
+        if (r >= row1) continue;
+        T* y;
+        bool turn = rotate;
+        if constexpr (APPEND) {
+          if (r < p.Hq) {
+            y = static_cast<T*>(p.q_out) + t * p.qo_token + r * p.qo_head;
+          } else {
+            if (slot < 0) continue;
+            const bool value = r >= p.Hq + p.Hkv;
+            y = static_cast<T*>(value ? p.v_pages : p.k_pages) + slot + (r - p.Hq - (value ? p.Hkv : 0)) * p.page_head;
+            turn = rotate && !value;
           }
         } else {
+          y = static_cast<T*>(p.y) + batch * p.y_batch + n * p.y_token + r * p.y_head;
+        }
+        y += c;
+        if (turn) {
 #pragma unroll
-          for (int e = 0; e < W; e += 2) {
-            const float x0 = to_float(a[i].v[e]), x1 = to_float(a[i].v[e + 1]);
-            const float2 w = t[e / 2];
-            a[i].v[e] = from_float<T>(x0 * w.x - x1 * w.y);
-            a[i].v[e + 1] = from_float<T>(x1 * w.x + x0 * w.y);
+          for (int e = 0; e < PAIRS; ++e) {
+            T& lo = HALF ? a[i].v[e] : a[i].v[2 * e];
+            T& hi = HALF ? b[i].v[e] : a[i].v[2 * e + 1];
+            const float x0 = to_float(lo), x1 = to_float(hi);
+            lo = from_float<T>(x0 * w[e].x - x1 * w[e].y);
+            hi = from_float<T>(x1 * w[e].x + x0 * w[e].y);
           }
         }
+        *reinterpret_cast<V*>(y) = a[i];
+        if (HALF && two) *reinterpret_cast<V*>(y + second) = b[i];
       }
-      if (to[i] != nullptr) *reinterpret_cast<V*>(to[i]) = a[i];
-      if (HALF && to2[i] != nullptr) *reinterpret_cast<V*>(to2[i]) = b2[i];
+      row += kRopeUnroll;
+      if (row >= row1) break;
+      load(row);
     }
   }
 }
@@ -252,31 +263,24 @@ namespace {
 
 using fa2dev::RopeParams;
 
-template <typename T, int W, bool HALF, bool APPEND, int ITEMS>
-cudaError_t run(const RopeParams& p, unsigned grid, size_t smem, cudaStream_t s) {
-  fa2dev::fa2_rope_kernel<T, W, HALF, APPEND, ITEMS><<<grid, fa2dev::kRopeThreads, smem, s>>>(p);
+template <typename T, int W, bool HALF, bool APPEND>
+cudaError_t run(const RopeParams& p, dim3 grid, cudaStream_t s) {
+  fa2dev::fa2_rope_kernel<T, W, HALF, APPEND><<<grid, fa2dev::kRopeThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
-template <typename T, int W, bool APPEND>
-cudaError_t by_layout(const RopeParams& p, unsigned grid, size_t smem, int items, cudaStream_t s) {
-  constexpr int WI = W > 1 ? W : 2;   // an interleaved pair is two neighbours at least
-  if (p.interleaved)
-    return items == 1 ? run<T, WI, false, APPEND, 1>(p, grid, smem, s) : run<T, WI, false, APPEND, 4>(p, grid, smem, s);
-  return items == 1 ? run<T, W, true, APPEND, 1>(p, grid, smem, s) : run<T, W, true, APPEND, 4>(p, grid, smem, s);
-}
-
 template <typename T, bool APPEND>
-cudaError_t by_width(const RopeParams& p, unsigned grid, size_t smem, int items, bool wide, cudaStream_t s) {
-  return wide ? by_layout<T, 16 / sizeof(T), APPEND>(p, grid, smem, items, s)
-              : by_layout<T, 1, APPEND>(p, grid, smem, items, s);
+cudaError_t by_layout(const RopeParams& p, dim3 grid, bool wide, cudaStream_t s) {
+  if (p.interleaved)   // a pair is two neighbours at least
+    return wide ? run<T, rope_width(sizeof(T), true), false, APPEND>(p, grid, s) : run<T, 2, false, APPEND>(p, grid, s);
+  return wide ? run<T, rope_width(sizeof(T), false), true, APPEND>(p, grid, s) : run<T, 1, true, APPEND>(p, grid, s);
 }
 
 template <bool APPEND>
-cudaError_t by_type(const RopeParams& p, int dtype, unsigned grid, size_t smem, int items, bool wide, cudaStream_t s) {
-  if (dtype == FA2_DTYPE_BF16) return by_width<__nv_bfloat16, APPEND>(p, grid, smem, items, wide, s);
-  if (dtype == FA2_DTYPE_FP16) return by_width<__half, APPEND>(p, grid, smem, items, wide, s);
-  if constexpr (!APPEND) return by_width<float, APPEND>(p, grid, smem, items, wide, s);
+cudaError_t by_type(const RopeParams& p, int dtype, dim3 grid, bool wide, cudaStream_t s) {
+  if (dtype == FA2_DTYPE_BF16) return by_layout<__nv_bfloat16, APPEND>(p, grid, wide, s);
+  if (dtype == FA2_DTYPE_FP16) return by_layout<__half, APPEND>(p, grid, wide, s);
+  if constexpr (!APPEND) return by_layout<float, APPEND>(p, grid, wide, s);
   return cudaErrorInvalidValue;
 }
 
@@ -284,35 +288,26 @@ cudaError_t by_type(const RopeParams& p, int dtype, unsigned grid, size_t smem, 
 
 cudaError_t launch_rope(RopeParams p, bool append, int dtype, bool wide, int sms, cudaStream_t s) {
   const int size = dtype == FA2_DTYPE_FP32 ? 4 : 2;
-  const int w = wide ? 16 / size : (p.interleaved ? 2 : 1);
+  const int w = wide ? rope_width(size, p.interleaved) : (p.interleaved ? 2 : 1);
   const int pair = p.interleaved ? 1 : 2;
-  const int rot_units = p.r / (w * pair);
-  p.units = rot_units + ((p.d - p.r) / w + pair - 1) / pair;
-  // Head rows of a block: four units a thread (the loads of one thread in
-  // flight together) when that leaves four blocks an SM, else one.
-  const long long all = p.total_tokens * p.total_rows * p.units;
-  int items = 4;
-  if (all < 4ll * sms * 4 * fa2dev::kRopeThreads) items = 1;
-  int rows_per_block = items * fa2dev::kRopeThreads / p.units;
-  if (rows_per_block < 1) rows_per_block = 1;
-  p.rows = p.total_rows < 8 ? p.total_rows : 8;
-  if (items == 1 && p.rows > rows_per_block) p.rows = rows_per_block;
-  p.tokens = rows_per_block / p.rows;
+  p.units = p.r / (w * pair) + ((p.d - p.r) / w + pair - 1) / pair;
+  p.tokens = fa2dev::kRopeThreads / p.units;
   if (p.tokens < 1) p.tokens = 1;
-  if (p.tokens > fa2dev::kRopeMaxTokens) p.tokens = fa2dev::kRopeMaxTokens;
-  // the sines of a block stay within the default 48 KB of shared memory
-  const int half = p.r / 2;
-  while (p.tokens > 1 && static_cast<size_t>(p.tokens) * half * sizeof(float2) > (32u << 10)) p.tokens /= 2;
-  p.row_tiles = (p.total_rows + p.rows - 1) / p.rows;
-  const long long blocks = (p.total_tokens + p.tokens - 1) / p.tokens * p.row_tiles;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  p.div_row_tiles = make_fast_div(p.row_tiles);
-  p.div_rows = make_fast_div(p.rows);
+  const long long tiles = (p.total_tokens + p.tokens - 1) / p.tokens;
+  if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
+  // Heads of a block: all of them, so that the sines are computed once, unless
+  // that leaves fewer than four blocks an SM; then as few as it takes, at least
+  // one unrolled step.
+  long long chunks = (4ll * sms + tiles - 1) / tiles;
+  const long long most = (p.total_rows + fa2dev::kRopeUnroll - 1) / fa2dev::kRopeUnroll;
+  if (chunks > most) chunks = most;
+  if (chunks > 65535) chunks = 65535;
+  p.rows = static_cast<int>((p.total_rows + chunks - 1) / chunks);
+  chunks = (p.total_rows + p.rows - 1) / p.rows;
   p.div_units = make_fast_div(p.units);
-  p.div_half = make_fast_div(half > 0 ? half : 1);
-  const size_t smem = static_cast<size_t>(p.tokens) * half * sizeof(float2);
-  return append ? by_type<true>(p, dtype, static_cast<unsigned>(blocks), smem, items, wide, s)
-                : by_type<false>(p, dtype, static_cast<unsigned>(blocks), smem, items, wide, s);
+  p.div_n = make_fast_div(static_cast<int>(p.N > 0 ? p.N : 1));
+  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(chunks));
+  return append ? by_type<true>(p, dtype, grid, wide, s) : by_type<false>(p, dtype, grid, wide, s);
 }
 
 }  // namespace fa2host

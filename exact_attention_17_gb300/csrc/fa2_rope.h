@@ -8,8 +8,6 @@
 
 namespace fa2dev {
 
-constexpr int kRopeMaxTokens = 128;   // tokens per block
-
 struct RopeParams {
   // rotary alone: x and y [B, H, N, d] with element strides
   const void* x;
@@ -37,16 +35,22 @@ struct RopeParams {
   long long total_tokens;
   int total_rows;          // head rows of a token
   // set by the launch
-  int tokens, rows, row_tiles, units;
-  FastDiv div_row_tiles, div_rows, div_units, div_half;
+  int tokens, rows;        // of a block
+  int units;               // of a head row
+  FastDiv div_units, div_n;
 };
 
 }  // namespace fa2dev
 
 namespace fa2host {
 
-// dtype: FA2_DTYPE_*; wide: every row start and stride allows 16-byte vectors
-// and the rotated columns (their half, unless interleaved) fill them.
+// Elements of a vector: four pairs to a unit (interleaved 16-bit: 16 bytes; in
+// halves 8 bytes twice; fp32: two pairs in 16 bytes, or four in 16 bytes twice).
+constexpr int rope_width(int elem_bytes, bool interleaved) { return interleaved && elem_bytes == 2 ? 8 : 4; }
+
+// dtype: FA2_DTYPE_*; wide: every row start and stride allows vectors of
+// rope_width elements, and the rotated columns (their half, unless
+// interleaved) fill them.
 cudaError_t launch_rope(fa2dev::RopeParams p, bool append, int dtype, bool wide, int sms, cudaStream_t s);
 
 }  // namespace fa2host

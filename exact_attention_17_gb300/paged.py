@@ -24,73 +24,124 @@ workspaces that a call makes belong to the stream that it runs on.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
 
 import exact_attention_17_gb300 as fa2
 
-_NULL_CONTEXT = contextlib.nullcontext()
+_LL2, _LL3 = ctypes.c_longlong * 2, ctypes.c_longlong * 3
+
+# Filled by the first call: importing the package does not import torch.
+torch = None
+_lib = None
+_codes = None          # element type -> FA2_DTYPE_*
+_raw_stream = None     # device index -> handle of the current stream
 
 
-def _on_stream(stream, device):
-    """(raw handle, context in which tensors are allocated on that stream)."""
-    import torch
+def _load():
+    global torch, _lib, _codes, _raw_stream
+    import torch as t
 
-    current = torch.cuda.current_stream(device)
-    if stream is None:
-        return current.cuda_stream, _NULL_CONTEXT
-    handle = getattr(stream, "cuda_stream", stream)
-    if handle == current.cuda_stream:
-        return handle, _NULL_CONTEXT
-    if handle == 0:
-        return handle, torch.cuda.stream(torch.cuda.default_stream(device))
-    return handle, torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device))
+    _lib = fa2.library()
+    _codes = fa2._dtype_codes()
+    _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None) or (lambda i: t.cuda.current_stream(i).cuda_stream)
+    torch = t
+
+
+class _Call:
+    """The device and the stream of a call.
+
+    ``handle`` is the raw stream.  Within the context the device is current, and
+    what torch allocates belongs to that stream (memory that its earlier work
+    still uses is not handed out to it, nor its own to others while it runs).
+    """
+
+    __slots__ = ("handle", "contexts")
+
+    def __init__(self, device, stream):
+        index = device.index
+        self.contexts = ()
+        if stream is None:
+            self.handle = _raw_stream(index)
+        else:
+            self.handle = handle = getattr(stream, "cuda_stream", stream)
+            if handle != _raw_stream(index):
+                if handle == 0:
+                    on = torch.cuda.default_stream(device)
+                else:
+                    on = torch.cuda.ExternalStream(handle, device=device)
+                self.contexts = (torch.cuda.stream(on),)
+        if torch.cuda.current_device() != index:
+            self.contexts = (torch.cuda.device(device),) + self.contexts
+
+    def __enter__(self):
+        for c in self.contexts:
+            c.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
+
+
+def _fail(rc, where):
+    raise fa2.FA2Error(rc, where)
 
 
 def _ints(name, t, shape, device):
     """An int32 CUDA tensor of `shape`, rows dense."""
-    import torch
-
-    if (t.dtype is not torch.int32 or tuple(t.shape) != shape or t.device != device
-            or (shape and shape[-1] > 1 and t.stride(-1) != 1)):
-        raise ValueError(f"{name} must be a dense int32 tensor of shape {shape} on {device}")
+    if t.dtype is not torch.int32 or t.shape != shape or t.device != device or (shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be a dense int32 tensor of shape {tuple(shape)} on {device}")
 
 
 def _rows(name, t, shape, dtype, device):
-    """A [T, H, d] tensor of the cache's type, last dimension dense."""
-    if t.dtype is not dtype or tuple(t.shape) != shape or t.device != device or t.stride(-1) != 1:
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {shape} on {device} with a dense last dimension")
+    """A [T, H, d] tensor of the cache's type, last dimension dense; its strides."""
+    strides = t.stride()
+    if t.dtype is not dtype or t.shape != shape or t.device != device or strides[-1] != 1:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device} with a dense last dimension")
+    return strides
 
 
-def _cache_args(k_pages, v_pages, page_table, kv_lens):
-    import torch
-
-    dtype, device = k_pages.dtype, k_pages.device
+def _cache_args(k_pages, v_pages, page_table, kv_lens, device, dtype):
     if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise ValueError("k_pages must be bf16 or fp16")
-    if not k_pages.is_cuda or k_pages.dim() != 4 or k_pages.stride(3) != 1:
+    shape, strides = k_pages.shape, k_pages.stride()
+    if not k_pages.is_cuda or len(shape) != 4 or strides[3] != 1:
         raise ValueError("k_pages must be a 4-D CUDA tensor with a dense last dimension")
-    if (v_pages.dtype is not dtype or v_pages.shape != k_pages.shape or v_pages.stride() != k_pages.stride()
-            or v_pages.device != device):
+    if v_pages.dtype is not dtype or v_pages.shape != shape or v_pages.stride() != strides or v_pages.device != device:
         raise ValueError("v_pages must match k_pages in type, shape, strides and device")
-    if page_table.dim() != 2:
+    table_shape = page_table.shape
+    if len(table_shape) != 2:
         raise ValueError("page_table must be [B, M]")
-    B, M = page_table.shape
-    _ints("page_table", page_table, (B, M), device)
+    B, M = table_shape
+    _ints("page_table", page_table, table_shape, device)
     _ints("kv_lens", kv_lens, (B,), device)
-    P, Hkv, S, d = k_pages.shape
-    ps, hs, ss, _ = k_pages.stride()
-    return fa2.PagedCacheArgs(k_pages.data_ptr(), v_pages.data_ptr(), P, Hkv, S, d, ps, hs, ss,
-                              fa2._dtype_codes()[dtype], page_table.data_ptr(), page_table.stride(0), M, B,
-                              kv_lens.data_ptr())
+    return fa2.PagedCacheArgs(k_pages.data_ptr(), v_pages.data_ptr(), shape[0], shape[1], shape[2], shape[3],
+                              strides[0], strides[1], strides[2], _codes[dtype], page_table.data_ptr(),
+                              page_table.stride(0), M, B, kv_lens.data_ptr())
 
 
-def _check_offsets(cu_q, B, T, device):
+def _offsets(cu_q, B, T, device):
+    """Pointer of cu_q, or None."""
     if cu_q is not None:
         _ints("cu_q", cu_q, (B + 1,), device)
-    elif T != B:
+        return cu_q.data_ptr()
+    if T != B:
         raise ValueError(f"without cu_q there is one new token for each of the {B} sequences, not {T}")
+    return None
+
+
+@functools.lru_cache(maxsize=1024)
+def _paged_workspace_bytes(device_index, *sizes):
+    with torch.cuda.device(device_index):
+        return _lib.fa2_forward_paged_workspace_bytes(*sizes)
+
+
+@functools.lru_cache(maxsize=None)
+def _default_scale(d):
+    """1/sqrt(d) rounded once to float32."""
+    return ctypes.c_float(1.0 / math.sqrt(d)).value
 
 
 def forward_paged(q, k_pages, v_pages, page_table, kv_lens, cu_q=None, causal: bool = True,
@@ -106,73 +157,62 @@ def forward_paged(q, k_pages, v_pages, page_table, kv_lens, cu_q=None, causal: b
     workspace (a uint8 CUDA tensor) is allocated here unless given; calls that
     may overlap need one each.
     """
-    import torch
-
-    args = _cache_args(k_pages, v_pages, page_table, kv_lens)
+    if torch is None:
+        _load()
     dtype, device = k_pages.dtype, k_pages.device
-    if q.dim() != 3 or q.shape[2] != args.d:
+    args = _cache_args(k_pages, v_pages, page_table, kv_lens, device, dtype)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != args.d:
         raise ValueError(f"q must be [T, Hq, {args.d}]")
-    T, Hq, d = q.shape
-    _rows("q", q, (T, Hq, d), dtype, device)
+    T, Hq, d = shape
+    strides = _rows("q", q, shape, dtype, device)
     if Hq % args.kv_heads != 0:
         raise ValueError(f"{Hq} query heads are no multiple of {args.kv_heads} key/value heads")
-    _check_offsets(cu_q, args.B, T, device)
-    out_dtype = dtype if out_dtype is None else out_dtype
-    if out_dtype is not torch.float32 and out_dtype is not dtype:
+    offsets = _offsets(cu_q, args.B, T, device)
+    if out_dtype is None:
+        out_dtype = dtype
+    elif out_dtype is not torch.float32 and out_dtype is not dtype:
         raise ValueError("out_dtype must be fp32 or the cache's type")
     if scale is None:
         scale = _default_scale(d)
-    with fa2._on_device(device):
-        handle, here = _on_stream(stream, device)
-        need = fa2.library().fa2_forward_paged_workspace_bytes(args.B, T, Hq, args.kv_heads, d, cu_q is not None)
-        with here:
-            if out is None:
-                out = torch.empty((T, Hq, d), dtype=out_dtype, device=device)
-            if lse is None:
-                lse = torch.empty((T, Hq), dtype=torch.float32, device=device)
-            if workspace is None:
-                workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
-        if out.dtype is not out_dtype or out.shape != (T, Hq, d) or not out.is_contiguous() or out.device != device:
+    with _Call(device, stream) as handle:
+        if out is None:
+            out = torch.empty(shape, dtype=out_dtype, device=device)
+        elif out.dtype is not out_dtype or out.shape != shape or not out.is_contiguous() or out.device != device:
             raise ValueError(f"out must be a contiguous {out_dtype} tensor of shape {(T, Hq, d)} on {device}")
-        if (lse.dtype is not torch.float32 or lse.shape != (T, Hq) or not lse.is_contiguous()
-                or lse.device != device):
+        if lse is None:
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=device)
+        elif (lse.dtype is not torch.float32 or lse.shape != (T, Hq) or not lse.is_contiguous()
+              or lse.device != device):
             raise ValueError(f"lse must be a contiguous fp32 tensor of shape {(T, Hq)} on {device}")
-        if not workspace.is_contiguous() or workspace.device != device:
-            raise ValueError(f"workspace must be a contiguous tensor on {device}")
-        rc = fa2.library().fa2_forward_paged(
-            ctypes.byref(args), q.data_ptr(), q.stride(0), q.stride(1), out.data_ptr(), lse.data_ptr(),
-            None if cu_q is None else cu_q.data_ptr(), T, Hq, int(bool(causal)), float(scale),
-            fa2._dtype_codes()[out_dtype], workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle)
-    if rc != fa2.FA2_OK:
-        raise fa2.FA2Error(rc, "fa2_forward_paged")
+        if workspace is None:
+            size = _paged_workspace_bytes(device.index, args.B, T, Hq, args.kv_heads, d, offsets is not None)
+            workspace = torch.empty(max(size, 1), dtype=torch.uint8, device=device)
+        else:
+            size = _workspace_size(workspace, device)
+        rc = _lib.fa2_forward_paged(ctypes.byref(args), q.data_ptr(), strides[0], strides[1], out.data_ptr(),
+                                    lse.data_ptr(), offsets, T, Hq, 1 if causal else 0, scale, _codes[out_dtype],
+                                    workspace.data_ptr(), size, handle)
+    if rc:
+        _fail(rc, "fa2_forward_paged")
     return out, lse
 
 
-_scales = {}
-
-
-def _default_scale(d):
-    """1/sqrt(d) rounded once to float32."""
-    if d not in _scales:
-        _scales[d] = ctypes.c_float(1.0 / math.sqrt(d)).value
-    return _scales[d]
+def _workspace_size(workspace, device):
+    if not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace.numel() * workspace.element_size()
 
 
 def _inv_freq_args(inv_freq, device, d):
-    import torch
-
     if inv_freq is None:
         return None, 0
-    if (inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous()
-            or inv_freq.device != device):
+    shape = inv_freq.shape
+    if inv_freq.dtype is not torch.float64 or len(shape) != 1 or not inv_freq.is_contiguous() or inv_freq.device != device:
         raise ValueError(f"inv_freq must be a contiguous 1-D float64 tensor on {device}")
-    if 2 * inv_freq.numel() > d:
+    if 2 * shape[0] > d:
         raise ValueError(f"inv_freq holds more than the {d // 2} pairs of a head")
-    return inv_freq.data_ptr(), 2 * inv_freq.numel()
-
-
-def _strides(t):
-    return (ctypes.c_longlong * 2)(t.stride(0), t.stride(1))
+    return inv_freq.data_ptr(), 2 * shape[0]
 
 
 def append_paged(k, v, k_pages, v_pages, page_table, kv_lens, cu_q=None, q=None, q_out=None, inv_freq=None,
@@ -185,40 +225,39 @@ def append_paged(k, v, k_pages, v_pages, page_table, kv_lens, cu_q=None, q=None,
     queries are rotated in the same launch and returned (``q_out``; pass
     ``q_out=q`` to rotate in place).  Rows behind cu_q[B] are not touched.
     """
-    import torch
-
-    args = _cache_args(k_pages, v_pages, page_table, kv_lens)
+    if torch is None:
+        _load()
     dtype, device = k_pages.dtype, k_pages.device
+    args = _cache_args(k_pages, v_pages, page_table, kv_lens, device, dtype)
+    d = args.d
     if k.dim() != 3:
-        raise ValueError(f"k must be [T, {args.kv_heads}, {args.d}]")
-    T, shape = k.shape[0], (k.shape[0], args.kv_heads, args.d)
-    _rows("k", k, shape, dtype, device)
-    _rows("v", v, shape, dtype, device)
-    _check_offsets(cu_q, args.B, T, device)
-    Hq = 0
-    if q is not None:
-        if q.dim() != 3:
-            raise ValueError(f"q must be [{T}, Hq, {args.d}]")
-        Hq = q.shape[1]
-        _rows("q", q, (T, Hq, args.d), dtype, device)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    freq, rotary_dim = _inv_freq_args(inv_freq, device, args.d)
-    with fa2._on_device(device):
-        handle, here = _on_stream(stream, device)
-        if q is not None and q_out is None:
-            with here:
-                q_out = torch.empty((T, Hq, args.d), dtype=dtype, device=device)
-        if q is not None:
-            _rows("q_out", q_out, (T, Hq, args.d), dtype, device)
-        rc = fa2.library().fa2_append_paged(
-            ctypes.byref(args), k.data_ptr(), _strides(k), v.data_ptr(), _strides(v),
-            None if q is None else q.data_ptr(), None if q is None else _strides(q),
-            None if q is None else q_out.data_ptr(), None if q is None else _strides(q_out), Hq,
-            None if cu_q is None else cu_q.data_ptr(), T, freq, rotary_dim, int(bool(interleaved)), float(mscale),
-            handle)
-    if rc != fa2.FA2_OK:
-        raise fa2.FA2Error(rc, "fa2_append_paged")
+        raise ValueError(f"k must be [T, {args.kv_heads}, {d}]")
+    T = k.shape[0]
+    shape = (T, args.kv_heads, d)
+    ks = _rows("k", k, shape, dtype, device)
+    vs = _rows("v", v, shape, dtype, device)
+    offsets = _offsets(cu_q, args.B, T, device)
+    freq, rotary_dim = _inv_freq_args(inv_freq, device, d)
+    with _Call(device, stream) as handle:
+        if q is None:
+            if q_out is not None:
+                raise ValueError("q_out without q")
+            Hq, queries, queries_out, qs, qos = 0, None, None, None, None
+        else:
+            if q.dim() != 3:
+                raise ValueError(f"q must be [{T}, Hq, {d}]")
+            Hq = q.shape[1]
+            st = _rows("q", q, (T, Hq, d), dtype, device)
+            if q_out is None:
+                q_out = torch.empty((T, Hq, d), dtype=dtype, device=device)
+            so = _rows("q_out", q_out, (T, Hq, d), dtype, device)
+            queries, queries_out = q.data_ptr(), q_out.data_ptr()
+            qs, qos = _LL2(st[0], st[1]), _LL2(so[0], so[1])
+        rc = _lib.fa2_append_paged(ctypes.byref(args), k.data_ptr(), _LL2(ks[0], ks[1]), v.data_ptr(),
+                                   _LL2(vs[0], vs[1]), queries, qs, queries_out, qos, Hq, offsets, T, freq, rotary_dim,
+                                   1 if interleaved else 0, mscale, handle)
+    if rc:
+        _fail(rc, "fa2_append_paged")
     return q_out
 
 
@@ -237,8 +276,8 @@ def rope_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: str | None = 
       divided by the factor, linear in the pair's number between; usually with
       ``mscale = 0.1 ln(factor) + 1``.
     """
-    import torch
-
+    if torch is None:
+        _load()
     r = rotary_dim
     if r < 2 or r % 2 != 0:
         raise ValueError("rotary_dim must be even and at least 2")
@@ -265,39 +304,38 @@ def rope_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: str | None = 
 
 
 def _rope(x, positions, inv_freq, interleaved, mscale, out, stream, transposed):
-    import torch
-
-    codes = fa2._dtype_codes()
-    if x.dtype not in codes or not x.is_cuda or x.dim() not in (3, 4) or x.stride(-1) != 1:
+    if torch is None:
+        _load()
+    dtype, device, shape, xs = x.dtype, x.device, x.shape, x.stride()
+    code = _codes.get(dtype)
+    dim = len(shape)
+    if code is None or not x.is_cuda or (dim != 4 and dim != 3) or xs[-1] != 1:
         raise ValueError("x must be a bf16, fp16 or fp32 CUDA tensor [T, H, d] or [B, H, N, d], last dimension dense")
-    device = x.device
-    if x.dim() == 3:     # [T, H, d]: one batch, tokens outside the heads
-        B, N, H, d = 1, *x.shape
+    if dim == 3:     # [T, H, d]: one batch, tokens outside the heads
+        N, H, d = shape
+        B = 1
     else:
-        B, H, N, d = x.shape
-    if positions.dtype not in (torch.int32, torch.int64) or positions.device != device:
+        B, H, N, d = shape
+    ps = positions.shape
+    if positions.device != device or (positions.dtype is not torch.int32 and positions.dtype is not torch.int64):
         raise ValueError(f"positions must be int32 or int64 on {device}")
-    if tuple(positions.shape) not in ((N,), (B, N)) or (N > 1 and positions.stride(-1) != 1):
-        raise ValueError(f"positions must be a dense [{N}]" + (f" or [{B}, {N}]" if x.dim() == 4 else ""))
+    if (ps != (N,) and ps != (B, N)) or (N > 1 and positions.stride(-1) != 1):
+        raise ValueError(f"positions must be a dense [{N}]" + (f" or [{B}, {N}]" if dim == 4 else ""))
     freq, rotary_dim = _inv_freq_args(inv_freq, device, d)
-    with fa2._on_device(device):
-        handle, here = _on_stream(stream, device)
+    with _Call(device, stream) as handle:
         if out is None:
-            with here:
-                out = torch.empty(x.shape, dtype=x.dtype, device=device)
-        if out.dtype is not x.dtype or out.shape != x.shape or out.device != device or out.stride(-1) != 1:
-            raise ValueError(f"out must be a {x.dtype} tensor of shape {tuple(x.shape)} on {device}, last dimension dense")
-
-        def strides(t):   # {batch, head, token}
-            s = (0, t.stride(1), t.stride(0)) if t.dim() == 3 else t.stride()[:3]
-            return (ctypes.c_longlong * 3)(*s)
-
-        rc = fa2.library().fa2_rope(
-            x.data_ptr(), strides(x), out.data_ptr(), strides(out), B, H, N, d, positions.data_ptr(),
-            int(positions.dtype is torch.int64), positions.stride(0) if positions.dim() == 2 else 0, freq, rotary_dim,
-            int(bool(interleaved)), float(mscale), int(transposed), codes[x.dtype], handle)
-    if rc != fa2.FA2_OK:
-        raise fa2.FA2Error(rc, "fa2_rope")
+            out = torch.empty(shape, dtype=dtype, device=device)
+        ys = out.stride()
+        if out.dtype is not dtype or out.shape != shape or out.device != device or ys[-1] != 1:
+            raise ValueError(f"out must be a {dtype} tensor of shape {tuple(shape)} on {device}, last dimension dense")
+        # {batch, head, token}
+        xs, ys = (_LL3(xs[0], xs[1], xs[2]), _LL3(ys[0], ys[1], ys[2])) if dim == 4 else (
+            _LL3(0, xs[1], xs[0]), _LL3(0, ys[1], ys[0]))
+        rc = _lib.fa2_rope(x.data_ptr(), xs, out.data_ptr(), ys, B, H, N, d, positions.data_ptr(),
+                           1 if positions.dtype is torch.int64 else 0, positions.stride(0) if len(ps) == 2 else 0, freq,
+                           rotary_dim, 1 if interleaved else 0, mscale, transposed, code, handle)
+    if rc:
+        _fail(rc, "fa2_rope")
     return out
 
 
@@ -311,80 +349,85 @@ def rope(x, positions, inv_freq, interleaved: bool = False, mscale: float = 1.0,
     (``rope_inv_freq``), times ``mscale``; the others are copied.  ``out=x``
     works in place.
     """
-    return _rope(x, positions, inv_freq, interleaved, mscale, out, stream, False)
+    return _rope(x, positions, inv_freq, interleaved, mscale, out, stream, 0)
 
 
 def rope_backward(do, positions, inv_freq, interleaved: bool = False, mscale: float = 1.0, out=None, stream=None):
     """Gradient of ``rope`` with respect to x for the upstream gradient ``do``
     (the transposed rotation); arguments as ``rope``."""
-    return _rope(do, positions, inv_freq, interleaved, mscale, out, stream, True)
+    return _rope(do, positions, inv_freq, interleaved, mscale, out, stream, 1)
 
 
 def _tables(page_table, lens, refs, page_size):
-    device = page_table.device
-    if page_table.dim() != 2 or not page_table.is_cuda or refs.dim() != 1:
+    if torch is None:
+        _load()
+    device, shape, pages = page_table.device, page_table.shape, refs.shape
+    if len(shape) != 2 or not page_table.is_cuda or len(pages) != 1:
         raise ValueError("page_table must be a CUDA tensor [B, M], refs [P]")
-    B, M = page_table.shape
-    _ints("page_table", page_table, (B, M), device)
+    B, M = shape
+    _ints("page_table", page_table, shape, device)
     _ints("lens", lens, (B,), device)
-    _ints("refs", refs, (refs.shape[0],), device)
+    _ints("refs", refs, pages, device)
     return fa2.PageTablesArgs(page_table.data_ptr(), page_table.stride(0), M, B, lens.data_ptr(), refs.data_ptr(),
-                              refs.shape[0], page_size), device
+                              pages[0], page_size), device
 
 
 def _pools(pools):
-    """Page data as an array of planes: a tensor [..., P, Hkv, S, d], or a list of such tensors."""
-    import torch
+    """Page data as an array of planes: a tensor [..., P, Hkv, S, d], or a list of such tensors.
 
-    tensors = [pools] if torch.is_tensor(pools) else list(pools)
-    pointers, shape, stride, device = [], None, None, None
+    (arguments of the library, the array they point to, slots per page, device)
+    """
+    if torch is None:
+        _load()
+    tensors = (pools,) if torch.is_tensor(pools) else tuple(pools)
+    if not tensors:
+        raise ValueError("pools must hold at least one tensor")
+    first, pointers = tensors[0], []
+    device, dtype, size = first.device, first.dtype, first.element_size()
     for t in tensors:
-        if not t.is_cuda or t.dim() < 4:
+        shape, strides = t.shape, t.stride()
+        if not t.is_cuda or len(shape) < 4:
             raise ValueError("pools must be CUDA tensors [..., P, Hkv, S, d]")
-        page = sorted((st, n) for st, n in zip(t.stride()[-3:], t.shape[-3:]) if n > 1)
-        dense = 1
-        for st, n in page:
-            if st != dense:
+        if t is not first and (shape[-4:] != first.shape[-4:] or strides[-4:] != first.stride()[-4:]
+                               or t.dtype is not dtype or t.device != device):
+            raise ValueError("all pools must have the same pages, strides, type and device")
+        planes = [t.data_ptr()]
+        for n, st in zip(shape[:-4], strides[:-4]):   # the leading dimensions, outermost first
+            planes = [p + i * st * size for p in planes for i in range(n)]
+        pointers += planes
+    P, Hkv, S, d = first.shape[-4:]
+    strides = first.stride()
+    if strides[-1] != 1 or strides[-2] != d or strides[-3] != S * d:
+        dense = 1   # in another order, perhaps
+        for st, n in sorted(zip(strides[-3:], (Hkv, S, d))):
+            if n > 1 and st != dense:
                 raise ValueError("the elements of a page must be dense")
             dense *= n
-        this = (tuple(t.shape[-4:]), t.stride()[-4:], t.dtype, t.device)
-        if shape is None:
-            shape, stride, device = this, t.stride(-4) * t.element_size(), t.device
-        if this != shape:
-            raise ValueError("all pools must have the same pages, strides, type and device")
-        planes = [t] if t.dim() == 4 else t.flatten(0, -5).unbind(0) if t.dim() == 5 else [
-            p for p in _leading(t)]
-        pointers += [p.data_ptr() for p in planes]
-    if shape is None:
-        raise ValueError("pools must hold at least one tensor")
-    (P, Hkv, S, d), size = shape[0], tensors[0].element_size()
     array = (ctypes.c_void_p * max(len(pointers), 1))(*pointers)
-    args = fa2.PagePoolsArgs(ctypes.cast(array, ctypes.c_void_p), len(pointers), P, stride, Hkv * S * d * size)
+    args = fa2.PagePoolsArgs(ctypes.addressof(array), len(pointers), P, strides[-4] * size, Hkv * S * d * size)
     return args, array, S, device
 
 
-def _leading(t):
-    """The [P, Hkv, S, d] planes of a tensor with more leading dimensions."""
-    if t.dim() == 4:
-        yield t
-    else:
-        for part in t.unbind(0):
-            yield from _leading(part)
+@functools.lru_cache(maxsize=1024)
+def _pages_workspace_bytes(num_pages, n):
+    return max(_lib.fa2_pages_workspace_bytes(num_pages, n), 1)
 
 
 def _workspace(num_pages, n, given, device):
-    import torch
-
-    need = fa2.library().fa2_pages_workspace_bytes(num_pages, n)
+    """(workspace, bytes)"""
     if given is None:
-        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
-    if not given.is_contiguous() or given.device != device:
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return given
+        size = _pages_workspace_bytes(num_pages, n)
+        return torch.empty(size, dtype=torch.uint8, device=device), size
+    return given, _workspace_size(given, device)
 
 
-def _size(workspace):
-    return workspace.numel() * workspace.element_size()
+def _list(name, t, device):
+    """Length of a 1-D int32 tensor."""
+    shape = t.shape
+    if len(shape) != 1:
+        raise ValueError(f"{name} must be 1-D")
+    _ints(name, t, shape, device)
+    return shape[0]
 
 
 def pages_reserve(page_table, lens, refs, add, page_size: int, workspace=None, stream=None):
@@ -395,27 +438,16 @@ def pages_reserve(page_table, lens, refs, add, page_size: int, workspace=None, s
     tensor [1]: 0, or the number of pages that lack, or -1 where a table row is
     too short -- then nothing has changed.
     """
-    import torch
-
     args, device = _tables(page_table, lens, refs, page_size)
     _ints("add", add, (args.B,), device)
-    with fa2._on_device(device):
-        handle, here = _on_stream(stream, device)
-        with here:
-            workspace = _workspace(args.num_pages, 0, workspace, device)
-            missing = torch.empty(1, dtype=torch.int32, device=device)
-        rc = fa2.library().fa2_pages_reserve(ctypes.byref(args), add.data_ptr(), missing.data_ptr(),
-                                             workspace.data_ptr(), _size(workspace), handle)
-    if rc != fa2.FA2_OK:
-        raise fa2.FA2Error(rc, "fa2_pages_reserve")
+    with _Call(device, stream) as handle:
+        workspace, size = _workspace(args.num_pages, 0, workspace, device)
+        missing = torch.empty(1, dtype=torch.int32, device=device)
+        rc = _lib.fa2_pages_reserve(ctypes.byref(args), add.data_ptr(), missing.data_ptr(), workspace.data_ptr(), size,
+                                    handle)
+    if rc:
+        _fail(rc, "fa2_pages_reserve")
     return missing
-
-
-def _pair_lists(src, dst, device):
-    n = src.shape[0] if src.dim() == 1 else -1
-    _ints("src", src, (n,), device)
-    _ints("dst", dst, (n,), device)
-    return n
 
 
 def pages_fork(page_table, lens, refs, src, dst, pools, workspace=None, stream=None):
@@ -425,35 +457,30 @@ def pages_fork(page_table, lens, refs, src, dst, pools, workspace=None, stream=N
     ``pools`` (a tensor [..., P, Hkv, S, d] or a list of them: all the layers' K
     and V).  Returns the pages that lack as ``pages_reserve`` does.
     """
-    import torch
-
     data, array, S, pool_device = _pools(pools)
     args, device = _tables(page_table, lens, refs, S)
     if pool_device != device or data.num_pages != args.num_pages:
         raise ValueError("pools must lie on the tables' device and hold len(refs) pages")
-    n = _pair_lists(src, dst, device)
-    with fa2._on_device(device):
-        handle, here = _on_stream(stream, device)
-        with here:
-            workspace = _workspace(args.num_pages, n, workspace, device)
-            missing = torch.empty(1, dtype=torch.int32, device=device)
-        rc = fa2.library().fa2_pages_fork(ctypes.byref(args), ctypes.byref(data), src.data_ptr(), dst.data_ptr(), n,
-                                          missing.data_ptr(), workspace.data_ptr(), _size(workspace), handle)
-    if rc != fa2.FA2_OK:
-        raise fa2.FA2Error(rc, "fa2_pages_fork")
+    n = _list("src", src, device)
+    _ints("dst", dst, (n,), device)
+    with _Call(device, stream) as handle:
+        workspace, size = _workspace(args.num_pages, n, workspace, device)
+        missing = torch.empty(1, dtype=torch.int32, device=device)
+        rc = _lib.fa2_pages_fork(ctypes.byref(args), ctypes.byref(data), src.data_ptr(), dst.data_ptr(), n,
+                                 missing.data_ptr(), workspace.data_ptr(), size, handle)
+    if rc:
+        _fail(rc, "fa2_pages_fork")
     return missing
 
 
-def pages_free(page_table, lens, refs, seqs, page_size: int = 16, stream=None):
+def pages_free(page_table, lens, refs, seqs, stream=None):
     """Empty the sequences ``seqs`` int32 [n]; pages nobody names any more become free (fa2_pages_free)."""
-    args, device = _tables(page_table, lens, refs, page_size)
-    n = seqs.shape[0] if seqs.dim() == 1 else -1
-    _ints("seqs", seqs, (n,), device)
-    with fa2._on_device(device):
-        handle, _ = _on_stream(stream, device)
-        rc = fa2.library().fa2_pages_free(ctypes.byref(args), seqs.data_ptr(), n, handle)
-    if rc != fa2.FA2_OK:
-        raise fa2.FA2Error(rc, "fa2_pages_free")
+    args, device = _tables(page_table, lens, refs, 16)   # (the slots per page play no part)
+    n = _list("seqs", seqs, device)
+    with _Call(device, stream) as handle:
+        rc = _lib.fa2_pages_free(ctypes.byref(args), seqs.data_ptr(), n, handle)
+    if rc:
+        _fail(rc, "fa2_pages_free")
 
 
 def pages_compact(page_table, lens, refs, pools, workspace=None, stream=None):
@@ -462,21 +489,17 @@ def pages_compact(page_table, lens, refs, pools, workspace=None, stream=None):
     Page data, ``page_table`` and ``refs`` follow.  Returns int32 [P]: where
     each page went (its own number where it stayed, -1 for a free one).
     """
-    import torch
-
     data, array, S, pool_device = _pools(pools)
     args, device = _tables(page_table, lens, refs, S)
     if pool_device != device or data.num_pages != args.num_pages:
         raise ValueError("pools must lie on the tables' device and hold len(refs) pages")
-    with fa2._on_device(device):
-        handle, here = _on_stream(stream, device)
-        with here:
-            workspace = _workspace(args.num_pages, 0, workspace, device)
-            moved = torch.empty(args.num_pages, dtype=torch.int32, device=device)
-        rc = fa2.library().fa2_pages_compact(ctypes.byref(args), ctypes.byref(data), moved.data_ptr(),
-                                             workspace.data_ptr(), _size(workspace), handle)
-    if rc != fa2.FA2_OK:
-        raise fa2.FA2Error(rc, "fa2_pages_compact")
+    with _Call(device, stream) as handle:
+        workspace, size = _workspace(args.num_pages, 0, workspace, device)
+        moved = torch.empty(args.num_pages, dtype=torch.int32, device=device)
+        rc = _lib.fa2_pages_compact(ctypes.byref(args), ctypes.byref(data), moved.data_ptr(), workspace.data_ptr(),
+                                    size, handle)
+    if rc:
+        _fail(rc, "fa2_pages_compact")
     return moved
 
 
@@ -487,12 +510,11 @@ def pages_copy(pools, src, dst, workspace=None, stream=None):
     is another's destination is skipped and reported (``FA2_ERR_PAGE``).
     """
     data, array, _, device = _pools(pools)
-    n = _pair_lists(src, dst, device)
-    with fa2._on_device(device):
-        handle, here = _on_stream(stream, device)
-        with here:
-            workspace = _workspace(0, n, workspace, device)
-        rc = fa2.library().fa2_pages_copy(ctypes.byref(data), src.data_ptr(), dst.data_ptr(), n,
-                                          workspace.data_ptr(), _size(workspace), handle)
-    if rc != fa2.FA2_OK:
-        raise fa2.FA2Error(rc, "fa2_pages_copy")
+    n = _list("src", src, device)
+    _ints("dst", dst, (n,), device)
+    with _Call(device, stream) as handle:
+        workspace, size = _workspace(0, n, workspace, device)
+        rc = _lib.fa2_pages_copy(ctypes.byref(data), src.data_ptr(), dst.data_ptr(), n, workspace.data_ptr(), size,
+                                 handle)
+    if rc:
+        _fail(rc, "fa2_pages_copy")
