@@ -75,20 +75,56 @@ __device__ __forceinline__ float2 rotation(double f, long long pos, float m, boo
   return make_float2(a * mc, b * ms);
 }
 
-template <typename T> __device__ __forceinline__ float to_float(T x);
-template <> __device__ __forceinline__ float to_float(float x) { return x; }
-template <> __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <> __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
-template <typename T> __device__ __forceinline__ T from_float(float x);
-template <> __device__ __forceinline__ float from_float(float x) { return x; }
-template <> __device__ __forceinline__ __nv_bfloat16 from_float(float x) { return __float2bfloat16_rn(x); }
-template <> __device__ __forceinline__ __half from_float(float x) { return __float2half_rn(x); }
-
-// W elements moved at once (16 bytes, or one element)
+// W elements moved at once.
 template <typename T, int W>
 struct alignas(sizeof(T) * W) Vec {
   T v[W];
 };
+
+// Two neighbouring elements as fp32, and back (rounded to nearest even).
+__device__ __forceinline__ float2 widen(const float* v) { return make_float2(v[0], v[1]); }
+__device__ __forceinline__ float2 widen(const __nv_bfloat16* v) {
+  const uint32_t x = *reinterpret_cast<const uint32_t*>(v);
+  return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
+__device__ __forceinline__ float2 widen(const __half* v) { return __half22float2(*reinterpret_cast<const __half2*>(v)); }
+__device__ __forceinline__ void narrow(float* v, float x, float y) {
+  v[0] = x;
+  v[1] = y;
+}
+__device__ __forceinline__ void narrow(__nv_bfloat16* v, float x, float y) {
+  *reinterpret_cast<uint32_t*>(v) = pack_bf16x2(x, y);
+}
+__device__ __forceinline__ void narrow(__half* v, float x, float y) { *reinterpret_cast<uint32_t*>(v) = pack_f16x2(x, y); }
+__device__ __forceinline__ float widen1(float x) { return x; }
+__device__ __forceinline__ float widen1(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float widen1(__half x) { return __half2float(x); }
+__device__ __forceinline__ void narrow1(float& v, float x) { v = x; }
+__device__ __forceinline__ void narrow1(__nv_bfloat16& v, float x) { v = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void narrow1(__half& v, float x) { v = __float2half_rn(x); }
+
+// Rotates a unit: vectors a and b against each other (HALF), or a's neighbours.
+template <typename T, int W, bool HALF, int PAIRS>
+__device__ __forceinline__ void turn(Vec<T, W>& a, Vec<T, W>& b, const float2 (&w)[PAIRS]) {
+  if constexpr (!HALF) {
+#pragma unroll
+    for (int e = 0; e < PAIRS; ++e) {
+      const float2 x = widen(&a.v[2 * e]);
+      narrow(&a.v[2 * e], x.x * w[e].x - x.y * w[e].y, x.y * w[e].x + x.x * w[e].y);
+    }
+  } else if constexpr (W % 2 == 0) {
+#pragma unroll
+    for (int e = 0; e < W; e += 2) {
+      const float2 x = widen(&a.v[e]), y = widen(&b.v[e]);
+      narrow(&a.v[e], x.x * w[e].x - y.x * w[e].y, x.y * w[e + 1].x - y.y * w[e + 1].y);
+      narrow(&b.v[e], y.x * w[e].x + x.x * w[e].y, y.y * w[e + 1].x + x.y * w[e + 1].y);
+    }
+  } else {
+    const float x = widen1(a.v[0]), y = widen1(b.v[0]);
+    narrow1(a.v[0], x * w[0].x - y * w[0].y);
+    narrow1(b.v[0], y * w[0].x + x * w[0].y);
+  }
+}
 
 // Where a new token of a cache goes.
 struct RopeToken {
@@ -141,6 +177,7 @@ template <typename T, int W, bool HALF, bool APPEND>
 __global__ void __launch_bounds__(kRopeThreads, 3) fa2_rope_kernel(const __grid_constant__ RopeParams p) {
   using V = Vec<T, W>;
   constexpr int PAIRS = HALF ? W : W / 2;
+  constexpr int U = HALF && sizeof(V) == 16 ? kRopeUnroll / 2 : kRopeUnroll;   // (registers)
   __shared__ RopeToken toks[APPEND ? kRopeThreads : 1];
   const long long tok0 = static_cast<long long>(blockIdx.x) * p.tokens;
   const int n_tok = static_cast<int>(min(static_cast<long long>(p.tokens), p.total_tokens - tok0));
@@ -153,11 +190,6 @@ __global__ void __launch_bounds__(kRopeThreads, 3) fa2_rope_kernel(const __grid_
     const int k = active ? fast_div(id, p.div_units) : 0;
     const int u = active ? id - k * p.units : 0;
     const long long t = tok0 + k;
-    long long batch = 0, n = t;
-    if (!APPEND && p.N < p.total_tokens) {
-      batch = t < 0x7fffffff ? static_cast<long long>(fast_div(static_cast<int>(t), p.div_n)) : t / p.N;
-      n = t - batch * p.N;
-    }
     // columns of the unit's vectors: c and, when `two`, c + second
     const bool rotate = u < rot_units;
     int c = u * W, second = p.r / 2;
@@ -167,36 +199,12 @@ __global__ void __launch_bounds__(kRopeThreads, 3) fa2_rope_kernel(const __grid_
       second = W;
       two = c + W < p.d;
     }
-    // where row `row` of the token is read
-    auto from = [&](int row) {
-      const T* x;
-      if constexpr (APPEND) {   // the queries' heads, the keys', the values'
-        if (row < p.Hq) x = static_cast<const T*>(p.q) + t * p.q_token + row * p.q_head;
-        else if (row < p.Hq + p.Hkv) x = static_cast<const T*>(p.k) + t * p.k_token + (row - p.Hq) * p.k_head;
-        else x = static_cast<const T*>(p.v) + t * p.v_token + (row - p.Hq - p.Hkv) * p.v_head;
-      } else {
-        x = static_cast<const T*>(p.x) + batch * p.x_batch + n * p.x_token + row * p.x_head;
-      }
-      return x + c;
-    };
-    V a[kRopeUnroll], b[kRopeUnroll];
-    auto load = [&](int row) {
-#pragma unroll
-      for (int i = 0; i < kRopeUnroll; ++i) {
-        if (!active || row + i >= row1) continue;
-        const T* x = from(row + i);
-        a[i] = *reinterpret_cast<const V*>(x);
-        if (HALF && two) b[i] = *reinterpret_cast<const V*>(x + second);
-      }
-    };
-    // the first heads, the frequencies and the positions are all on their way at once
-    load(row0);
     double f[PAIRS];
     if (rotate) {
 #pragma unroll
       for (int e = 0; e < PAIRS; ++e) f[e] = p.inv_freq[HALF ? c + e : c / 2 + e];
     }
-    long long pos, slot = -1;
+    long long pos, batch = 0, n = t, slot = -1;
     bool live = active;
     if constexpr (APPEND) {
       if (base == 0) {
@@ -207,51 +215,82 @@ __global__ void __launch_bounds__(kRopeThreads, 3) fa2_rope_kernel(const __grid_
       slot = toks[k].dst;
       live = active && toks[k].live;
     } else {
+      if (p.N < p.total_tokens) {
+        batch = t < 0x7fffffff ? static_cast<long long>(fast_div(static_cast<int>(t), p.div_n)) : t / p.N;
+        n = t - batch * p.N;
+      }
       const long long at = batch * p.pos_batch + n;
       pos = p.pos64 ? static_cast<const long long*>(p.positions)[at] : static_cast<const int*>(p.positions)[at];
     }
     if (!live) continue;   // (no barrier follows but in rows of more than 256 units, which are of one token)
     float2 w[PAIRS];
-    if (rotate) {
-#pragma unroll
-      for (int e = 0; e < PAIRS; ++e) w[e] = rotation(f[e], pos, p.mscale, p.transposed != 0);
-    }
-    for (int row = row0;;) {
-#pragma unroll
-      for (int i = 0; i < kRopeUnroll; ++i) {
-        const int r = row + i;
-        if (r >= row1) continue;
-        T* y;
-        bool turn = rotate;
-        if constexpr (APPEND) {
-          if (r < p.Hq) {
-            y = static_cast<T*>(p.q_out) + t * p.qo_token + r * p.qo_head;
-          } else {
-            if (slot < 0) continue;
-            const bool value = r >= p.Hq + p.Hkv;
-            y = static_cast<T*>(value ? p.v_pages : p.k_pages) + slot + (r - p.Hq - (value ? p.Hkv : 0)) * p.page_head;
-            turn = rotate && !value;
-          }
-        } else {
-          y = static_cast<T*>(p.y) + batch * p.y_batch + n * p.y_token + r * p.y_head;
-        }
-        y += c;
-        if (turn) {
-#pragma unroll
-          for (int e = 0; e < PAIRS; ++e) {
-            T& lo = HALF ? a[i].v[e] : a[i].v[2 * e];
-            T& hi = HALF ? b[i].v[e] : a[i].v[2 * e + 1];
-            const float x0 = to_float(lo), x1 = to_float(hi);
-            lo = from_float<T>(x0 * w[e].x - x1 * w[e].y);
-            hi = from_float<T>(x1 * w[e].x + x0 * w[e].y);
-          }
-        }
-        *reinterpret_cast<V*>(y) = a[i];
-        if (HALF && two) *reinterpret_cast<V*>(y + second) = b[i];
+    // the queries' heads, the keys' and the values' of a new token, or all heads of one array
+#pragma unroll 1
+    for (int part = 0; part < (APPEND ? 3 : 1); ++part) {
+      const T* x;
+      T* y;
+      long long xs, ys;
+      int from = row0, to = row1;
+      if constexpr (APPEND) {
+        const int first = part == 0 ? 0 : p.Hq + (part - 1) * p.Hkv;
+        from = max(row0, first) - first;
+        to = min(row1, first + (part == 0 ? p.Hq : p.Hkv)) - first;
+        if (part > 0 && slot < 0) to = from;
+        xs = part == 0 ? p.q_head : part == 1 ? p.k_head : p.v_head;
+        ys = part == 0 ? p.qo_head : p.page_head;
+        x = static_cast<const T*>(part == 0 ? p.q : part == 1 ? p.k : p.v) +
+            t * (part == 0 ? p.q_token : part == 1 ? p.k_token : p.v_token);
+        y = static_cast<T*>(part == 0 ? p.q_out : part == 1 ? p.k_pages : p.v_pages) +
+            (part == 0 ? t * p.qo_token : slot);
+      } else {
+        xs = p.x_head;
+        ys = p.y_head;
+        x = static_cast<const T*>(p.x) + batch * p.x_batch + n * p.x_token;
+        y = static_cast<T*>(p.y) + batch * p.y_batch + n * p.y_token;
       }
-      row += kRopeUnroll;
-      if (row >= row1) break;
-      load(row);
+      int left = to - from;
+      if (left <= 0) continue;
+      x += from * xs + c;
+      y += from * ys + c;
+      const bool turns = rotate && part < 2;
+      // U heads on their way while the U before them are rotated and stored
+      V a[U], b[U], a2[U], b2[U];
+      auto load = [&](V (&va)[U], V (&vb)[U], int count) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          if (i < count) {
+            va[i] = *reinterpret_cast<const V*>(x);
+            if (HALF && two) vb[i] = *reinterpret_cast<const V*>(x + second);
+          }
+          x += xs;
+        }
+      };
+      load(a, b, left);
+      if (part == 0 || (part == 1 && row0 >= p.Hq)) {   // the first part that turns
+        if (rotate) {
+#pragma unroll
+          for (int e = 0; e < PAIRS; ++e) w[e] = rotation(f[e], pos, p.mscale, p.transposed != 0);
+        }
+      }
+      for (;;) {
+        if (left > U) load(a2, b2, left - U);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          if (i < left) {
+            if (turns) turn<T, W, HALF>(a[i], b[i], w);
+            *reinterpret_cast<V*>(y) = a[i];
+            if (HALF && two) *reinterpret_cast<V*>(y + second) = b[i];
+          }
+          y += ys;
+        }
+        left -= U;
+        if (left <= 0) break;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          a[i] = a2[i];
+          if (HALF) b[i] = b2[i];
+        }
+      }
     }
   }
 }
