@@ -897,8 +897,14 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
         const int key0 = (t_begin + j) * kKeysPerTile;
         // V rows behind the last key: zeros, written by the first sub-tile that reads them
         if (key0 + kKeysPerTile > kv_len && (sub == 0 || j >= n0)) {
+          // In the double-buffered order S(j) may complete before V(j-1) has
+          // landed, and a wait for V(j) could not tell it from V(j-2) then (the
+          // parity is the same): P(j-1) V first.
           const int iv = base + 2 * j + 1;
-          if (!__all_sync(0xffffffffu, wait_bar(&bars->kv_full[iv % STAGES], (iv / STAGES) & 1, abort, p.timeout_ns))) {
+          bool landed = true;
+          if (Cfg::kDoubleS && j > 0) landed = wait_bar(&bars->o_done[sub], (g - 1) & 1, abort, p.timeout_ns);
+          landed = landed && wait_bar(&bars->kv_full[iv % STAGES], (iv / STAGES) & 1, abort, p.timeout_ns);
+          if (!__all_sync(0xffffffffu, landed)) {
             ok = false;
             break;
           }
