@@ -1,15 +1,19 @@
-"""Compile libfa2.so (sm_103a) in-tree with nvcc.
+"""Compile libfa2.so (sm_103a) in-tree with nvcc, and the torch binding with g++.
 
 The kernel families live in separate translation units that compile in
 parallel; the host side links the CUDA runtime statically and finds the
 driver entry points it needs (tensor-map encoding, address ranges) at run
-time, so the library has no link-time dependency on libcuda.
+time, so the library has no link-time dependency on libcuda.  The binding
+(_binding.so) is a Python extension module against torch's headers and is
+handed the library's functions when it is loaded.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -19,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libfa2.so")
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
+BINDING_PATH = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["fa2_api.cu", "fa2_tc_d64_bf16.cu", "fa2_tc_d128_bf16.cu", "fa2_tc_d256_bf16.cu",
@@ -47,9 +53,41 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
+def _replace(path, make):
+    """Has make(temporary path) write a file next to `path`, then puts it in its place."""
+    fd, tmp = tempfile.mkstemp(suffix=".so", dir=PKG)
+    os.close(fd)
+    try:
+        r = subprocess.run(make(tmp), capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"building {os.path.basename(path)} failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, path)
+    finally:
+        if os.path.exists(tmp):
+            os.remove(tmp)
+
+
+def build_binding(force: bool = False) -> str:
+    """Build _binding.so unless it is newer than its sources and the torch it is built against."""
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)   # found, not imported
+    inputs = [BINDING_SOURCE, os.path.join(INCLUDE, "fa2.h"), os.path.join(torch_dir, "version.py")]
+    if (not force and os.path.exists(BINDING_PATH)
+            and all(os.path.getmtime(f) <= os.path.getmtime(BINDING_PATH) for f in inputs)):
+        return BINDING_PATH
+    includes = [INCLUDE, os.path.join(torch_dir, "include"),
+                os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")]
+    libs = os.path.join(torch_dir, "lib")
+    _replace(BINDING_PATH, lambda tmp: ["g++", "-O2", "-std=c++17", "-fPIC", "-shared"] + ["-I" + i for i in includes]
+             + [BINDING_SOURCE, "-o", tmp, "-L" + libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+                "-Wl,-rpath," + libs])
+    return BINDING_PATH
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Build libfa2.so next to this file unless it is newer than every source."""
+    """Build libfa2.so and the binding next to this file unless they are newer than their sources."""
     if not force and up_to_date():
+        build_binding()
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     common = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -65,22 +103,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(build_binding, force)
         results = list(ex.map(compile_one, SOURCES))
+        binding.result()
     if verbose:
         for _, log in results:
             print(log)
-    fd, tmp = tempfile.mkstemp(suffix=".so", dir=PKG)
-    os.close(fd)
-    try:
-        cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + [o for o, _ in results]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, LIB_PATH)
-    finally:
-        if os.path.exists(tmp):
-            os.remove(tmp)
+    _replace(LIB_PATH, lambda tmp: [nvcc()] + ARCH + ["-shared", "-o", tmp] + [o for o, _ in results])
     return LIB_PATH
 
 

@@ -20,30 +20,45 @@ A step of a server, layer by layer::
     o, lse = fa2.forward_paged(q, k_pages, v_pages, page_table, lens, cu_q=cu_q)
 
 This module only marshals arguments (see the package docstring).  Outputs and
-workspaces that a call makes belong to the stream that it runs on.
+workspaces that a call makes belong to the stream that it runs on.  A call on the
+current device and stream that leaves its outputs to be made goes through the
+compiled binding (csrc/binding.cpp), which makes the same checks; whatever that
+does not take comes here.
 """
 from __future__ import annotations
 
 import ctypes
 import functools
 import math
+import os
 
 import exact_attention_17_gb300 as fa2
+
+from .build import BINDING_PATH
 
 _LL2, _LL3 = ctypes.c_longlong * 2, ctypes.c_longlong * 3
 
 # Filled by the first call: importing the package does not import torch.
 torch = None
 _lib = None
+_fast = None           # the compiled binding
 _codes = None          # element type -> FA2_DTYPE_*
 _raw_stream = None     # device index -> handle of the current stream
 
 
 def _load():
-    global torch, _lib, _codes, _raw_stream
+    global torch, _lib, _fast, _codes, _raw_stream
     import torch as t
 
     _lib = fa2.library()
+    if not os.path.exists(BINDING_PATH):
+        raise RuntimeError(f"{BINDING_PATH} is not built; run `python -m exact_attention_17_gb300.build`")
+    from . import _binding as _fast
+
+    _fast.init(*(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in (
+        "fa2_forward_paged", "fa2_forward_paged_workspace_bytes", "fa2_rope", "fa2_append_paged",
+        "fa2_pages_workspace_bytes", "fa2_pages_reserve", "fa2_pages_fork", "fa2_pages_free", "fa2_pages_compact",
+        "fa2_pages_copy")))
     _codes = fa2._dtype_codes()
     _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None) or (lambda i: t.cuda.current_stream(i).cuda_stream)
     torch = t
@@ -87,6 +102,13 @@ class _Call:
 
 def _fail(rc, where):
     raise fa2.FA2Error(rc, where)
+
+
+def _answer(r, where):
+    """What the compiled binding answered: the outputs, or a status."""
+    if type(r) is int:
+        _fail(r, where)
+    return r
 
 
 def _ints(name, t, shape, device):
@@ -159,6 +181,10 @@ def forward_paged(q, k_pages, v_pages, page_table, kv_lens, cu_q=None, causal: b
     """
     if torch is None:
         _load()
+    if out is None and lse is None and out_dtype is None and workspace is None and stream is None:
+        r = _fast.forward_paged(q, k_pages, v_pages, page_table, kv_lens, cu_q, causal, scale)
+        if r is not None:
+            return _answer(r, "fa2_forward_paged")
     dtype, device = k_pages.dtype, k_pages.device
     args = _cache_args(k_pages, v_pages, page_table, kv_lens, device, dtype)
     shape = q.shape
@@ -227,6 +253,10 @@ def append_paged(k, v, k_pages, v_pages, page_table, kv_lens, cu_q=None, q=None,
     """
     if torch is None:
         _load()
+    if q is not None and q_out is None and stream is None:
+        r = _fast.append_paged(k, v, k_pages, v_pages, page_table, kv_lens, cu_q, q, inv_freq, interleaved, mscale)
+        if r is not None:
+            return _answer(r, "fa2_append_paged")
     dtype, device = k_pages.dtype, k_pages.device
     args = _cache_args(k_pages, v_pages, page_table, kv_lens, device, dtype)
     d = args.d
@@ -306,6 +336,10 @@ def rope_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: str | None = 
 def _rope(x, positions, inv_freq, interleaved, mscale, out, stream, transposed):
     if torch is None:
         _load()
+    if out is None and stream is None:
+        r = _fast.rope(x, positions, inv_freq, interleaved, mscale, transposed)
+        if r is not None:
+            return _answer(r, "fa2_rope")
     dtype, device, shape, xs = x.dtype, x.device, x.shape, x.stride()
     code = _codes.get(dtype)
     dim = len(shape)
@@ -438,6 +472,12 @@ def pages_reserve(page_table, lens, refs, add, page_size: int, workspace=None, s
     tensor [1]: 0, or the number of pages that lack, or -1 where a table row is
     too short -- then nothing has changed.
     """
+    if torch is None:
+        _load()
+    if workspace is None and stream is None:
+        r = _fast.pages_reserve(page_table, lens, refs, add, page_size)
+        if r is not None:
+            return _answer(r, "fa2_pages_reserve")
     args, device = _tables(page_table, lens, refs, page_size)
     _ints("add", add, (args.B,), device)
     with _Call(device, stream) as handle:
@@ -457,6 +497,12 @@ def pages_fork(page_table, lens, refs, src, dst, pools, workspace=None, stream=N
     ``pools`` (a tensor [..., P, Hkv, S, d] or a list of them: all the layers' K
     and V).  Returns the pages that lack as ``pages_reserve`` does.
     """
+    if torch is None:
+        _load()
+    if workspace is None and stream is None:
+        r = _fast.pages_fork(page_table, lens, refs, src, dst, pools)
+        if r is not None:
+            return _answer(r, "fa2_pages_fork")
     data, array, S, pool_device = _pools(pools)
     args, device = _tables(page_table, lens, refs, S)
     if pool_device != device or data.num_pages != args.num_pages:
@@ -475,6 +521,13 @@ def pages_fork(page_table, lens, refs, src, dst, pools, workspace=None, stream=N
 
 def pages_free(page_table, lens, refs, seqs, stream=None):
     """Empty the sequences ``seqs`` int32 [n]; pages nobody names any more become free (fa2_pages_free)."""
+    if torch is None:
+        _load()
+    if stream is None:
+        r = _fast.pages_free(page_table, lens, refs, seqs)
+        if r is not None:
+            _answer(r, "fa2_pages_free")
+            return
     args, device = _tables(page_table, lens, refs, 16)   # (the slots per page play no part)
     n = _list("seqs", seqs, device)
     with _Call(device, stream) as handle:
@@ -489,6 +542,12 @@ def pages_compact(page_table, lens, refs, pools, workspace=None, stream=None):
     Page data, ``page_table`` and ``refs`` follow.  Returns int32 [P]: where
     each page went (its own number where it stayed, -1 for a free one).
     """
+    if torch is None:
+        _load()
+    if workspace is None and stream is None:
+        r = _fast.pages_compact(page_table, lens, refs, pools)
+        if r is not None:
+            return _answer(r, "fa2_pages_compact")
     data, array, S, pool_device = _pools(pools)
     args, device = _tables(page_table, lens, refs, S)
     if pool_device != device or data.num_pages != args.num_pages:
@@ -509,6 +568,13 @@ def pages_copy(pools, src, dst, workspace=None, stream=None):
     Of several pairs with one destination the last counts; a pair whose source
     is another's destination is skipped and reported (``FA2_ERR_PAGE``).
     """
+    if torch is None:
+        _load()
+    if workspace is None and stream is None:
+        r = _fast.pages_copy(pools, src, dst)
+        if r is not None:
+            _answer(r, "fa2_pages_copy")
+            return
     data, array, _, device = _pools(pools)
     n = _list("src", src, device)
     _ints("dst", dst, (n,), device)
