@@ -41,11 +41,21 @@
 //    of the tiles being cut.  A part's normalised O and LSE go to the workspace,
 //    and a second kernel merges them (as fa2_combine.cu, in the order of the
 //    keys: results do not depend on timing).
+//  * Producers.  The tiled copies that one warp issues run one after the other:
+//    20.8 bytes per clock in boxes of 16 KB (a 128-byte row in 6 clocks), 14.0 in
+//    boxes of 2 KB, whichever lanes issue them; two warps reach 40.5, four 75 to
+//    82.  One warp keeps up with the tiles of head dimensions 64 and 128 (a warp
+//    each for K and V was 3 to 6% slower).  At 256 a tile is 64 KB, and with
+//    room for one of K and one of V a copy starts only when the MMAs of the tile
+//    before are done: three warps share each tile there (200 -> 171 us for 2600
+//    tokens over 2000-4096 keys when K had two warps and V one).
 //  * Segments.  The producer warp runs ahead: it loads the next segment's Q and
 //    first tiles while the current one finishes.  One named barrier per segment,
 //    which every role passes for every segment, also after an abort, hands over
 //    the segment's description.
 #pragma once
+
+#include <type_traits>
 
 #include "fa2_fwd_sm103.cuh"
 
@@ -380,6 +390,43 @@ __device__ __forceinline__ PagedParts paged_parts_even(const PagedParams& p, int
   return r;
 }
 
+// Whole warp: the page numbers of a sequence's tiles, in ascending order of the
+// tiles, 32 table entries at a time (one per lane) and the next 32 on their way.
+struct PageCursor {
+  const int* table;
+  int live;        // table entries that hold keys
+  int chunk0;      // first entry in `pages`
+  int pages, pages_next;
+
+  __device__ __forceinline__ PageCursor(const PagedParams& p, const PagedUnit& w, int tiles) {
+    table = p.page_table + (tiles > 0 ? w.table : 0);
+    live = tiles > 0 ? (w.kv_len + (1 << p.page_log2) - 1) >> p.page_log2 : 0;
+    chunk0 = tiles > 0 ? (w.t_begin << 7) >> p.page_log2 : 0;
+    pages = fetch(p, chunk0);
+    pages_next = fetch(p, chunk0 + 32);
+  }
+  __device__ __forceinline__ int fetch(const PagedParams& p, int first) const {
+    const int i = first + (threadIdx.x & 31);
+    int id = 0;
+    if (i < live) {
+      id = table[i];
+      if (id < 0 || id >= p.num_pages) atomicOr(p.status, kDevErrPage);
+    }
+    return id;
+  }
+  // lane x: the tile's x-th page; *count: how many there are
+  __device__ __forceinline__ int tile(const PagedParams& p, int t, int* count) {
+    const int first = (t << 7) >> p.page_log2;
+    if (first >= chunk0 + 32) {
+      chunk0 += 32;
+      pages = pages_next;
+      pages_next = fetch(p, chunk0 + 32);
+    }
+    *count = min(kKeysPerTile >> min(p.page_log2, 7), live - first);
+    return __shfl_sync(0xffffffffu, pages, (first - chunk0 + (threadIdx.x & 31)) & 31);
+  }
+};
+
 // Bytes of one head's K and V that a group of heads may hold in L2 together.
 constexpr long long kPagedL2Bytes = 64ll << 20;
 
@@ -448,6 +495,9 @@ __device__ __forceinline__ PagedParts paged_item(const PagedParams& p, int index
   return r;
 }
 
+template <int N>
+using Int = std::integral_constant<int, N>;
+
 // Named barrier of the segments (kBarP0 and kBarP1 are the dense kernel's).
 constexpr int kBarSegment = 3;
 constexpr int kBarShares = 4;   // the softmax warps, while they merge their shares
@@ -469,8 +519,10 @@ struct PagedConfig : FwdConfig<D, SUBS> {
   static constexpr int kProducer = 72;
   static_assert(SUBS * 128 * kSoftmax + 128 * kProducer <= FwdShape<SUBS>::kLaunch * FwdShape<SUBS>::kThreads,
                 "register rebalancing exceeds the launch allocation");
-  // every role: softmax, producer and MMA warps, and the watcher where there is one
-  static constexpr int kSegmentThreads = SUBS * 128 + 64 + (Base::kNamedP ? 32 : 0);
+  // Three producer warps, each with its 64-column chunks of every K and V tile.
+  static constexpr bool kThree = D == 256;
+  // every role: softmax, producer and MMA warps, and the watcher or the other two producers where there are any
+  static constexpr int kSegmentThreads = SUBS * 128 + 64 + (Base::kNamedP ? 32 : kThree ? 64 : 0);
 };
 
 template <int STAGES>
@@ -492,7 +544,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
     fa2_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedParams p) {
   using Cfg = PagedConfig<D, SUBS>;
-  constexpr int kWarpProducer = 4 * SUBS;      // schedule and TMA warp
+  constexpr int kWarpProducer = 4 * SUBS;      // schedule and copies
   constexpr int kWarpMma = 4 * SUBS + 1;       // MMA warp, owns the TMEM allocation
   constexpr int kWarpWatch = 4 * SUBS + 2;     // K/V watcher (named-barrier variants)
   constexpr int STAGES = Cfg::kStages;
@@ -523,11 +575,64 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
     return max(0, min(w.t_end, key_tiles_of(kept)) - w.t_begin);
   };
 
+  // ---- the producers' copies; whole warps, `ok` is cleared after an abort
+  auto warp_wait = [&](uint64_t* bar, int phase, bool& ok) {
+    if (!ok) return;
+    ok = __all_sync(0xffffffffu, wait_bar(bar, phase, abort, p.timeout_ns));
+    if (!ok && lane == 0) raise_abort(abort, p.status);
+  };
+  // Chunks C0 .. C1 - 1 of copy `index` into the ring: K (even) or V (odd) of the
+  // key tile `tile`, which lies at or behind the cursor.  Everything is ready
+  // before the wait for the slot: instructions after it delay every tile.
+  int last[2] = {-1, -1};   // this warp's last copies of K and of V
+  auto copy = [&](auto C0, auto C1, const PagedUnit& w, PageCursor& pages, int tile, int index, bool& ok) {
+    constexpr int kFirst = decltype(C0)::value, kEnd = decltype(C1)::value;
+    const int slot = index % STAGES, lap = index / STAGES;
+    const int slots_log2 = min(p.page_log2, 7);   // slots of a page that the tile reads
+    int count;
+    const int id = pages.tile(p, tile, &count);
+    const CUtensorMap* map = (index & 1) == 0 ? &tm_k : &tm_v;
+    const int row = (tile << 7) & ((1 << p.page_log2) - 1);
+    uint8_t* dst = sKV + slot * TILE + (static_cast<uint32_t>(lane) << slots_log2) * 128;
+    const uint32_t bytes = static_cast<uint32_t>(count * (kEnd - kFirst)) * (128u << slots_log2);
+    if (lap > 0) warp_wait(&bars->kv_empty[slot], (lap - 1) & 1, ok);
+    if (!ok) return;
+    if (lane == 0) bar_arrive_expect_tx(&bars->kv_full[slot], bytes);
+    __syncwarp();
+    if (lane < count) {
+#pragma unroll
+      for (int c = kFirst; c < kEnd; ++c)
+        tma_load_4d(dst + c * kChunkBytes, map, &bars->kv_full[slot], c * 64, row, w.head, id);
+    }
+    __syncwarp();
+    last[index & 1] = index;
+  };
+  // Three producers: their chunks of K and of V.  In the order of the MMAs: K(j+1),
+  // whose slot S(j) frees, then V(j), whose slot P(j-1) V frees.
+  auto copy_three = [&](auto K0, auto K1, auto V0, auto V1, const PagedUnit& w, int n, int tiles, PageCursor& k_pages,
+                        PageCursor& v_pages, int first, bool& ok) {
+    for (int j = first; j <= n && ok; ++j) {
+      if (j < n) copy(K0, K1, w, k_pages, w.t_begin + j, 2 * (tiles + j), ok);
+      if (j > 0 && ok) copy(V0, V1, w, v_pages, w.t_begin + j - 1, 2 * (tiles + j) - 1, ok);
+    }
+  };
+  // Before the CTA may exit, the copies of a producer must have landed: the last
+  // STAGES, where it made them all, else the last of K and of V (a two-slot ring).
+  auto drain = [&]() {
+    if (lane != 0) return;
+    volatile int never = 0;
+    const int end = max(last[0], last[1]);
+    for (int i = max(0, end - STAGES + 1); i <= end; ++i)
+      if (!Cfg::kThree || i == last[i & 1])
+        wait_bar(&bars->kv_full[i % STAGES], (i / STAGES) & 1, &never, p.timeout_ns);
+  };
+  static_assert(!Cfg::kThree || STAGES == 2, "a slot each for K and V");
+
   if (warp == kWarpProducer && lane == 0) {
     bar_init(&bars->q_full, 1);
     bar_init(&shared->q_empty, 1);
     for (int s = 0; s < STAGES; ++s) {
-      bar_init(&bars->kv_full[s], 1);
+      bar_init(&bars->kv_full[s], Cfg::kThree ? 3 : 1);
       bar_init(&bars->kv_empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -557,9 +662,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
   if (warp >= kWarpProducer) {
     regs_decrease<Cfg::kProducer>();
     if (warp == kWarpProducer) {
-      // ------------------------------------------------------------ schedule and TMA producer
-      const int slots_log2 = min(p.page_log2, 7);           // slots of a page that one tile reads
-      const int tile_pages = kKeysPerTile >> slots_log2;    // pages (boxes per 64 columns) of a tile
+      // ------------------------------------------------------------ schedule and copies
       PagedWalk walk;
       PagedUnit w;
       if (p.even) {
@@ -568,7 +671,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
       } else {
         w = paged_item<SUBS>(p, static_cast<int>(blockIdx.x), false, D).u;
       }
-      int issued = 0, loads = 0;
+      int tiles = 0, loads = 0;   // tiles of the segments before; Q loads
       bool ok = true;
       for (int k = 0;; ++k) {
         if (lane == 0) shared->unit[k & 1] = w;
@@ -578,68 +681,15 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
           n = tiles_for(w, 0);
           if (SUBS == 2) n = max(n, tiles_for(w, 1));
         }
-        // table entries [chunk0, chunk0 + 32) of the sequence in `pages`, the next 32 in `pages_next`
-        const int* table = p.page_table + (n > 0 ? w.table : 0);
-        const int live_pages = n > 0 ? (w.kv_len + (1 << p.page_log2) - 1) >> p.page_log2 : 0;
-        int chunk0 = n > 0 ? (w.t_begin << 7) >> p.page_log2 : 0;
-        auto fetch = [&](int first) {
-          const int i = first + lane;
-          int id = 0;
-          if (i < live_pages) {
-            id = table[i];
-            if (id < 0 || id >= p.num_pages) atomicOr(p.status, kDevErrPage);
-          }
-          return id;
-        };
-        int pages = fetch(chunk0), pages_next = fetch(chunk0 + 32);
-        // copy i of this segment: K (even i) or V of tile i / 2
-        auto load = [&](int i) {
-          const int slot = issued % STAGES, lap = issued / STAGES;
-          if (ok && lap > 0) {
-            if (lane == 0) {
-              ok = wait_bar(&bars->kv_empty[slot], (lap - 1) & 1, abort, p.timeout_ns);
-              if (!ok) raise_abort(abort, p.status);
-            }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-          }
-          if (!ok) return;
-          const int tile = w.t_begin + (i >> 1);
-          const int first = (tile << 7) >> p.page_log2;       // table entry of the tile's first page
-          if (first >= chunk0 + 32) {
-            chunk0 += 32;
-            pages = pages_next;
-            pages_next = fetch(chunk0 + 32);
-          }
-          const int count = min(tile_pages, live_pages - first);
-          const int id = __shfl_sync(0xffffffffu, pages, (first - chunk0 + lane) & 31);
-          if (lane == 0)
-            bar_arrive_expect_tx(&bars->kv_full[slot], static_cast<uint32_t>(count) * NCH * (128u << slots_log2));
-          __syncwarp();
-          if (lane < count) {
-            const CUtensorMap* map = (i & 1) == 0 ? &tm_k : &tm_v;
-            const int row = p.page_log2 > 7 ? (tile << 7) & ((1 << p.page_log2) - 1) : 0;
-            uint8_t* dst = sKV + slot * TILE + (static_cast<uint32_t>(lane) << slots_log2) * 128;
-#pragma unroll
-            for (int c = 0; c < NCH; ++c)
-              tma_load_4d(dst + c * kChunkBytes, map, &bars->kv_full[slot], c * 64, row, w.head, id);
-          }
-          __syncwarp();
-          ++issued;
-        };
+        PageCursor pages(p, w, n);
         // Ahead of the hand-over: the first copies, which do not wait for the
         // last V of the segment before (its slot comes STAGES - 1 copies
         // later), and Q, once the last S of the segment before is complete.
         const int early = min(STAGES - 1, 2 * n);
         for (int i = 0; i < early; ++i) {
-          load(i);
-          if (i == 0 && ok) {
-            if (loads > 0) {
-              if (lane == 0) {
-                ok = wait_bar(&shared->q_empty, (loads - 1) & 1, abort, p.timeout_ns);
-                if (!ok) raise_abort(abort, p.status);
-              }
-              ok = __shfl_sync(0xffffffffu, ok, 0);
-            }
+          copy(Int<0>{}, Int<Cfg::kThree ? 2 : NCH>{}, w, pages, w.t_begin + (i >> 1), 2 * tiles + i, ok);
+          if (i == 0) {
+            if (loads > 0) warp_wait(&shared->q_empty, (loads - 1) & 1, ok);
             if (ok) {
               // Q boxes of the live tokens, a box per lane
               const uint32_t box_bytes = static_cast<uint32_t>(p.box_tokens) * p.G * 128;
@@ -650,9 +700,9 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
                 bar_arrive_expect_tx(&bars->q_full, static_cast<uint32_t>(boxes) * kCopies * NCH * box_bytes);
               __syncwarp();
               for (int y = lane; y < boxes * kCopies; y += 32) {
-                const int x = y / kCopies, copy = y % kCopies;
+                const int x = y / kCopies, part = y % kCopies;
                 const int sub = x / per_sub;
-                uint8_t* dst = sQ + sub * TILE + (x - sub * per_sub) * box_bytes + copy * (32 * 128);
+                uint8_t* dst = sQ + sub * TILE + (x - sub * per_sub) * box_bytes + part * (32 * 128);
                 for (int c = 0; c < NCH; ++c)
                   tma_load_3d(dst + c * kChunkBytes, &tm_q, &bars->q_full, c * 64, w.head * p.G,
                               w.row0 + x * p.box_tokens);
@@ -664,19 +714,42 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
         }
         named_sync(kBarSegment, Cfg::kSegmentThreads);
         if (!w.valid) break;
-        for (int i = early; i < 2 * n; ++i) load(i);
+        if constexpr (Cfg::kThree) {
+          PageCursor v_pages(p, w, n);
+          copy_three(Int<0>{}, Int<2>{}, Int<0>{}, Int<1>{}, w, n, tiles, pages, v_pages, 1, ok);
+        } else {
+          for (int i = early; i < 2 * n && ok; ++i)
+            copy(Int<0>{}, Int<NCH>{}, w, pages, w.t_begin + (i >> 1), 2 * tiles + i, ok);
+        }
+        tiles += n;
         if (p.even)
           w = walk.next<SUBS>(p);
         else
           w.valid = 0;
       }
-      // Before the CTA may exit, every copy it started must have landed.
-      if (lane == 0) {
+      if (lane == 0 && loads > 0) {
         volatile int never = 0;
-        if (loads > 0) wait_bar(&bars->q_full, (loads - 1) & 1, &never, p.timeout_ns);
-        for (int i = max(0, issued - STAGES); i < issued; ++i)
-          wait_bar(&bars->kv_full[i % STAGES], (i / STAGES) & 1, &never, p.timeout_ns);
+        wait_bar(&bars->q_full, (loads - 1) & 1, &never, p.timeout_ns);
       }
+      drain();
+      __syncwarp();
+    } else if (warp != kWarpMma && Cfg::kThree) {
+      // ------------------------------------------------------------ the second and third producer
+      int tiles = 0;
+      bool ok = true;
+      for (int k = 0;; ++k) {
+        named_sync(kBarSegment, Cfg::kSegmentThreads);
+        const PagedUnit w = shared->unit[k & 1];
+        if (!w.valid) break;
+        const int n = tiles_for(w, 0);
+        PageCursor pages(p, w, n), v_pages(p, w, n);
+        if (warp == kWarpMma + 1)
+          copy_three(Int<2>{}, Int<3>{}, Int<1>{}, Int<3>{}, w, n, tiles, pages, v_pages, 0, ok);
+        else
+          copy_three(Int<3>{}, Int<4>{}, Int<3>{}, Int<4>{}, w, n, tiles, pages, v_pages, 0, ok);
+        tiles += n;
+      }
+      drain();
       __syncwarp();
     } else if (warp == kWarpWatch && Cfg::kNamedP) {
       // ------------------------------------------------------------ K/V watcher
@@ -797,39 +870,27 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
             const int slot_v = iv % STAGES, slot_k = ik % STAGES;
             uint64_t* bv = &bars->kv_full[slot_v];
             const uint32_t pv = (iv / STAGES) & 1;
-            if constexpr (Cfg::kDoubleS) {
-              // S(j+1) into the other buffer ahead of P(j) V
-              if (j + 1 < n0) {
-                if (!wait_bar(&bars->kv_full[slot_k], (ik / STAGES) & 1, abort, p.timeout_ns)) { ok = false; break; }
-                tc_fence_after_sync();
-                issue_s(0, slot_k, (g + 1) & 1);
-                mma_commit(&bars->s_full[(g + 1) & 1]);
-                mma_commit(&bars->kv_empty[slot_k]);
-                if (j + 2 == n0) mma_commit(&shared->q_empty);
-              }
-              if (!wait_bar3(bv, pv, &bars->p_ready[g & 1], (g >> 1) & 1, bv, pv, abort, p.timeout_ns)) {
-                ok = false;
-                break;
-              }
+            auto next_s = [&](int buf) {   // S(j+1)
+              ok = wait_bar(&bars->kv_full[slot_k], (ik / STAGES) & 1, abort, p.timeout_ns);
+              if (!ok) return;
               tc_fence_after_sync();
-              issue_pv(0, slot_v, j > 0, g & 1);
-              mma_commit(&bars->o_done[0]);
-              mma_commit(&bars->kv_empty[slot_v]);
-            } else {
-              if (!wait_bar3(bv, pv, &bars->p_ready[0], g & 1, bv, pv, abort, p.timeout_ns)) { ok = false; break; }
-              tc_fence_after_sync();
-              issue_pv(0, slot_v, j > 0, 0);
-              if (j + 1 == n0) mma_commit(&bars->o_done[0]);
-              mma_commit(&bars->kv_empty[slot_v]);
-              if (j + 1 < n0) {
-                if (!wait_bar(&bars->kv_full[slot_k], (ik / STAGES) & 1, abort, p.timeout_ns)) { ok = false; break; }
-                tc_fence_after_sync();
-                issue_s(0, slot_k, 0);
-                mma_commit(&bars->s_full[0]);
-                mma_commit(&bars->kv_empty[slot_k]);
-                if (j + 2 == n0) mma_commit(&shared->q_empty);
-              }
-            }
+              issue_s(0, slot_k, buf);
+              mma_commit(&bars->s_full[buf]);
+              mma_commit(&bars->kv_empty[slot_k]);
+              if (j + 2 == n0) mma_commit(&shared->q_empty);
+            };
+            // double-buffered: S(j+1) into the other buffer ahead of P(j) V
+            const int buf = Cfg::kDoubleS ? g & 1 : 0;
+            if (Cfg::kDoubleS && j + 1 < n0) next_s(buf ^ 1);
+            ok = ok && wait_bar3(bv, pv, &bars->p_ready[buf], Cfg::kDoubleS ? (g >> 1) & 1 : g & 1, bv, pv, abort,
+                                 p.timeout_ns);
+            if (!ok) break;
+            tc_fence_after_sync();
+            issue_pv(0, slot_v, j > 0, buf);
+            if (!Cfg::kOutDoneLast || j + 1 == n0) mma_commit(&bars->o_done[0]);
+            mma_commit(&bars->kv_empty[slot_v]);
+            if (!Cfg::kDoubleS && j + 1 < n0) next_s(0);
+            if (!ok) break;
           }
           if (!ok) raise_abort(abort, p.status);
         }
@@ -897,6 +958,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
         const int key0 = (t_begin + j) * kKeysPerTile;
         // V rows behind the last key: zeros, written by the first sub-tile that reads them
         if (key0 + kKeysPerTile > kv_len && (sub == 0 || j >= n0)) {
+          const int tid = wq * 32 + lane;
           // In the double-buffered order S(j) may complete before V(j-1) has
           // landed, and a wait for V(j) could not tell it from V(j-2) then (the
           // parity is the same): P(j-1) V first.
@@ -904,16 +966,19 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
           bool landed = true;
           if (Cfg::kDoubleS && j > 0) landed = wait_bar(&bars->o_done[sub], (g - 1) & 1, abort, p.timeout_ns);
           landed = landed && wait_bar(&bars->kv_full[iv % STAGES], (iv / STAGES) & 1, abort, p.timeout_ns);
-          if (!__all_sync(0xffffffffu, landed)) {
+          landed = __all_sync(0xffffffffu, landed);
+          if (landed) {
+            const uint32_t v_addr = smem_addr(sKV + (iv % STAGES) * TILE);
+            const uint32_t keep_bytes = static_cast<uint32_t>(kv_len - key0) * 128;
+#pragma unroll
+            for (int c = 0; c < NCH; ++c)
+              for (uint32_t at = keep_bytes + tid * 16; at < kChunkBytes; at += kRowsPerSub * 16)
+                st_shared_v4(v_addr + c * kChunkBytes + at, 0u, 0u, 0u, 0u);
+          }
+          if (!landed) {
             ok = false;
             break;
           }
-          const uint32_t v_addr = smem_addr(sKV + (iv % STAGES) * TILE);
-          const uint32_t keep_bytes = static_cast<uint32_t>(kv_len - key0) * 128;
-#pragma unroll
-          for (int c = 0; c < NCH; ++c)
-            for (uint32_t at = keep_bytes + (wq * 32 + lane) * 16; at < kChunkBytes; at += kRowsPerSub * 16)
-              st_shared_v4(v_addr + c * kChunkBytes + at, 0u, 0u, 0u, 0u);
           fence_proxy_async_shared();
         }
         if (warp_live) {

@@ -226,3 +226,20 @@ def test_numbers_outside_the_cache_are_reported():
     o, lse = fa2.forward_paged(q, cache.k, cache.v, cache.table, cache.lens)
     assert status() == fa2.FA2_OK
     check(o, lse, q, cache, [1, 1], True, 1 / math.sqrt(d))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("q_len", [1, 3, 40, 400])
+def test_no_wait_runs_out(d, q_len):
+    """Every wait in the kernels gives up after two seconds; none gets there."""
+    cache = Cache([3000, 1500, 700], 2, 32, d, BF, seed=21)
+    q_lens = [q_len] * 3
+    q = queries(q_lens, 8, d, BF, seed=22)
+    cu = offsets(q_lens)
+    fa2.forward_paged(q, cache.k, cache.v, cache.table, cache.lens, cu_q=cu)
+    first, last = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    first.record()
+    fa2.forward_paged(q, cache.k, cache.v, cache.table, cache.lens, cu_q=cu)
+    last.record()
+    torch.cuda.synchronize()
+    assert first.elapsed_time(last) < 500.0
