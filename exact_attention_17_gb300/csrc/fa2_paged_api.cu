@@ -490,7 +490,7 @@ size_t copy_ints(int n) { return 1 + 2 * static_cast<size_t>(n); }
 
 int launched(cudaError_t e) { return e == cudaSuccess ? FA2_OK : FA2_ERR_LAUNCH; }
 
-constexpr int kMaxPairs = 1 << 20;
+constexpr int kMaxPairs = 1 << 16;   // the lists are searched for indices named twice
 
 }  // namespace
 

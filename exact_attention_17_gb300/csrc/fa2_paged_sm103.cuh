@@ -443,8 +443,8 @@ __device__ __forceinline__ PagedParts paged_item(const PagedParams& p, int index
     total += static_cast<long long>(s.blocks) * key_tiles_of(s.kv_len);
   }
   total = warp_sum(total) * p.Hkv;
-  const int per_unit =
-      static_cast<int>(max((total + p.ctas - 1) / p.ctas, static_cast<long long>(p.min_tiles)));
+  const int per_unit = static_cast<int>(
+      min(max((total + p.ctas - 1) / p.ctas, static_cast<long long>(p.min_tiles)), 1ll << 24));   // more than any length
 
   PagedParts r;
   r.u.valid = 0;

@@ -352,8 +352,11 @@ typedef struct {
  *              fa2_forward_paged_workspace_bytes bytes; its contents do not
  *              matter, on entry or afterwards.  Calls that may run at the same
  *              time (streams, graphs) need one each.
- * P is rounded to the cache's type for the P V product; sums are fp32.  The
- * result does not depend on timing: repeated calls give the same bits.
+ * O, LSE and workspace overlap neither each other nor an input.  P is rounded to
+ * the cache's type for the P V product; sums are fp32.  The result does not
+ * depend on timing: repeated calls give the same bits.  A value of a live token
+ * that is not finite may reach every row of its sequence (a masked weight of 0
+ * times infinity is NaN), as in the formula.
  * T = 0, Hq = 0 or B = 0 is a valid empty problem.  Errors as fa2_forward.
  */
 int fa2_forward_paged(const fa2_paged_cache *cache, const void *Q, long long q_token_stride,
@@ -372,8 +375,8 @@ size_t fa2_forward_paged_workspace_bytes(int B, int T, int Hq, int kv_heads, int
  * f_i = inv_freq[i] radians per position (device memory, 64-bit; scaling for
  * long contexts is a matter of these numbers and of mscale).  The other columns
  * are copied.  transposed != 0 applies the transposed rotation: the gradient.
- * Angles are exact to 2^-25 turns for any position below 2^31 in magnitude; products are fp32 and
- * rounded once.
+ * Angles are exact to 2^-25 turns for any position below 2^31 in magnitude;
+ * products are fp32 and rounded once.
  *   X, Y       [B, H, N, d], strides {batch, head, token} in elements; Y = X
  *              (same strides) works in place, other overlaps are refused
  *              (FA2_ERR_MEMORY).  d is even, at most 1024.  Interleaved
@@ -393,7 +396,7 @@ int fa2_rope(const void *X, const long long *x_strides, void *Y, const long long
  * queries Q [T, Hq, d] into Q_out (Hq = 0: none; Q_out = Q works in place).
  * K, V [T, kv_heads, d]; strides {token, head} in elements, multiples of 8.
  * Tokens at negative positions (c_b > kv_lens[b]) are not written.  The pages
- * written must not be shared by sequences.
+ * written must not be shared by sequences, and K, V and Q not lie in them.
  */
 int fa2_append_paged(const fa2_paged_cache *cache, const void *K, const long long *k_strides,
                      const void *V, const long long *v_strides, const void *Q,
@@ -408,7 +411,8 @@ int fa2_append_paged(const fa2_paged_cache *cache, const void *K, const long lon
  * -1, 0 and 0.  A page that several sequences share is full.  num_pages is at
  * most 2^21 - 1.  Entries that contradict each other (a page number outside the
  * pool, a freed page freed again, a sequence index outside [0, B)) are skipped
- * and reported as FA2_ERR_PAGE by the device status word.
+ * and reported as FA2_ERR_PAGE by the device status word.  Lists (src, dst, seqs)
+ * hold at most 65536 indices.  Calls on the same tables go on one stream.
  */
 typedef struct {
   int *page_table;

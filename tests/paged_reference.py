@@ -4,6 +4,7 @@ Not a test module: the GPU tests import it.  The caches hold NaN in every slot
 that belongs to nobody (unused pages, slots behind a sequence's last token), and
 their tables hold numbers far outside the pool behind each row's last page.
 """
+import gc
 import math
 
 import torch
@@ -127,3 +128,12 @@ def rotate_bound(x, inv_freq, interleaved, dtype, mscale=1.0):
     else:
         out[..., :r // 2], out[..., r // 2:r] = bound, bound
     return out
+
+
+def release_memory():
+    """Leaves the device's memory to the next test module as it was found: what
+    exceptions' frames hold, the workspaces of matrix products, cached blocks."""
+    gc.collect()
+    torch.cuda.synchronize()
+    torch._C._cuda_clearCublasWorkspaces()
+    torch.cuda.empty_cache()

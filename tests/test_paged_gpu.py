@@ -6,7 +6,7 @@ import torch
 
 import exact_attention_17_gb300 as fa2
 from exact_attention_17_gb300 import build as libbuild
-from paged_reference import EPS, Cache, attention, offsets
+from paged_reference import EPS, Cache, attention, offsets, release_memory
 
 pytestmark = pytest.mark.gpu
 
@@ -21,6 +21,7 @@ def library():
     fa2.fa2_device_status(None, reset=True)
     yield
     assert fa2.fa2_device_status(None, reset=True) == fa2.FA2_OK
+    release_memory()
 
 
 def queries(q_lens, Hq, d, dtype, seed, std=1.0, tail=0):
@@ -197,6 +198,64 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for c, q, (o, lse) in results:
         check(o, lse, q, c, [2, 40], True, 1 / math.sqrt(d))
+
+
+def test_two_captured_calls_on_two_streams():
+    """Each capture has its own workspace: replays may overlap each other and an eager call."""
+    d = 128
+    cu = offsets([3, 50])
+    calls = []
+    for s in range(2):
+        cache = Cache([7000, 900], 2, 32, d, BF, seed=30 + s)
+        q = queries([3, 50], 8, d, BF, seed=40 + s)
+        fa2.forward_paged(q, cache.k, cache.v, cache.table, cache.lens, cu_q=cu)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = fa2.forward_paged(q, cache.k, cache.v, cache.table, cache.lens, cu_q=cu)
+        calls.append((cache, q, graph, out, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for cache, q, graph, out, stream in calls:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        eager = fa2.forward_paged(calls[0][1], calls[0][0].k, calls[0][0].v, calls[0][0].table, calls[0][0].lens, cu_q=cu)
+    torch.cuda.synchronize()
+    for cache, q, graph, (o, lse), stream in calls:
+        check(o, lse, q, cache, [3, 50], True, 1 / math.sqrt(d))
+    assert torch.equal(eager[0], calls[0][3][0])
+
+
+def test_given_outputs_and_workspace_are_checked_and_used():
+    d = 64
+    cache = Cache([5000, 30], 2, 16, d, BF, seed=23)
+    q = queries([1, 1], 8, d, BF, seed=24)
+    o, lse = fa2.forward_paged(q, cache.k, cache.v, cache.table, cache.lens)     # the compiled binding
+    need = fa2.library().fa2_forward_paged_workspace_bytes(2, 2, 8, 2, d, 0)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    ws.fill_(255)                                                                  # NaN everywhere
+    given = [torch.empty_like(o), torch.empty_like(lse)]
+    fa2.forward_paged(q, cache.k, cache.v, cache.table, cache.lens, out=given[0], lse=given[1], workspace=ws)
+    assert torch.equal(given[0], o) and torch.equal(given[1], lse)
+    args = (q, cache.k, cache.v, cache.table, cache.lens)
+    with pytest.raises(fa2.FA2Error) as e:
+        fa2.forward_paged(*args, workspace=ws[:need - 256])
+    assert e.value.status == fa2.FA2_ERR_MEMORY
+    for bad in (dict(out=o.float()), dict(out=o[:1]), dict(lse=lse.half()), dict(out_dtype=HF), dict(cu_q=cache.lens),
+                dict(workspace=ws[::2])):
+        with pytest.raises(ValueError):
+            fa2.forward_paged(*args, **bad)
+    for bad in ((q[:, :7], *args[1:]), (q[:1], *args[1:]), (q.half(), *args[1:]), (q, cache.k, cache.v.half(), *args[3:]),
+                (q, cache.k[..., :32], cache.v[..., :32], *args[3:]), (*args[:3], cache.table.long(), cache.lens),
+                (*args[:3], cache.table[:1], cache.lens), (*args[:4], cache.lens.cpu())):
+        with pytest.raises(ValueError):
+            fa2.forward_paged(*bad)
+    with pytest.raises(fa2.FA2Error) as e:
+        fa2.forward_paged(*args, scale=0.0)
+    assert e.value.status == fa2.FA2_ERR_SCALE
+    odd = torch.empty((4, 2, 24, d), dtype=BF, device="cuda")                      # 24 slots a page
+    with pytest.raises(fa2.FA2Error) as e:
+        fa2.forward_paged(q, odd, odd, cache.table, cache.lens)
+    assert e.value.status == fa2.FA2_ERR_SHAPE
 
 
 def test_numbers_outside_the_cache_are_reported():

@@ -179,7 +179,7 @@ def test_pages(lib):
             fork(tables(), pools(), dst=None), fork(tables(), pools(), missing=None), free(tables(), seqs=None),
             compact(tables(), pools(), moved=None), copy(pools(), src=None), copy(pools(), dst=None)] == [null] * 9
     assert [fork(tables(), pools(), n=-1), fork(tables(), pools(num_pages=5)), free(tables(), n=-1),
-            compact(tables(), pools(num_pages=5)), copy(pools(), n=-1), copy(pools(), n=(1 << 20) + 1)] == [shape] * 6
+            compact(tables(), pools(num_pages=5)), copy(pools(), n=-1), copy(pools(), n=(1 << 16) + 1)] == [shape] * 6
     assert free(tables(), n=0, seqs=None) == fa2.FA2_OK
     assert copy(pools(), n=0, src=None) == fa2.FA2_OK
 
@@ -189,7 +189,7 @@ def test_pages_workspace(lib):
     assert f(0, 0) == 256
     assert f(1000, 5) == (4 * 2001 + 255) // 256 * 256
     assert f(3, 100) == (4 * 301 + 255) // 256 * 256
-    assert f(-1, 0) == f(0, -1) == f(1 << 21, 0) == f(0, (1 << 20) + 1) == 0
+    assert f(-1, 0) == f(0, -1) == f(1 << 21, 0) == f(0, (1 << 16) + 1) == 0
 
 
 def test_binding_refuses_host_tensors_and_bad_arguments():

@@ -7,6 +7,7 @@ import torch
 
 import exact_attention_17_gb300 as fa2
 from exact_attention_17_gb300 import build as libbuild
+from paged_reference import release_memory
 
 pytestmark = pytest.mark.gpu
 
@@ -19,6 +20,7 @@ def library():
     fa2.fa2_device_status(None, reset=True)
     yield
     assert fa2.fa2_device_status(None, reset=True) == fa2.FA2_OK
+    release_memory()
 
 
 def status():

@@ -6,7 +6,7 @@ import torch
 
 import exact_attention_17_gb300 as fa2
 from exact_attention_17_gb300 import build as libbuild
-from paged_reference import EPS, Cache, offsets, rotate, rotate_bound
+from paged_reference import EPS, Cache, offsets, release_memory, rotate, rotate_bound
 
 pytestmark = pytest.mark.gpu
 
@@ -21,6 +21,7 @@ def library():
     fa2.fa2_device_status(None, reset=True)
     yield
     assert fa2.fa2_device_status(None, reset=True) == fa2.FA2_OK
+    release_memory()
 
 
 def normal(shape, dtype, seed):
