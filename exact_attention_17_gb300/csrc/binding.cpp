@@ -312,6 +312,17 @@ at::Tensor pages_workspace(int pages, int n, at::Device d, size_t* size) {
   return make({static_cast<int64_t>(*size > 0 ? *size : 1)}, at::kByte, d);
 }
 
+// An int32 tensor [1] that the workspace follows in the same allocation (an
+// allocation costs a small call about two microseconds).
+at::Tensor answer_and_workspace(int pages, int n, at::Device d, char** ws, size_t* size) {
+  constexpr int64_t kAnswerBytes = 256;
+  *size = pages_workspace_fn(pages, n);
+  at::Tensor t = make({(kAnswerBytes + static_cast<int64_t>(*size)) / 4}, at::kInt, d);
+  *ws = static_cast<char*>(t.data_ptr()) + kAnswerBytes;
+  t.unsafeGetTensorImpl()->set_sizes_contiguous({1});
+  return t;
+}
+
 int* int_ptr(const at::Tensor& t) { return static_cast<int*>(t.data_ptr()); }
 
 // (page_table, lens, refs, add, page_size)
@@ -326,9 +337,10 @@ PyObject* pages_reserve(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor* add = tensor(a[3]);
     if (list(add, device) != t.B) return none();
     size_t size;
-    at::Tensor ws = pages_workspace(t.num_pages, 0, device, &size), missing = make({1}, at::kInt, device);
+    char* ws;
+    at::Tensor missing = answer_and_workspace(t.num_pages, 0, device, &ws, &size);
     const fa2_stream_t s = stream_of(device);
-    const int rc = call([&] { return reserve_fn(&t, int_ptr(*add), int_ptr(missing), ws.data_ptr(), size, s); });
+    const int rc = call([&] { return reserve_fn(&t, int_ptr(*add), int_ptr(missing), ws, size, s); });
     return result(rc, std::move(missing));
   });
 }
@@ -348,11 +360,11 @@ PyObject* pages_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t count = list(src, device);
     if (count < 0 || list(dst, device) != count) return none();
     size_t size;
-    at::Tensor ws = pages_workspace(t.num_pages, static_cast<int>(count), device, &size);
-    at::Tensor missing = make({1}, at::kInt, device);
+    char* ws;
+    at::Tensor missing = answer_and_workspace(t.num_pages, static_cast<int>(count), device, &ws, &size);
     const fa2_stream_t s = stream_of(device);
     const int rc = call([&] {
-      return fork_fn(&t, &d, int_ptr(*src), int_ptr(*dst), static_cast<int>(count), int_ptr(missing), ws.data_ptr(), size, s);
+      return fork_fn(&t, &d, int_ptr(*src), int_ptr(*dst), static_cast<int>(count), int_ptr(missing), ws, size, s);
     });
     return result(rc, std::move(missing));
   });

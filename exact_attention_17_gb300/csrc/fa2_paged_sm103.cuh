@@ -216,13 +216,27 @@ struct PagedPlace {
   }
 };
 
+// Lane b: sequence b, one of the first 32, and the cost of its blocks.
+struct PagedFirst {
+  PagedSeq s;
+  long long cost;
+};
+
+template <int SUBS>
+__device__ __forceinline__ PagedFirst paged_first(const PagedParams& p) {
+  PagedFirst f;
+  f.s = paged_seq(p, threadIdx.x & 31, p.sub_tokens * SUBS);
+  f.cost = cost_before<SUBS>(p, f.s, f.s.blocks);
+  return f;
+}
+
 // Whole warp: the length of one of p.ctas equal ranges of the list, at least an
 // item's fixed cost and one tile, so that an item's inner ranges all have tiles;
 // and the length of the list.
 template <int SUBS>
-__device__ __forceinline__ long long paged_share(const PagedParams& p, long long* total) {
-  long long sum = 0;
-  for (int b = threadIdx.x & 31; b < p.B; b += 32) {
+__device__ __forceinline__ long long paged_share(const PagedParams& p, const PagedFirst& f, long long* total) {
+  long long sum = f.cost;
+  for (int b = (threadIdx.x & 31) + 32; b < p.B; b += 32) {
     const PagedSeq s = paged_seq(p, b, p.sub_tokens * SUBS);
     sum += cost_before<SUBS>(p, s, s.blocks);
   }
@@ -235,13 +249,13 @@ __device__ __forceinline__ long long paged_share(const PagedParams& p, long long
 
 // Whole warp: the item that position `pos` (below the list's length) lies in.
 template <int SUBS>
-__device__ __forceinline__ PagedPlace paged_find(const PagedParams& p, long long pos) {
+__device__ __forceinline__ PagedPlace paged_find(const PagedParams& p, const PagedFirst& f, long long pos) {
   const int lane = threadIdx.x & 31;
   PagedPlace w = {};
   long long before = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const PagedSeq s = paged_seq(p, b0 + lane, p.sub_tokens * SUBS);
-    const long long per_head = cost_before<SUBS>(p, s, s.blocks);
+    const PagedSeq s = b0 == 0 ? f.s : paged_seq(p, b0 + lane, p.sub_tokens * SUBS);
+    const long long per_head = b0 == 0 ? f.cost : cost_before<SUBS>(p, s, s.blocks);
     const long long mine = per_head * p.Hkv, sum = warp_scan(mine) + before;
     const unsigned here = __ballot_sync(0xffffffffu, pos >= sum - mine && pos < sum);
     if (here == 0) {
@@ -353,11 +367,12 @@ template <int SUBS>
 __device__ __forceinline__ PagedWalk paged_walk(const PagedParams& p, int cta) {
   PagedWalk w;
   long long total;
-  const long long share = paged_share<SUBS>(p, &total);
+  const PagedFirst f = paged_first<SUBS>(p);
+  const long long share = paged_share<SUBS>(p, f, &total);
   w.cta = cta;
   w.lo = cta * share;
   w.hi = cta < p.ctas ? min(w.lo + share, total) : w.lo;
-  if (w.lo < w.hi) w.at = paged_find<SUBS>(p, w.lo);
+  if (w.lo < w.hi) w.at = paged_find<SUBS>(p, f, w.lo);
   return w;
 }
 
@@ -375,10 +390,11 @@ __device__ __forceinline__ PagedParts paged_parts_even(const PagedParams& p, int
   PagedParts r;
   r.u.valid = 0;
   long long total;
-  const long long share = paged_share<SUBS>(p, &total);
+  const PagedFirst f = paged_first<SUBS>(p);
+  const long long share = paged_share<SUBS>(p, f, &total);
   const long long pos = (index + 1ll) * share;
   if (index + 1 >= p.ctas || pos >= total) return r;
-  const PagedPlace w = paged_find<SUBS>(p, pos);
+  const PagedPlace w = paged_find<SUBS>(p, f, pos);
   const int t = w.tile(pos);
   if (t == 0 || t == w.tiles || w.tile(pos - share) > 0) return r;
   r.u = paged_unit(p, w.s, w.b, w.head, p.sub_tokens * SUBS, w.i);
@@ -1302,13 +1318,13 @@ constexpr int kPagedMergeMany = 6;    // parts from which the warps of a block s
 // column share its rows, eight rows a warp: lane = (row, 4 of 16 columns), so
 // that reads are 128 and writes 32 neighbouring bytes at least.  With m = max_s
 // L_s and w_s = exp(L_s - m): O = sum_s w_s O_s / sum w_s, LSE = m + log sum w_s;
-// parts with L_s = -inf have w_s = 0 and their O is not read.  An item of many
+// parts with L_s = -inf have w_s = 0 and their O is not used.  An item of many
 // parts has few rows (it was cut because there were few items): its block's
 // warps take every fourth part each and add up through shared memory.
 template <int D, bool F16, int SUBS>
 __global__ void __launch_bounds__(kPagedMergeWarps * 32) fa2_paged_merge_kernel(const __grid_constant__ PagedParams p) {
   __shared__ float4 sums[kPagedMergeWarps - 1][D / 16][32];
-  __shared__ float weights[kPagedMergeWarps - 1][32];
+  __shared__ float2 weights[kPagedMergeWarps - 1][32];
   const int index = static_cast<int>(blockIdx.x);
   const PagedParts w = p.even ? paged_parts_even<SUBS>(p, index) : paged_item<SUBS>(p, index, true, D);
   // launched while the partial results are computed: they are complete from here on
@@ -1323,28 +1339,33 @@ __global__ void __launch_bounds__(kPagedMergeWarps * 32) fa2_paged_merge_kernel(
     const int row = (g0 + (share ? 0 : warp)) * kPagedMergeRows + (lane & 7), group = lane >> 3;
     const bool live = row < rows;
     auto slot = [&](int s) { return static_cast<long long>(s == 0 ? w.first : w.rest + (s - 1) * w.step); };
+    // One pass, the parts' loads independent of each other: m is the running
+    // maximum, sums are scaled when it moves.
     const float* L = p.LSE_part + (live ? row : 0);
-    float mx = -INFINITY;
-#pragma unroll 4
-    for (int s = 0; s < w.parts; ++s) mx = fmaxf(mx, L[slot(s) * p.part_rows]);
+    const float* O = p.O_part + static_cast<long long>(group) * p.part_rows * 4 + (live ? row : 0) * 4;
     float4 acc[D / 16];
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
+    float sum = 0.f, m = -INFINITY;
 #pragma unroll 2
     for (int s = first; s < w.parts; s += step) {
-      const float ls = L[slot(s) * p.part_rows];
-      if (!live || ls == -INFINITY) continue;
-      const float e = expf(ls - mx);
-      sum += e;
-      const float* src = p.O_part + (slot(s) * (D / 4) + group) * p.part_rows * 4 + row * 4;
+      const long long at = slot(s) * p.part_rows;
+      const float ls = L[at];
+      float4 x[D / 16];
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+        x[c] = *reinterpret_cast<const float4*>(O + at * D + static_cast<long long>(c) * 16 * p.part_rows);
+      const float top = fmaxf(m, ls);
+      const float keep = m == -INFINITY ? 0.f : expf(m - top), e = ls == -INFINITY ? 0.f : expf(ls - top);
+      m = top;
+      sum = fmaf(sum, keep, e);
+      const bool has = e != 0.f;   // (the O of a part without keys was not written)
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
-        const float4 x = *reinterpret_cast<const float4*>(src + static_cast<long long>(c) * 16 * p.part_rows);
-        acc[c].x = fmaf(e, x.x, acc[c].x);
-        acc[c].y = fmaf(e, x.y, acc[c].y);
-        acc[c].z = fmaf(e, x.z, acc[c].z);
-        acc[c].w = fmaf(e, x.w, acc[c].w);
+        acc[c].x = fmaf(acc[c].x, keep, has ? e * x[c].x : 0.f);
+        acc[c].y = fmaf(acc[c].y, keep, has ? e * x[c].y : 0.f);
+        acc[c].z = fmaf(acc[c].z, keep, has ? e * x[c].z : 0.f);
+        acc[c].w = fmaf(acc[c].w, keep, has ? e * x[c].w : 0.f);
       }
     }
     if (share) {
@@ -1352,20 +1373,24 @@ __global__ void __launch_bounds__(kPagedMergeWarps * 32) fa2_paged_merge_kernel(
       if (warp > 0) {
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) sums[warp - 1][c][lane] = acc[c];
-        weights[warp - 1][lane] = sum;
+        weights[warp - 1][lane] = make_float2(m, sum);
       }
       __syncthreads();
       if (warp > 0) continue;
 #pragma unroll
       for (int x = 0; x < kPagedMergeWarps - 1; ++x) {
-        sum += weights[x][lane];
+        const float2 other = weights[x][lane];
+        const float top = fmaxf(m, other.x);
+        const float keep = m == -INFINITY ? 0.f : expf(m - top), e = other.x == -INFINITY ? 0.f : expf(other.x - top);
+        m = top;
+        sum = fmaf(sum, keep, e * other.y);
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
           const float4 y = sums[x][c][lane];
-          acc[c].x += y.x;
-          acc[c].y += y.y;
-          acc[c].z += y.z;
-          acc[c].w += y.w;
+          acc[c].x = fmaf(acc[c].x, keep, e * y.x);
+          acc[c].y = fmaf(acc[c].y, keep, e * y.y);
+          acc[c].z = fmaf(acc[c].z, keep, e * y.z);
+          acc[c].w = fmaf(acc[c].w, keep, e * y.w);
         }
       }
     }
@@ -1383,7 +1408,7 @@ __global__ void __launch_bounds__(kPagedMergeWarps * 32) fa2_paged_merge_kernel(
       else
         *reinterpret_cast<float4*>(static_cast<float*>(p.O) + at) = x;
     }
-    if (group == 0) p.LSE[out] = sum == 0.f ? -INFINITY : mx + logf(sum);
+    if (group == 0) p.LSE[out] = sum == 0.f ? -INFINITY : m + logf(sum);
   }
 }
 

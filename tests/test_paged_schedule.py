@@ -34,7 +34,7 @@ class Batch:
         self.kv = [rng.choice([0, rng.randint(0, 20000 if long_items else 5000)]) for _ in range(n)]
         self.blocks = [-(-x // self.block) for x in self.q]
         self.ctas = rng.choice([4, 152, 304])
-        self.min_tiles = 2
+        self.min_tiles = 1
 
     def keys(self, b, i):
         return max(1, kept(self.causal, self.kv[b], self.q[b], min((i + 1) * self.block, self.q[b]) - 1))
