@@ -111,6 +111,12 @@ constexpr int kItemWaves = 4;
 // Least key tiles of a range: two single tokens over 1000 keys take 16.5 us with
 // one, 18.3 with two, 20.5 with four and 26.6 with eight.
 constexpr int kMinTiles = 1;
+// What an item costs besides its keys (pipeline fill, epilogue), in keys.  Of
+// 128, 256, 384, 512 and 768: ragged chunks of 12 sequences take 68.8, 60.1, 59.4,
+// 57.6 and 60.7 us, two single tokens over 1000 keys (a range is at least an
+// item's cost and a tile) 17.2, 16.5, 18.4, 19.8 and 22.5.
+constexpr int kItemKeys = 512;
+constexpr int kItemKeysNarrow = 256;
 
 // Sub-tiles per CTA: two (256 rows on one K/V stream) where the sequences'
 // average chunk fills more than one sub-tile, else one with two CTAs per SM, of
@@ -222,6 +228,7 @@ extern "C" int fa2_forward_paged(const fa2_paged_cache* cache, const void* Q, lo
   p.ctas = plan.ctas;
   p.inv_ctas = 1.0 / plan.ctas;
   p.min_tiles = kMinTiles;
+  p.item_keys = plan.narrow ? kItemKeysNarrow : kItemKeys;
   p.causal = causal != 0;
   p.o_half = half_out ? 1 : 0;
   p.narrow = plan.narrow ? 1 : 0;

@@ -86,6 +86,7 @@ struct PagedParams {
   int ctas;                // even: ranges; else the number of equal shares above which an item is cut
   double inv_ctas;
   int min_tiles;           // least key tiles per range
+  int item_keys;           // what an item costs besides its keys, in keys
   int causal;
   int o_half;
   int narrow;              // blocks of at most 32 rows
@@ -136,13 +137,11 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b, int b
   return s;
 }
 
-// Cost of an item: kKeysPerItem for its start and end, then its keys, at least
-// one (a lone sub-tile takes about as long as two, whose MMAs and softmax
-// overlap).  Sums of costs over a sequence's blocks are closed forms in keys,
-// which tiles would not be; a position x inside an item stands for tile ceil((x
-// - kKeysPerItem) / 128), cut to the item's tiles.
-constexpr int kKeysPerItem = 256;
-
+// Cost of an item: item_keys for its start and end, then its keys, at least one (a
+// lone sub-tile takes about as long as two, whose MMAs and softmax overlap).
+// Sums of costs over a sequence's blocks are closed forms in keys, which tiles
+// would not be; a position x inside an item stands for tile ceil((x - item_keys) /
+// 128), cut to the item's tiles.
 __device__ __forceinline__ int block_keys(const PagedParams& p, const PagedSeq& s, int block, int i) {
   return max(1, paged_kept(p.causal, s.kv_len, s.q_len, min((i + 1) * block, s.q_len) - 1));
 }
@@ -163,7 +162,7 @@ __device__ __forceinline__ long long cost_before(const PagedParams& p, const Pag
   } else {
     keys = static_cast<long long>(full) * max(1, s.kv_len);
   }
-  keys += static_cast<long long>(i) * kKeysPerItem;
+  keys += static_cast<long long>(i) * p.item_keys;
   if (i == s.blocks) keys += max(1, s.kv_len);
   return keys;
 }
@@ -202,8 +201,8 @@ struct PagedPlace {
   PagedSeq s;
 
   // the item's tile at position `pos` of the list
-  __device__ __forceinline__ int tile(long long pos) const {
-    const long long x = pos - start - kKeysPerItem;
+  __device__ __forceinline__ int tile(const PagedParams& p, long long pos) const {
+    const long long x = pos - start - p.item_keys;
     if (x <= 0) return 0;
     if (pos >= start + cost) return tiles;
     return min(tiles, key_tiles_of(static_cast<int>(x)));
@@ -212,7 +211,7 @@ struct PagedPlace {
   __device__ __forceinline__ void measure(const PagedParams& p) {
     const int keys = block_keys(p, s, p.sub_tokens * SUBS, i);
     tiles = key_tiles_of(keys);
-    cost = kKeysPerItem + keys;
+    cost = p.item_keys + keys;
   }
 };
 
@@ -244,7 +243,7 @@ __device__ __forceinline__ long long paged_share(const PagedParams& p, const Pag
   *total = sum;
   // total / ctas rounded up (the 64-bit product is off by less than one), so that the ranges cover the list
   const long long share = static_cast<long long>(static_cast<double>(sum) * p.inv_ctas) + 2;
-  return max(share, static_cast<long long>(p.min_tiles) * kKeysPerTile + kKeysPerItem);
+  return max(share, static_cast<long long>(p.min_tiles) * kKeysPerTile + p.item_keys);
 }
 
 // Whole warp: the item that position `pos` (below the list's length) lies in.
@@ -322,7 +321,7 @@ struct PagedWalk {
     PagedUnit u;
     u.valid = 0;
     while (lo < hi && !u.valid) {
-      const int from = at.tile(lo), to = at.tile(hi);
+      const int from = at.tile(p, lo), to = at.tile(p, hi);
       if (from < to) {
         u = paged_unit(p, at.s, at.b, at.head, p.sub_tokens * SUBS, at.i);
         u.t_begin = from;
@@ -395,14 +394,14 @@ __device__ __forceinline__ PagedParts paged_parts_even(const PagedParams& p, int
   const long long pos = (index + 1ll) * share;
   if (index + 1 >= p.ctas || pos >= total) return r;
   const PagedPlace w = paged_find<SUBS>(p, f, pos);
-  const int t = w.tile(pos);
-  if (t == 0 || t == w.tiles || w.tile(pos - share) > 0) return r;
+  const int t = w.tile(p, pos);
+  if (t == 0 || t == w.tiles || w.tile(p, pos - share) > 0) return r;
   r.u = paged_unit(p, w.s, w.b, w.head, p.sub_tokens * SUBS, w.i);
   r.first = 2 * index + 1;
   r.rest = 2 * (index + 1);
   r.step = 2;
   r.parts = 2;
-  for (long long next = pos + share; next < total && w.tile(next) < w.tiles; next += share) ++r.parts;
+  for (long long next = pos + share; next < total && w.tile(p, next) < w.tiles; next += share) ++r.parts;
   return r;
 }
 

@@ -12,7 +12,7 @@ import random
 
 import pytest
 
-KEYS, PER_ITEM = 128, 256   # keys of a tile, an item's fixed cost in keys
+KEYS = 128   # keys of a tile
 
 
 def tiles_of(keys):
@@ -35,6 +35,7 @@ class Batch:
         self.blocks = [-(-x // self.block) for x in self.q]
         self.ctas = rng.choice([4, 152, 304])
         self.min_tiles = 1
+        self.per_item = rng.choice([256, 512])   # an item's fixed cost in keys
 
     def keys(self, b, i):
         return max(1, kept(self.causal, self.kv[b], self.q[b], min((i + 1) * self.block, self.q[b]) - 1))
@@ -51,14 +52,14 @@ class Batch:
             keys = none + n * (lead + none * self.block) + self.block * (n * (n + 1) // 2)
         else:
             keys = full * max(1, self.kv[b])
-        keys += i * PER_ITEM
+        keys += i * self.per_item
         return keys + (max(1, self.kv[b]) if i == self.blocks[b] else 0)
 
     def total(self):
         return sum(self.cost_before(b, self.blocks[b]) for b in range(len(self.q))) * self.heads
 
     def share(self):
-        return max(int(self.total() * (1.0 / self.ctas)) + 2, self.min_tiles * KEYS + PER_ITEM)
+        return max(int(self.total() * (1.0 / self.ctas)) + 2, self.min_tiles * KEYS + self.per_item)
 
     def find(self, pos):
         """[sequence, head, block, start of the item] that the position lies in."""
@@ -82,10 +83,10 @@ class Batch:
     def tile(self, item, pos):
         b, _, i, start = item
         keys = self.keys(b, i)
-        x = pos - start - PER_ITEM
+        x = pos - start - self.per_item
         if x <= 0:
             return 0
-        return tiles_of(keys) if pos >= start + PER_ITEM + keys else min(tiles_of(keys), tiles_of(x))
+        return tiles_of(keys) if pos >= start + self.per_item + keys else min(tiles_of(keys), tiles_of(x))
 
     def walk(self, cta):
         """Segments (item, first tile, last tile, slot) of a range."""
@@ -99,7 +100,7 @@ class Batch:
             if first < last:
                 whole = tiles_of(self.keys(at[0], at[2]))
                 yield tuple(at[:3]), first, last, 2 * cta if first > 0 else 2 * cta + 1 if last < whole else -1
-            at[3] += PER_ITEM + self.keys(at[0], at[2])
+            at[3] += self.per_item + self.keys(at[0], at[2])
             lo = max(lo, at[3])
             at[2] += 1
             if at[2] == self.blocks[at[0]]:
@@ -135,7 +136,7 @@ def test_equal_ranges_cover_every_item_once(seed):
     batch = Batch(rng)
     for b, n in enumerate(batch.blocks):
         for i in range(n + 1):
-            assert batch.cost_before(b, i) == sum(PER_ITEM + batch.keys(b, k) for k in range(i))
+            assert batch.cost_before(b, i) == sum(batch.per_item + batch.keys(b, k) for k in range(i))
     if batch.total() == 0:
         return
     assert batch.share() * batch.ctas >= batch.total()
