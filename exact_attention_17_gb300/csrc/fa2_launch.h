@@ -16,8 +16,8 @@ namespace fa2host {
 
 // Launches a kernel that may start while the one before it on the stream still
 // runs; it waits for that one (griddepcontrol.wait) before it reads its results.
-template <typename Kernel, typename Params>
-cudaError_t launch_behind(Kernel kernel, dim3 grid, int threads, cudaStream_t s, const Params& p) {
+template <typename... Params, typename... Args>
+cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t s, const Args&... args) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -27,7 +27,7 @@ cudaError_t launch_behind(Kernel kernel, dim3 grid, int threads, cudaStream_t s,
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // Raise the dynamic shared-memory limit of every kernel in the unit (current device).

@@ -10,9 +10,10 @@
 //
 // Each operation is one planning block, which ranks pages by ballots over
 // chunks of the reference counts, and where page data moves a copy kernel
-// behind it on the same stream, which reads the planned list: nothing returns
-// to the host.  Bound: planning by the latency of one block's passes over refs,
+// behind it on the same stream (made ready while the block plans), which reads
+// the planned list: nothing returns to the host.  Bound: planning by the latency of one block's passes over refs,
 // copying by bytes (each page read and written once).
+#include "fa2_launch.h"
 #include "fa2_pages.h"
 
 namespace fa2dev {
@@ -153,6 +154,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 // nothing to copy), then n new lengths.
 __global__ void __launch_bounds__(kPlanThreads)
     fa2_pages_fork_kernel(const PageTables t, const int* src, const int* dst, int n, int* missing, int* pairs) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the copies may be made ready
   __shared__ int warp_sums[kPlanWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int* from = pairs + 1;
@@ -290,6 +292,7 @@ __global__ void __launch_bounds__(128) fa2_pages_free_kernel(const PageTables t,
 // pairs as in fork: pages of number >= used (the count of used pages) go to the
 // free numbers below it, in ascending order.
 __global__ void __launch_bounds__(kPlanThreads) fa2_pages_compact_kernel(const PageTables t, int* moved, int* pairs) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the copies may be made ready
   __shared__ int warp_sums[kPlanWarps];
   int* from = pairs + 1;
   int* to = from + t.num_pages;
@@ -324,6 +327,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa2_pages_compact_kernel(const P
 // whose source another pair writes is refused.
 __global__ void __launch_bounds__(256)
     fa2_pages_pairs_kernel(const int* src, const int* dst, int n, int num_pages, int* pairs, int* status) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the copies may be made ready
   const int lane = threadIdx.x & 31;
   const int i = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   if (blockIdx.x == 0 && threadIdx.x == 0) pairs[0] = n;
@@ -353,7 +357,10 @@ constexpr int kCopyChunk = kCopyThreads * kCopyPer * 16;
 // The listed pairs of every plane, chunk by chunk; and, when `moved` is given,
 // the table entries renamed by it.
 __global__ void __launch_bounds__(kCopyThreads)
-    fa2_pages_copy_kernel(const PagePlanes d, const int* pairs, int room, PageTables t, const int* moved) {
+    fa2_pages_copy_kernel(const __grid_constant__ PagePlanes d, const int* pairs, int room, const PageTables t,
+                          const int* moved) {
+  // launched while the list is planned: it is there from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n = min(pairs[0], room);
   const int* from = pairs + 1;
   const int* to = from + room;
@@ -425,8 +432,8 @@ cudaError_t launch_pages_fork(const PageTables& t, const int* src, const int* ds
   fa2_pages_fork_kernel<<<1, kPlanThreads, 0, s>>>(t, src, dst, n, missing, ws);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  fa2_pages_copy_kernel<<<copy_grid(n, d, sms), kCopyThreads, 0, s>>>(d, ws, n, t, nullptr);
-  return cudaGetLastError();
+  return launch_behind(fa2_pages_copy_kernel, dim3(copy_grid(n, d, sms)), kCopyThreads, s, d, ws, n, t,
+                       static_cast<const int*>(nullptr));
 }
 
 cudaError_t launch_pages_free(const PageTables& t, const int* seqs, int n, cudaStream_t s) {
@@ -439,8 +446,8 @@ cudaError_t launch_pages_compact(const PageTables& t, const PagePlanes& d, int* 
   fa2_pages_compact_kernel<<<1, kPlanThreads, 0, s>>>(t, moved, ws);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  fa2_pages_copy_kernel<<<copy_grid(t.num_pages, d, sms), kCopyThreads, 0, s>>>(d, ws, t.num_pages, t, moved);
-  return cudaGetLastError();
+  return launch_behind(fa2_pages_copy_kernel, dim3(copy_grid(t.num_pages, d, sms)), kCopyThreads, s, d, ws, t.num_pages,
+                       t, moved);
 }
 
 cudaError_t launch_pages_copy(const PagePlanes& d, const int* src, const int* dst, int n, int* ws, int* status,
@@ -449,8 +456,8 @@ cudaError_t launch_pages_copy(const PagePlanes& d, const int* src, const int* ds
   fa2_pages_pairs_kernel<<<blocks, 256, 0, s>>>(src, dst, n, d.num_pages, ws, status);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  fa2_pages_copy_kernel<<<copy_grid(n, d, sms), kCopyThreads, 0, s>>>(d, ws, n, PageTables{}, nullptr);
-  return cudaGetLastError();
+  return launch_behind(fa2_pages_copy_kernel, dim3(copy_grid(n, d, sms)), kCopyThreads, s, d, ws, n, PageTables{},
+                       static_cast<const int*>(nullptr));
 }
 
 }  // namespace fa2host
