@@ -36,9 +36,10 @@
 //    part.  With `even` the list of all items is cut into ranges of equal cost,
 //    one per CTA of a single wave: a CTA walks its range segment by segment, at
 //    most its first and last segment being parts of an item.
-//    Without it (many items, the host's choice) a CTA takes one item, in an
-//    order that keeps a group of heads in L2, items of more than an even share
-//    of the tiles being cut.  A part's normalised O and LSE go to the workspace,
+//    Without it (many items, the host's choice) the CTAs take whole items one
+//    after the other from a counter, in an order that keeps a group of heads in
+//    L2, items of more than an even share of the tiles being cut; who computes
+//    an item does not change it.  A part's normalised O and LSE go to the workspace,
 //    and a second kernel merges them (as fa2_combine.cu, in the order of the
 //    keys: results do not depend on timing).
 //  * Producers.  The tiled copies that one warp issues run one after the other:
@@ -82,8 +83,9 @@ struct PagedParams {
   int table_width;
   long long table_stride;
   int max_len;             // table_width << page_log2, at most 2^30
-  int even;                // equal ranges of the work, one per CTA (else one item per CTA)
-  int ctas;                // even: ranges; else the number of equal shares above which an item is cut
+  int even;                // equal ranges of the work, one per CTA (else whole items)
+  int ctas;                // CTAs of the grid; an item of more than one CTA's share is cut
+  int* counter;            // whole items: how many CTAs have taken besides their first (starts at 0)
   double inv_ctas;
   int min_tiles;           // least key tiles per range
   int item_keys;           // what an item costs besides its keys, in keys
@@ -307,7 +309,7 @@ __device__ __forceinline__ PagedUnit paged_unit(const PagedParams& p, const Page
   return u;
 }
 
-// Whole warp: walks the segments of range `cta`.  A part that begins inside an
+// Whole warp: walks the segments of range `cta` (even).  A part that begins inside an
 // item goes to slot 2 cta, one that begins it and does not end it to slot 2 cta
 // + 1: a range has at most one of each.
 struct PagedWalk {
@@ -445,7 +447,7 @@ struct PageCursor {
 // Bytes of one head's K and V that a group of heads may hold in L2 together.
 constexpr long long kPagedL2Bytes = 64ll << 20;
 
-// Whole warp, one item per CTA: unit `index` (items = false), or the item of
+// Whole warp, items from a counter: unit `index` (items = false), or the item of
 // rank `index` among those cut into several units (items = true; its parts are
 // in slots first, first + 1, ...).
 template <int SUBS>
@@ -679,13 +681,19 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
     if (warp == kWarpProducer) {
       // ------------------------------------------------------------ schedule and copies
       PagedWalk walk;
-      PagedUnit w;
-      if (p.even) {
-        walk = paged_walk<SUBS>(p, static_cast<int>(blockIdx.x));
-        w = walk.next<SUBS>(p);
-      } else {
-        w = paged_item<SUBS>(p, static_cast<int>(blockIdx.x), false, D).u;
-      }
+      bool begun = false;
+      auto next_unit = [&]() {
+        if (NARROW || p.even) return walk.next<SUBS>(p);   // (narrow blocks always have equal ranges)
+        int index = blockIdx.x;   // the first unit by number, the others as CTAs become free
+        if (begun) {
+          if (lane == 0) index = gridDim.x + atomicAdd(p.counter, 1);
+          index = __shfl_sync(0xffffffffu, index, 0);
+        }
+        begun = true;
+        return paged_item<SUBS>(p, index, false, D).u;
+      };
+      if (NARROW || p.even) walk = paged_walk<SUBS>(p, static_cast<int>(blockIdx.x));
+      PagedUnit w = next_unit();
       int tiles = 0, loads = 0;   // tiles of the segments before; Q loads
       bool ok = true;
       for (int k = 0;; ++k) {
@@ -737,10 +745,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
             copy(Int<0>{}, Int<NCH>{}, w, pages, w.t_begin + (i >> 1), 2 * tiles + i, ok);
         }
         tiles += n;
-        if (p.even)
-          w = walk.next<SUBS>(p);
-        else
-          w.valid = 0;
+        w = next_unit();
       }
       if (lane == 0 && loads > 0) {
         volatile int never = 0;

@@ -335,9 +335,10 @@ cudaError_t launch_rope(RopeParams p, bool append, int dtype, bool wide, int sms
   const long long tiles = (p.total_tokens + p.tokens - 1) / p.tokens;
   if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
   // Heads of a block: all of them, so that the sines are computed once, unless
-  // that leaves fewer than four blocks an SM; then as few as it takes, at least
-  // one unrolled step.
-  long long chunks = (4ll * sms + tiles - 1) / tiles;
+  // that leaves fewer than two blocks an SM; then as few as it takes, at least one
+  // unrolled step.  (10460 tokens of 40 rows in 327 blocks: 24.6 us; two, four and
+  // eight times the blocks: 27.4, 30.7 and 45.1.)
+  long long chunks = (2ll * sms + tiles - 1) / tiles;
   const long long most = (p.total_rows + fa2dev::kRopeUnroll - 1) / fa2dev::kRopeUnroll;
   if (chunks > most) chunks = most;
   if (chunks > 65535) chunks = 65535;
