@@ -45,15 +45,20 @@
 //  * Producers.  The tiled copies that one warp issues run one after the other:
 //    20.8 bytes per clock in boxes of 16 KB (a 128-byte row in 6 clocks), 14.0 in
 //    boxes of 2 KB, whichever lanes issue them; two warps reach 40.5, four 75 to
-//    82.  One warp keeps up with the tiles of head dimensions 64 and 128 (a warp
-//    each for K and V was 3 to 6% slower).  At 256 a tile is 64 KB, and with
-//    room for one of K and one of V a copy starts only when the MMAs of the tile
-//    before are done: three warps share each tile there (200 -> 171 us for 2600
-//    tokens over 2000-4096 keys when K had two warps and V one).
+//    82.  Two 128-row sub-tiles take a 64 KB key tile in about 3000 clocks at head
+//    dimension 128, more than one warp delivers in small pages: two warps share
+//    each tile there, by columns (8192 tokens over 16384 keys in pages of 16, 32
+//    and 128: 1327, 1180 and 1173 -> 1141, 1116 and 1117 us; a warp each for K and
+//    V was slower than one).  At 256 a tile is 64 KB, and with room for one of K
+//    and one of V a copy starts only when the MMAs of the tile before are done:
+//    three warps share each tile (200 -> 171 us for 2600 tokens over 2000-4096
+//    keys when K had two warps and V one).
 //  * Segments.  The producer warp runs ahead: it loads the next segment's Q and
 //    first tiles while the current one finishes.  One named barrier per segment,
 //    which every role passes for every segment, also after an abort, hands over
-//    the segment's description.
+//    the segment's description (the other producers have one of their own, ahead
+//    of it).  A ring of descriptions that each role reads at its own pace was
+//    slower: 1115 -> 1158 us for those 8192 tokens.
 #pragma once
 
 #include <type_traits>
@@ -517,7 +522,8 @@ using Int = std::integral_constant<int, N>;
 
 // Named barrier of the segments (kBarP0 and kBarP1 are the dense kernel's).
 constexpr int kBarSegment = 3;
-constexpr int kBarShares = 4;   // the softmax warps, while they merge their shares
+constexpr int kBarShares = 4;      // the softmax warps, while they merge their shares
+constexpr int kBarProducers = 5;   // the producers, at a segment's description
 
 template <int D, int SUBS>
 struct PagedConfig : FwdConfig<D, SUBS> {
@@ -536,10 +542,11 @@ struct PagedConfig : FwdConfig<D, SUBS> {
   static constexpr int kProducer = 72;
   static_assert(SUBS * 128 * kSoftmax + 128 * kProducer <= FwdShape<SUBS>::kLaunch * FwdShape<SUBS>::kThreads,
                 "register rebalancing exceeds the launch allocation");
-  // Three producer warps, each with its 64-column chunks of every K and V tile.
-  static constexpr bool kThree = D == 256;
-  // every role: softmax, producer and MMA warps, and the watcher or the other two producers where there are any
-  static constexpr int kSegmentThreads = SUBS * 128 + 64 + (Base::kNamedP ? 32 : kThree ? 64 : 0);
+  // Producer warps, each with its 64-column chunks of every K and V tile.
+  static constexpr bool kThree = D == 256, kTwo = D == 128 && SUBS == 2;
+  static constexpr int kProducers = kThree ? 3 : kTwo ? 2 : 1;
+  // softmax, first producer and MMA warps, and the watcher where there is one
+  static constexpr int kSegmentThreads = SUBS * 128 + 64 + (Base::kNamedP ? 32 : 0);
 };
 
 template <int STAGES>
@@ -649,7 +656,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
     bar_init(&bars->q_full, 1);
     bar_init(&shared->q_empty, 1);
     for (int s = 0; s < STAGES; ++s) {
-      bar_init(&bars->kv_full[s], Cfg::kThree ? 3 : 1);
+      bar_init(&bars->kv_full[s], Cfg::kProducers);
       bar_init(&bars->kv_empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -680,6 +687,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
     regs_decrease<Cfg::kProducer>();
     if (warp == kWarpProducer) {
       // ------------------------------------------------------------ schedule and copies
+      constexpr int kMine = Cfg::kThree ? 2 : Cfg::kTwo ? 1 : NCH;   // chunks of K that this warp copies
       PagedWalk walk;
       bool begun = false;
       auto next_unit = [&]() {
@@ -699,6 +707,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
       for (int k = 0;; ++k) {
         if (lane == 0) shared->unit[k & 1] = w;
         __syncwarp();
+        if (Cfg::kProducers > 1) named_sync(kBarProducers, Cfg::kProducers * 32);
         int n = 0;
         if (w.valid) {
           n = tiles_for(w, 0);
@@ -708,9 +717,10 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
         // Ahead of the hand-over: the first copies, which do not wait for the
         // last V of the segment before (its slot comes STAGES - 1 copies
         // later), and Q, once the last S of the segment before is complete.
-        const int early = min(STAGES - 1, 2 * n);
+        // (The first segment is handed over at once.)
+        const int early = k == 0 ? min(1, n) : min(STAGES - 1, 2 * n);
         for (int i = 0; i < early; ++i) {
-          copy(Int<0>{}, Int<Cfg::kThree ? 2 : NCH>{}, w, pages, w.t_begin + (i >> 1), 2 * tiles + i, ok);
+          copy(Int<0>{}, Int<kMine>{}, w, pages, w.t_begin + (i >> 1), 2 * tiles + i, ok);
           if (i == 0) {
             if (loads > 0) warp_wait(&shared->q_empty, (loads - 1) & 1, ok);
             if (ok) {
@@ -742,7 +752,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
           copy_three(Int<0>{}, Int<2>{}, Int<0>{}, Int<1>{}, w, n, tiles, pages, v_pages, 1, ok);
         } else {
           for (int i = early; i < 2 * n && ok; ++i)
-            copy(Int<0>{}, Int<NCH>{}, w, pages, w.t_begin + (i >> 1), 2 * tiles + i, ok);
+            copy(Int<0>{}, Int<kMine>{}, w, pages, w.t_begin + (i >> 1), 2 * tiles + i, ok);
         }
         tiles += n;
         w = next_unit();
@@ -753,20 +763,27 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
       }
       drain();
       __syncwarp();
-    } else if (warp != kWarpMma && Cfg::kThree) {
-      // ------------------------------------------------------------ the second and third producer
+    } else if (Cfg::kThree ? warp != kWarpMma : Cfg::kTwo && warp == kWarpWatch + 1) {
+      // ------------------------------------------------------------ the other producers
       int tiles = 0;
       bool ok = true;
       for (int k = 0;; ++k) {
-        named_sync(kBarSegment, Cfg::kSegmentThreads);
+        named_sync(kBarProducers, Cfg::kProducers * 32);
         const PagedUnit w = shared->unit[k & 1];
         if (!w.valid) break;
-        const int n = tiles_for(w, 0);
-        PageCursor pages(p, w, n), v_pages(p, w, n);
-        if (warp == kWarpMma + 1)
-          copy_three(Int<2>{}, Int<3>{}, Int<1>{}, Int<3>{}, w, n, tiles, pages, v_pages, 0, ok);
-        else
-          copy_three(Int<3>{}, Int<4>{}, Int<3>{}, Int<4>{}, w, n, tiles, pages, v_pages, 0, ok);
+        int n = tiles_for(w, 0);
+        if (SUBS == 2) n = max(n, tiles_for(w, 1));
+        PageCursor pages(p, w, n);
+        if constexpr (Cfg::kThree) {
+          PageCursor v_pages(p, w, n);
+          if (warp == kWarpMma + 1)
+            copy_three(Int<2>{}, Int<3>{}, Int<1>{}, Int<3>{}, w, n, tiles, pages, v_pages, 0, ok);
+          else
+            copy_three(Int<3>{}, Int<4>{}, Int<3>{}, Int<4>{}, w, n, tiles, pages, v_pages, 0, ok);
+        } else {
+          for (int i = 0; i < 2 * n && ok; ++i)
+            copy(Int<1>{}, Int<NCH>{}, w, pages, w.t_begin + (i >> 1), 2 * tiles + i, ok);
+        }
         tiles += n;
       }
       drain();
