@@ -106,10 +106,15 @@ struct PagedPlan {
 
 int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 
-// Blocks of queries that fill this many waves of CTAs are taken whole: 0.9 waves
-// (132 items) 67.8 us whole and 57.5 in equal ranges, 2.2 waves 160 and 167, 6.7
-// waves 1120 and 1220.
-constexpr int kItemWaves = 2;
+// Blocks of queries that fill this many waves of CTAs are taken whole: many at a
+// time then share keys in L2, where equal ranges spread over all heads at once,
+// but the last wave ends unevenly.  Over 90 ragged batches (time whole / equal
+// ranges): d <= 128, below 3 waves 0.83 to 1.60, mean 1.2; 3.5 to 7 waves 0.88 to
+// 1.18, mean 1.0, and 0.90 for 32 long heads at 6.7.  d = 256, whose blocks have
+// half the rows and whose tiles are twice as large: below 2 waves 0.80 to 1.45,
+// mean 1.1; above 0.77 to 1.07, mean 0.9.
+constexpr int kItemWaves = 4;
+constexpr int kItemWaves256 = 2;
 // Least key tiles of a range: two single tokens over 1000 keys take 16.5 us with
 // one, 18.3 with two, 20.5 with four and 26.6 with eight.
 constexpr int kMinTiles = 1;
@@ -136,7 +141,8 @@ PagedPlan plan_paged(int B, int T, int Hq, int Hkv, int d, bool has_cu, int sms)
   const int block = q.sub_tokens * q.subs;
   q.items = (has_cu ? T / block + static_cast<long long>(B < T ? B : T) : B) * Hkv;
   q.ctas = sms * (q.subs == 2 || d == 256 ? 1 : 2);
-  q.even = q.narrow || !has_cu || T / block * static_cast<long long>(Hkv) < kItemWaves * static_cast<long long>(q.ctas);
+  const long long waves = d == 256 ? kItemWaves256 : kItemWaves;
+  q.even = q.narrow || !has_cu || T / block * static_cast<long long>(Hkv) < waves * q.ctas;
   q.slots = 2 * q.ctas;
   const long long rows = static_cast<long long>(has_cu ? (T < block ? T : block) : 1) * q.G;
   q.part_rows = static_cast<int>(rows);
