@@ -15,15 +15,19 @@
 namespace fa2host {
 
 // Launches a kernel that may start while the one before it on the stream still
-// runs; it waits for that one (griddepcontrol.wait) before it reads its results.
+// runs (when that one allows it, griddepcontrol.launch_dependents).  Every block
+// waits for the one before to end (griddepcontrol.wait) before it reads or
+// writes what others may, so that "complete" reaches back along the stream.
 template <typename... Params, typename... Args>
-cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t s, const Args&... args) {
+cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int threads, unsigned smem, cudaStream_t s,
+                          const Args&... args) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;

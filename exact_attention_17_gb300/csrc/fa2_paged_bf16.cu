@@ -16,11 +16,18 @@ cudaError_t set_limits() {
 template <int D, int SUBS, bool NARROW>
 cudaError_t run(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const fa2dev::PagedParams& p,
                 unsigned grid, dim3 merge_grid, cudaStream_t s) {
-  fa2dev::fa2_paged_tc_kernel<D, kF16, SUBS, NARROW>
-      <<<grid, fa2dev::FwdShape<SUBS>::kThreads, fa2dev::PagedConfig<D, SUBS>::kSmemBytes, s>>>(mq, mk, mv, p);
-  cudaError_t e = cudaGetLastError();
+  const auto kernel = fa2dev::fa2_paged_tc_kernel<D, kF16, SUBS, NARROW>;
+  constexpr int kThreads = fa2dev::FwdShape<SUBS>::kThreads;
+  constexpr unsigned kSmem = fa2dev::PagedConfig<D, SUBS>::kSmemBytes;
+  cudaError_t e;
+  if (p.even) {
+    e = launch_behind(kernel, dim3(grid), kThreads, kSmem, s, mq, mk, mv, p);
+  } else {   // (behind the counter's memset)
+    kernel<<<grid, kThreads, kSmem, s>>>(mq, mk, mv, p);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess || merge_grid.x == 0) return e;
-  return launch_behind(fa2dev::fa2_paged_merge_kernel<D, kF16, SUBS>, merge_grid, fa2dev::kPagedMergeWarps * 32, s, p);
+  return launch_behind(fa2dev::fa2_paged_merge_kernel<D, kF16, SUBS>, merge_grid, fa2dev::kPagedMergeWarps * 32, 0, s, p);
 }
 }  // namespace
 

@@ -689,7 +689,9 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
   tc_fence_after_sync();
   const uint32_t tmem = bars->tmem_base;
 
-  // the merge may start (it finds its items and then waits for this grid to end)
+  // The grid before this one is complete from here on; behind that, the merge may
+  // start (it finds its items and then waits for this grid to end).
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp >= kWarpProducer) {
@@ -1359,6 +1361,7 @@ __global__ void __launch_bounds__(kPagedMergeWarps * 32) fa2_paged_merge_kernel(
   const PagedParts w = p.even ? paged_parts_even<SUBS>(p, index) : paged_item<SUBS>(p, index, true, D);
   // launched while the partial results are computed: they are complete from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!w.u.valid || w.first < 0 || w.first >= p.slots || w.rest + (w.parts - 2) * w.step >= p.slots) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = w.u.ntok * p.G;

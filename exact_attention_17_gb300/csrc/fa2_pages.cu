@@ -26,6 +26,13 @@ constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanPer = 8;                                  // counts per thread and pass
 constexpr int kPlanChunk = kPlanThreads * kPlanPer;
 
+// The next kernel on the stream may be made ready; the one before is complete
+// from here on.  All kernels here begin so, whole grids, before any access.
+__device__ __forceinline__ void begin_behind() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Exclusive prefix sum of v over the block (thread order) and the total.
 __device__ __forceinline__ int block_scan(int v, int* total, int* warp_sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -94,6 +101,7 @@ __device__ __forceinline__ int pages_for(long long tokens, int log2) {
 // missing: 0, or the pages that lacked, or -1 (a row of the table too short); nothing is changed unless 0.
 __global__ void __launch_bounds__(kPlanThreads)
     fa2_pages_reserve_kernel(const PageTables t, const int* add, int* missing, int* fresh) {
+  begin_behind();
   __shared__ int warp_sums[kPlanWarps];
   __shared__ int narrow;
   if (threadIdx.x == 0) narrow = 0;
@@ -157,7 +165,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 // nothing to copy), then n new lengths.
 __global__ void __launch_bounds__(kPlanThreads)
     fa2_pages_fork_kernel(const PageTables t, const int* src, const int* dst, int n, int* missing, int* pairs) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the copies may be made ready
+  begin_behind();
   __shared__ int warp_sums[kPlanWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int* from = pairs + 1;
@@ -266,6 +274,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 
 // One block per listed sequence.
 __global__ void __launch_bounds__(128) fa2_pages_free_kernel(const PageTables t, const int* seqs, int n) {
+  begin_behind();
   const int i = blockIdx.x;
   const int b = seqs[i];
   if (b < 0 || b >= t.B) {
@@ -295,7 +304,7 @@ __global__ void __launch_bounds__(128) fa2_pages_free_kernel(const PageTables t,
 // pairs as in fork: pages of number >= used (the count of used pages) go to the
 // free numbers below it, in ascending order.
 __global__ void __launch_bounds__(kPlanThreads) fa2_pages_compact_kernel(const PageTables t, int* moved, int* pairs) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the copies may be made ready
+  begin_behind();
   __shared__ int warp_sums[kPlanWarps];
   int* from = pairs + 1;
   int* to = from + t.num_pages;
@@ -330,7 +339,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa2_pages_compact_kernel(const P
 // whose source another pair writes is refused.
 __global__ void __launch_bounds__(256)
     fa2_pages_pairs_kernel(const int* src, const int* dst, int n, int num_pages, int* pairs, int* status) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the copies may be made ready
+  begin_behind();
   const int lane = threadIdx.x & 31;
   const int i = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   if (blockIdx.x == 0 && threadIdx.x == 0) pairs[0] = n;
@@ -363,7 +372,7 @@ __global__ void __launch_bounds__(kCopyThreads)
     fa2_pages_copy_kernel(const __grid_constant__ PagePlanes d, const int* pairs, int room, const PageTables t,
                           const int* moved) {
   // launched while the list is planned: it is there from here on
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  begin_behind();
   const int n = min(pairs[0], room);
   const int* from = pairs + 1;
   const int* to = from + room;
@@ -426,40 +435,35 @@ unsigned copy_grid(long long pairs, const PagePlanes& d, int sms) {
 }  // namespace
 
 cudaError_t launch_pages_reserve(const PageTables& t, const int* add, int* missing, int* ws, cudaStream_t s) {
-  fa2_pages_reserve_kernel<<<1, kPlanThreads, 0, s>>>(t, add, missing, ws);
-  return cudaGetLastError();
+  return launch_behind(fa2_pages_reserve_kernel, dim3(1), kPlanThreads, 0, s, t, add, missing, ws);
 }
 
 cudaError_t launch_pages_fork(const PageTables& t, const int* src, const int* dst, int n, const PagePlanes& d,
                               int* missing, int* ws, int sms, cudaStream_t s) {
-  fa2_pages_fork_kernel<<<1, kPlanThreads, 0, s>>>(t, src, dst, n, missing, ws);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_behind(fa2_pages_fork_kernel, dim3(1), kPlanThreads, 0, s, t, src, dst, n, missing, ws);
   if (e != cudaSuccess) return e;
-  return launch_behind(fa2_pages_copy_kernel, dim3(copy_grid(n, d, sms)), kCopyThreads, s, d, ws, n, t,
+  return launch_behind(fa2_pages_copy_kernel, dim3(copy_grid(n, d, sms)), kCopyThreads, 0, s, d, ws, n, t,
                        static_cast<const int*>(nullptr));
 }
 
 cudaError_t launch_pages_free(const PageTables& t, const int* seqs, int n, cudaStream_t s) {
-  fa2_pages_free_kernel<<<static_cast<unsigned>(n), 128, 0, s>>>(t, seqs, n);
-  return cudaGetLastError();
+  return launch_behind(fa2_pages_free_kernel, dim3(static_cast<unsigned>(n)), 128, 0, s, t, seqs, n);
 }
 
 cudaError_t launch_pages_compact(const PageTables& t, const PagePlanes& d, int* moved, int* ws, int sms,
                                  cudaStream_t s) {
-  fa2_pages_compact_kernel<<<1, kPlanThreads, 0, s>>>(t, moved, ws);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_behind(fa2_pages_compact_kernel, dim3(1), kPlanThreads, 0, s, t, moved, ws);
   if (e != cudaSuccess) return e;
-  return launch_behind(fa2_pages_copy_kernel, dim3(copy_grid(t.num_pages, d, sms)), kCopyThreads, s, d, ws, t.num_pages,
+  return launch_behind(fa2_pages_copy_kernel, dim3(copy_grid(t.num_pages, d, sms)), kCopyThreads, 0, s, d, ws, t.num_pages,
                        t, moved);
 }
 
 cudaError_t launch_pages_copy(const PagePlanes& d, const int* src, const int* dst, int n, int* ws, int* status,
                               int sms, cudaStream_t s) {
   const unsigned blocks = static_cast<unsigned>((static_cast<long long>(n) * 32 + 255) / 256);
-  fa2_pages_pairs_kernel<<<blocks, 256, 0, s>>>(src, dst, n, d.num_pages, ws, status);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_behind(fa2_pages_pairs_kernel, dim3(blocks), 256, 0, s, src, dst, n, d.num_pages, ws, status);
   if (e != cudaSuccess) return e;
-  return launch_behind(fa2_pages_copy_kernel, dim3(copy_grid(n, d, sms)), kCopyThreads, s, d, ws, n, PageTables{},
+  return launch_behind(fa2_pages_copy_kernel, dim3(copy_grid(n, d, sms)), kCopyThreads, 0, s, d, ws, n, PageTables{},
                        static_cast<const int*>(nullptr));
 }
 

@@ -29,6 +29,7 @@
 #include <cuda_fp16.h>
 
 #include "fa2_host.h"
+#include "fa2_launch.h"
 #include "fa2_rope.h"
 
 namespace fa2dev {
@@ -186,6 +187,8 @@ __global__ void __launch_bounds__(kRopeThreads, 3) fa2_rope_kernel(const __grid_
   const int n_tok = static_cast<int>(min(static_cast<long long>(p.tokens), p.total_tokens - tok0));
   const int row0 = blockIdx.y * p.rows, row1 = min(row0 + p.rows, p.total_rows);
   const int rot_units = p.r / (HALF ? 2 * W : W);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   for (int base = 0; base < n_tok * p.units; base += kRopeThreads) {   // once, but for rows of more than 256 units
     const int id = base + threadIdx.x;
@@ -307,8 +310,7 @@ using fa2dev::RopeParams;
 
 template <typename T, int W, bool HALF, bool APPEND>
 cudaError_t run(const RopeParams& p, dim3 grid, cudaStream_t s) {
-  fa2dev::fa2_rope_kernel<T, W, HALF, APPEND><<<grid, fa2dev::kRopeThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_behind(fa2dev::fa2_rope_kernel<T, W, HALF, APPEND>, grid, fa2dev::kRopeThreads, 0, s, p);
 }
 
 template <typename T, bool APPEND>
