@@ -302,3 +302,71 @@ def test_no_wait_runs_out(d, q_len):
     last.record()
     torch.cuda.synchronize()
     assert first.elapsed_time(last) < 500.0
+
+
+def serve(steps, group, sync):
+    """Dependent calls: room, append, attention, whose output makes the next step's tokens; forks between."""
+    d, Hq, Hkv, S, B = 64, 8, 2, 16, 6
+    g = torch.Generator().manual_seed(77)
+    pool = torch.full((2, 256, Hkv, S, d), float("nan"), dtype=BF, device="cuda")
+    table = torch.full((B, 40), -1, dtype=torch.int32, device="cuda")
+    lens, refs = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros(256, dtype=torch.int32, device="cuda")
+    x = torch.randn(B * group, Hq, d, generator=g).to(BF).cuda()
+    cu = offsets([group] * B) if group > 1 else None
+    add = torch.full((B,), group, dtype=torch.int32, device="cuda")
+    freq = fa2.rope_inv_freq(d, device="cuda")
+    src, dst = (torch.tensor([i], dtype=torch.int32, device="cuda") for i in (0, 5))
+    wait = torch.cuda.synchronize if sync else (lambda: None)
+    wait()
+    seen = []
+    for step in range(steps):
+        if step % 4 == 3:
+            fa2.pages_free(table, lens, refs, dst)
+            wait()
+            fa2.pages_fork(table, lens, refs, src, dst, (pool[0], pool[1]))
+            wait()
+        missing = fa2.pages_reserve(table, lens, refs, add, S)
+        wait()
+        q = fa2.append_paged(x[:, :Hkv], x[:, Hkv:2 * Hkv], pool[0], pool[1], table, lens, cu, q=x, inv_freq=freq)
+        wait()
+        o, lse = fa2.forward_paged(q, pool[0], pool[1], table, lens, cu_q=cu)
+        wait()
+        x = fa2.rope(o.transpose(0, 1).unsqueeze(0), torch.arange(B * group, device="cuda"),
+                     freq)[0].transpose(0, 1).contiguous() if step % 2 else o
+        wait()
+        seen += [missing, q, o, lse]
+    torch.cuda.synchronize()
+    return seen + [table, lens, refs]
+
+
+@pytest.mark.parametrize("group", [1, 7])
+def test_dependent_calls_without_waits_between(group):
+    """Kernels start behind one another: the same bits as with the device idle between calls."""
+    want = serve(24, group, True)
+    for _ in range(3):
+        for a, b in zip(serve(24, group, False), want):
+            assert torch.equal(a, b)
+
+
+def test_captured_chain_of_many_blocks():
+    """Whole items from the counter in the workspace, replayed: the counter starts over every time."""
+    d, Hq, Hkv = 128, 16, 16
+    q_lens, kv = [2100, 8000], [2500, 8000]
+    cache = Cache(kv, Hkv, 64, d, BF, seed=50)
+    q = queries(q_lens, Hq, d, BF, seed=51)
+    cu = offsets(q_lens)
+    want = fa2.forward_paged(q, cache.k, cache.v, cache.table, cache.lens, cu_q=cu)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        first = fa2.forward_paged(q, cache.k, cache.v, cache.table, cache.lens, cu_q=cu)
+        second = fa2.forward_paged(first[0], cache.k, cache.v, cache.table, cache.lens, cu_q=cu)
+    chained = fa2.forward_paged(want[0], cache.k, cache.v, cache.table, cache.lens, cu_q=cu)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(first + second, want + chained):
+        assert torch.equal(a, b)
+    rows = [0, 1, 2099]
+    O, L, bO, bL = attention(q[:2100], cache.keys[:1], cache.values[:1], [2100], True, 1 / math.sqrt(d), BF, EPS[BF])
+    assert ((want[0][rows].double() - O[rows]).abs() <= bO[rows]).all()
+    assert ((want[1][rows].double() - L[rows]).abs() <= bL[rows]).all()
