@@ -115,13 +115,15 @@ int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 // mean 1.1; above 0.77 to 1.07, mean 0.9.
 constexpr int kItemWaves = 4;
 constexpr int kItemWaves256 = 2;
-// Least key tiles of a range: two single tokens over 1000 keys take 16.5 us with
-// one, 18.3 with two, 20.5 with four and 26.6 with eight.
+// Least key tiles of a range: two single tokens over 1000 keys took 16.5 us with
+// one, 18.3 with two, 20.5 with four and 26.6 with eight (14.3 with one since
+// launches overlap, which changes all of them alike).
 constexpr int kMinTiles = 1;
 // What an item costs besides its keys (pipeline fill, epilogue), in keys.  Of
 // 128, 256, 384, 512 and 768: ragged chunks of 12 sequences take 68.8, 60.1, 59.4,
 // 57.6 and 60.7 us, two single tokens over 1000 keys (a range is at least an
-// item's cost and a tile) 17.2, 16.5, 18.4, 19.8 and 22.5.
+// item's cost and a tile) 17.2, 16.5, 18.4, 19.8 and 22.5 (all before launches
+// overlapped).
 constexpr int kItemKeys = 512;
 constexpr int kItemKeysNarrow = 256;
 

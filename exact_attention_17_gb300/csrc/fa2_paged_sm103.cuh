@@ -61,13 +61,13 @@
 //    slower: 1115 -> 1158 us for those 8192 tokens.
 //
 // Bound and measured.  Single tokens: bytes (64 sequences of 1000-8192 keys, 8
-// key/value heads of 128: 1.11 GB in 174.5 us, 6.38 TB/s; four of 100000-131072
-// keys, d = 64: 87 us, 5.57 TB/s).  Chunks: the tensor pipe, fed by one issuing
+// key/value heads of 128: 1.11 GB in 171.6 us, 6.49 TB/s; four of 100000-131072
+// keys, d = 64: 84.3 us, 5.74 TB/s).  Chunks: the tensor pipe, fed by one issuing
 // thread per SM, and the K/V tiles that the SMs read from L2 (8192 tokens over
 // 16384 keys, 32 heads of 128, causal: 1115 us, 1480 TFLOP/s; d = 256: 159 us for
 // 146 GFLOP, each SM reading 128 KB a tile).  Small calls: latency, 4 us from the
 // launch to the first S, 2 us a tile, and the merge (two tokens over 1000 keys:
-// 16.4 us, the merge's launch included).
+// 14.3 us, the merge's launch included).
 #pragma once
 
 #include <type_traits>
