@@ -370,3 +370,41 @@ def test_captured_chain_of_many_blocks():
     O, L, bO, bL = attention(q[:2100], cache.keys[:1], cache.values[:1], [2100], True, 1 / math.sqrt(d), BF, EPS[BF])
     assert ((want[0][rows].double() - O[rows]).abs() <= bO[rows]).all()
     assert ((want[1][rows].double() - L[rows]).abs() <= bL[rows]).all()
+
+
+def test_captured_behind_a_copy_and_another_stream():
+    """The node before a call may be a copy or a clearing, and another stream's work may join."""
+    d, Hq, Hkv = 128, 8, 2
+    cache = Cache([700, 40, 333], Hkv, 16, d, BF, seed=60)
+    q = queries([1] * 3, Hq, d, BF, seed=61)
+    want = fa2.forward_paged(q, cache.k, cache.v, cache.table, cache.lens)
+    freq = fa2.rope_inv_freq(d, device="cuda")
+    pos = torch.arange(3, device="cuda")
+    turned = fa2.rope(q, pos, freq)
+    lens, q2, q3 = torch.zeros_like(cache.lens), torch.zeros_like(q), torch.zeros_like(q)
+    scratch = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            q2.copy_(q)
+            r2 = fa2.rope(q2, pos, freq)
+        lens.copy_(cache.lens)
+        scratch.zero_()
+        q3.copy_(q)
+        got = fa2.forward_paged(q3, cache.k, cache.v, cache.table, lens)
+        main.wait_stream(side)
+        r3 = fa2.rope(r2, pos * 0, freq)            # behind both streams
+        again = fa2.forward_paged(q2, cache.k, cache.v, cache.table, lens)
+    for _ in range(3):
+        lens.zero_()
+        q2.zero_()
+        q3.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got + again, want + want):
+            assert torch.equal(a, b)
+        assert torch.equal(r2, turned) and torch.equal(r3, turned)
