@@ -1180,7 +1180,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
       const uint32_t o_phase = Cfg::kOutDoneLast ? outs & 1 : (done + n_tiles - 1) & 1;
       if constexpr (NARROW) {
         // The four warps' shares of the rows: O = sum_w e_w O_w / sum_w e_w l_w, e_w =
-        // 2^(m_w - max m).  32 columns of 16 rows at a time through the staging
+        // 2^(m_w - max m).  512 values of each warp at a time through the staging
         // rows.  Every warp passes every barrier, also after an abort.
         if (n_tiles > 0) {
           if (ok) ok = __all_sync(0xffffffffu, wait_bar(&bars->o_done[0], o_phase, abort, p.timeout_ns));
@@ -1198,34 +1198,41 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
           }
           const float mine = l == 0.f ? 0.f : ex2_approx(m - top) / sum;
           if (store && ok && wq == 0) *lse_out = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;
-          const uint32_t stage = smem_addr(smem + Cfg::kSmemStage);   // [4][16 rows][128 bytes]
-          const int out_row = threadIdx.x >> 3, unit = threadIdx.x & 7;   // what I add up and store
+          // per warp 2 KB: 16 rows of 32 columns, or 8 of 64 or 4 of 128
+          const uint32_t stage = smem_addr(smem + Cfg::kSmemStage);
+          const int wide = rows <= 4 && D >= 128 ? 2 : rows <= 8 ? 1 : 0;   // log2 of the column blocks of 32 in a pass
+          const int out_row = threadIdx.x >> (3 + wide), unit = threadIdx.x & ((8 << wide) - 1);   // what I add up and store
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tO + c * 32, o);
-            tmem_ld_wait(o);
+          for (int c = 0; c < D / 32; c += 1 << wide) {
 #pragma unroll 1
             for (int r0 = 0; r0 < rows; r0 += 16) {
-              if (lane >= r0 && lane < r0 + 16) {
+              const int slot = lane - r0;
+#pragma unroll 1
+              for (int x = 0; x < 1 << wide; ++x) {
+                uint32_t o[32];
+                tmem_ld32(tO + (c + x) * 32, o);
+                tmem_ld_wait(o);
+                if (slot >= 0 && slot < 16 >> wide) {
 #pragma unroll
-                for (int u = 0; u < 8; ++u)
-                  st_shared_v4(stage + wq * 2048 + (lane & 15) * 128 + ((u ^ (lane & 7)) << 4),
-                               __float_as_uint(__uint_as_float(o[4 * u]) * mine),
-                               __float_as_uint(__uint_as_float(o[4 * u + 1]) * mine),
-                               __float_as_uint(__uint_as_float(o[4 * u + 2]) * mine),
-                               __float_as_uint(__uint_as_float(o[4 * u + 3]) * mine));
+                  for (int u = 0; u < 8; ++u)
+                    st_shared_v4(stage + wq * 2048 + (slot << (7 + wide)) + x * 128 + ((u ^ (slot & 7)) << 4),
+                                 __float_as_uint(__uint_as_float(o[4 * u]) * mine),
+                                 __float_as_uint(__uint_as_float(o[4 * u + 1]) * mine),
+                                 __float_as_uint(__uint_as_float(o[4 * u + 2]) * mine),
+                                 __float_as_uint(__uint_as_float(o[4 * u + 3]) * mine));
+                }
               }
               named_sync(kBarShares, kRowsPerSub);
               const int r = r0 + out_row;
               if (r < rows && fits && ok) {
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                const uint32_t from = stage + (out_row << (7 + wide)) + ((unit ^ (out_row & 7)) << 4);
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                   float4 y;
                   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                                : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w)
-                               : "r"(stage + x * 2048 + out_row * 128 + ((unit ^ (out_row & 7)) << 4))
+                               : "r"(from + x * 2048)
                                : "memory");
                   v.x += y.x;
                   v.y += y.y;
