@@ -116,8 +116,8 @@ int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 constexpr int kItemWaves = 4;
 constexpr int kItemWaves256 = 2;
 // Least key tiles of a range: two single tokens over 1000 keys took 16.5 us with
-// one, 18.3 with two, 20.5 with four and 26.6 with eight (14.3 with one since
-// launches overlap, which changes all of them alike).
+// one, 18.3 with two, 20.5 with four and 26.6 with eight (13.8 with one since
+// launches overlap and shares merge in wider passes, which changes all alike).
 constexpr int kMinTiles = 1;
 // What an item costs besides its keys (pipeline fill, epilogue), in keys.  Of
 // 128, 256, 384, 512 and 768: ragged chunks of 12 sequences take 68.8, 60.1, 59.4,

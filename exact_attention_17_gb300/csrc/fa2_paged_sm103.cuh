@@ -67,7 +67,7 @@
 // 16384 keys, 32 heads of 128, causal: 1115 us, 1480 TFLOP/s; d = 256: 159 us for
 // 146 GFLOP, each SM reading 128 KB a tile).  Small calls: latency, 4 us from the
 // launch to the first S, 2 us a tile, and the merge (two tokens over 1000 keys:
-// 14.3 us, the merge's launch included).
+// 13.8 us, the merge's launch included).
 #pragma once
 
 #include <type_traits>
@@ -137,18 +137,18 @@ struct PagedSeq {
 };
 
 __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b, int block) {
-  PagedSeq s;
-  s.q0 = s.q_len = s.kv_len = 0;
+  int begin = 0, end = 0, kv = 0;   // nothing for b >= B
   if (b < p.B) {
-    const int begin = p.cu_q ? p.cu_q[b] : b;
-    const int end = p.cu_q ? p.cu_q[b + 1] : b + 1;
-    const int kv = p.kv_lens[b];
-    s.q0 = min(max(begin, 0), p.T);
-    s.q_len = max(0, min(end, p.T) - s.q0);
-    s.kv_len = min(max(kv, 0), p.max_len);
-    if (blockIdx.x == 0 && (begin < 0 || end < begin || end > p.T || kv < 0 || kv > p.max_len))
-      atomicOr(p.status, kDevErrPage);
+    begin = p.cu_q ? p.cu_q[b] : b;
+    end = p.cu_q ? p.cu_q[b + 1] : b + 1;
+    kv = p.kv_lens[b];
   }
+  PagedSeq s;
+  s.q0 = min(max(begin, 0), p.T);
+  s.q_len = max(0, min(end, p.T) - s.q0);
+  s.kv_len = min(max(kv, 0), p.max_len);
+  if (blockIdx.x == 0 && (begin < 0 || end < begin || end > p.T || kv < 0 || kv > p.max_len))
+    atomicOr(p.status, kDevErrPage);
   s.blocks = (s.q_len + block - 1) / block;
   return s;
 }
@@ -231,17 +231,36 @@ struct PagedPlace {
   }
 };
 
-// Lane b: sequence b, one of the first 32, and the cost of its blocks.
-struct PagedFirst {
+// Lane x: the cost of the blocks of its strip of the sequences, x strip .. (x +
+// 1) strip - 1, and the sequence where a strip is one (32 sequences or fewer).
+// After a strip's first lines its loads hit the first-level cache.  (Four
+// sequences a step made the code longer and every small call slower, by up to
+// 3 of 84 us; strips against steps of 32 sequences, read twice: 4096 sequences of
+// at most 512 keys 964 -> 842 us.)
+struct PagedStrips {
+  int strip;
   PagedSeq s;
   long long cost;
 };
 
 template <int SUBS>
-__device__ __forceinline__ PagedFirst paged_first(const PagedParams& p) {
-  PagedFirst f;
-  f.s = paged_seq(p, threadIdx.x & 31, p.sub_tokens * SUBS);
-  f.cost = cost_before<SUBS>(p, f.s, f.s.blocks);
+__device__ __forceinline__ PagedStrips paged_strips(const PagedParams& p) {
+  const int lane = threadIdx.x & 31, block = p.sub_tokens * SUBS;
+  PagedStrips f;
+  f.strip = (p.B + 31) / 32;
+  if (f.strip == 1) {
+    f.s = paged_seq(p, lane, block);
+    f.cost = cost_before<SUBS>(p, f.s, f.s.blocks);
+    return f;
+  }
+  const int end = min(p.B, (lane + 1) * f.strip);
+  f.s = {};
+  f.cost = 0;
+#pragma unroll 1
+  for (int b = lane * f.strip; b < end; ++b) {
+    const PagedSeq s = paged_seq(p, b, block);
+    f.cost += cost_before<SUBS>(p, s, s.blocks);
+  }
   return f;
 }
 
@@ -249,13 +268,8 @@ __device__ __forceinline__ PagedFirst paged_first(const PagedParams& p) {
 // item's fixed cost and one tile, so that an item's inner ranges all have tiles;
 // and the length of the list.
 template <int SUBS>
-__device__ __forceinline__ long long paged_share(const PagedParams& p, const PagedFirst& f, long long* total) {
-  long long sum = f.cost;
-  for (int b = (threadIdx.x & 31) + 32; b < p.B; b += 32) {
-    const PagedSeq s = paged_seq(p, b, p.sub_tokens * SUBS);
-    sum += cost_before<SUBS>(p, s, s.blocks);
-  }
-  sum = warp_sum(sum) * p.Hkv;
+__device__ __forceinline__ long long paged_share(const PagedParams& p, const PagedStrips& f, long long* total) {
+  const long long sum = warp_sum(f.cost) * p.Hkv;
   *total = sum;
   // total / ctas rounded up (the 64-bit product is off by less than one), so that the ranges cover the list
   const long long share = static_cast<long long>(static_cast<double>(sum) * p.inv_ctas) + 2;
@@ -264,13 +278,23 @@ __device__ __forceinline__ long long paged_share(const PagedParams& p, const Pag
 
 // Whole warp: the item that position `pos` (below the list's length) lies in.
 template <int SUBS>
-__device__ __forceinline__ PagedPlace paged_find(const PagedParams& p, const PagedFirst& f, long long pos) {
+__device__ __forceinline__ PagedPlace paged_find(const PagedParams& p, const PagedStrips& f, long long pos) {
   const int lane = threadIdx.x & 31;
   PagedPlace w = {};
   long long before = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const PagedSeq s = b0 == 0 ? f.s : paged_seq(p, b0 + lane, p.sub_tokens * SUBS);
-    const long long per_head = b0 == 0 ? f.cost : cost_before<SUBS>(p, s, s.blocks);
+  int begin = 0, end = p.B;
+  if (f.strip > 1) {   // the strip
+    const long long mine = f.cost * p.Hkv, sum = warp_scan(mine);
+    const unsigned here = __ballot_sync(0xffffffffu, pos >= sum - mine && pos < sum);
+    if (here == 0) return w;
+    const int src = __ffs(here) - 1;
+    before = __shfl_sync(0xffffffffu, sum - mine, src);
+    begin = src * f.strip;
+    end = min(p.B, begin + f.strip);
+  }
+  for (int b0 = begin; b0 < end; b0 += 32) {
+    const PagedSeq s = f.strip == 1 ? f.s : paged_seq(p, b0 + lane < end ? b0 + lane : p.B, p.sub_tokens * SUBS);
+    const long long per_head = f.strip == 1 ? f.cost : cost_before<SUBS>(p, s, s.blocks);
     const long long mine = per_head * p.Hkv, sum = warp_scan(mine) + before;
     const unsigned here = __ballot_sync(0xffffffffu, pos >= sum - mine && pos < sum);
     if (here == 0) {
@@ -382,7 +406,7 @@ template <int SUBS>
 __device__ __forceinline__ PagedWalk paged_walk(const PagedParams& p, int cta) {
   PagedWalk w;
   long long total;
-  const PagedFirst f = paged_first<SUBS>(p);
+  const PagedStrips f = paged_strips<SUBS>(p);
   const long long share = paged_share<SUBS>(p, f, &total);
   w.cta = cta;
   w.lo = cta * share;
@@ -405,7 +429,7 @@ __device__ __forceinline__ PagedParts paged_parts_even(const PagedParams& p, int
   PagedParts r;
   r.u.valid = 0;
   long long total;
-  const PagedFirst f = paged_first<SUBS>(p);
+  const PagedStrips f = paged_strips<SUBS>(p);
   const long long share = paged_share<SUBS>(p, f, &total);
   const long long pos = (index + 1ll) * share;
   if (index + 1 >= p.ctas || pos >= total) return r;
@@ -1200,7 +1224,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
           if (store && ok && wq == 0) *lse_out = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;
           // per warp 2 KB: 16 rows of 32 columns, or 8 of 64 or 4 of 128
           const uint32_t stage = smem_addr(smem + Cfg::kSmemStage);
-          const int wide = rows <= 4 && D >= 128 ? 2 : rows <= 8 ? 1 : 0;   // log2 of the column blocks of 32 in a pass
+          const int wide = D == 64 ? 0 : rows <= 4 ? 2 : rows <= 8 ? 1 : 0;   // log2 of the column blocks of 32 in a pass
           const int out_row = threadIdx.x >> (3 + wide), unit = threadIdx.x & ((8 << wide) - 1);   // what I add up and store
 #pragma unroll 1
           for (int c = 0; c < D / 32; c += 1 << wide) {

@@ -408,3 +408,17 @@ def test_captured_behind_a_copy_and_another_stream():
         for a, b in zip(got + again, want + want):
             assert torch.equal(a, b)
         assert torch.equal(r2, turned) and torch.equal(r3, turned)
+
+
+@pytest.mark.parametrize("B", [33, 64, 1025, 2100])
+@pytest.mark.parametrize("chunks", [False, True])
+def test_many_short_sequences(B, chunks):
+    """The schedule's strips of sequences: more than one each, and more than 32."""
+    d, Hq, Hkv, S = 64, 4, 2, 16
+    kv = [(53 * i) % 40 if i % 9 else 0 for i in range(B)]
+    q_lens = [(i % 3) if chunks else 1 for i in range(B)]
+    kv = [max(n, c) for n, c in zip(kv, q_lens)] if chunks else kv
+    cache = Cache(kv, Hkv, S, d, BF, seed=70)
+    q = queries(q_lens, Hq, d, BF, seed=71)
+    o, lse = fa2.forward_paged(q, cache.k, cache.v, cache.table, cache.lens, cu_q=offsets(q_lens) if chunks else None)
+    check(o, lse, q, cache, q_lens, True, 1 / math.sqrt(d))
