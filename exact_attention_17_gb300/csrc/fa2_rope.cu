@@ -137,15 +137,32 @@ struct RopeToken {
   int live;          // 0: nothing is written for this token
 };
 
-// Whole block: positions and slots of `n_tok` tokens from tok0 on, a warp per token.
+// A sequence's length and the rows of its new tokens lie within the table and the call's tokens.
+__device__ __forceinline__ bool append_in_order(const RopeParams& p, int begin, int end, int len) {
+  return (begin >= 0) & (begin <= end) & (end <= p.total_tokens) & (len >= 0) & (len <= p.max_len);
+}
+
+// Whole block: positions and slots of `n_tok` tokens from tok0 on, a warp per
+// token.  Where a sequence's numbers are not in order, its tokens are not
+// written: a slot taken from them could be an older token's.  (Their queries turn
+// at the positions that attention gives them, from the numbers cut to their range.)
+// Sequences without a token in the call are looked at and reported too, by the
+// first block's first warp, which reads all offsets for its token anyway.
 __device__ __forceinline__ void append_tokens(const RopeParams& p, int tok0, int n_tok, RopeToken* toks) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int k = warp; k < n_tok; k += kRopeThreads / 32) {
     const int t = tok0 + k;
     int b = t, begin = t, end = t + 1;
     if (p.cu_q != nullptr) {
+      const bool all = blockIdx.x == 0 && blockIdx.y == 0 && k == 0;
+      bool good = true;
       int c = 0;   // sequences that end at or before t
-      for (int i = lane + 1; i <= p.B; i += 32) c += p.cu_q[i] <= t ? 1 : 0;
+      for (int i = lane + 1; i <= p.B; i += 32) {
+        const int e = p.cu_q[i], a = all ? p.cu_q[i - 1] : e, n = all ? p.kv_lens[i - 1] : 0;   // (loads side by side)
+        c += e <= t ? 1 : 0;
+        good &= !all | append_in_order(p, a, e, n);
+      }
+      if (!good) atomicOr(p.status, kDevErrPage);
       b = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(c)));
       begin = b < p.B ? p.cu_q[b] : 0;
       end = b < p.B ? p.cu_q[b + 1] : 0;
@@ -157,9 +174,9 @@ __device__ __forceinline__ void append_tokens(const RopeParams& p, int tok0, int
       o.live = b < p.B && begin <= t && t < end;
       if (o.live) {
         const int len = p.kv_lens[b];
-        const long long pos = static_cast<long long>(len) - end + t;
+        const long long pos = min(max(len, 0), p.max_len) - min(static_cast<long long>(end), p.total_tokens) + t;
         o.pos = pos;
-        if (len > p.max_len) {
+        if (!append_in_order(p, begin, end, len)) {
           atomicOr(p.status, kDevErrPage);
         } else if (pos >= 0) {
           const int page = p.page_table[b * p.table_stride + (pos >> p.page_log2)];

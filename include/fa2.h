@@ -395,8 +395,10 @@ int fa2_rope(const void *X, const long long *x_strides, void *Y, const long long
  * their positions (rotary_dim = 0: as they are); in the same launch rotates the
  * queries Q [T, Hq, d] into Q_out (Hq = 0: none; Q_out = Q works in place).
  * K, V [T, kv_heads, d]; strides {token, head} in elements, multiples of 8.
- * Tokens at negative positions (c_b > kv_lens[b]) are not written.  The pages
- * written must not be shared by sequences, and K, V and Q not lie in them.
+ * Tokens at negative positions (c_b > kv_lens[b]) are not written, and none of a
+ * sequence whose length or offsets lie outside the cache or the tokens, or whose
+ * offsets descend (FA2_ERR_PAGE).  The pages written must not be shared by
+ * sequences, and K, V and Q not lie in them.
  */
 int fa2_append_paged(const fa2_paged_cache *cache, const void *K, const long long *k_strides,
                      const void *V, const long long *v_strides, const void *Q,
