@@ -106,7 +106,7 @@ bool cache_of(PyObject* const* a, fa2_paged_cache* c, at::Device* device) {
     return false;
   *device = k->device();
   if (!ints(table, table->sizes(), *device) || !ints(lens, {table->size(0)}, *device) || !fits_int(k->sizes()) ||
-      !fits_int(table->sizes()))
+      !fits_int(table->sizes()) || k->size(1) == 0)   // (no heads: callers divide by them)
     return false;
   c->k_pages = k->data_ptr();
   c->v_pages = v->data_ptr();

@@ -192,7 +192,7 @@ def forward_paged(q, k_pages, v_pages, page_table, kv_lens, cu_q=None, causal: b
         raise ValueError(f"q must be [T, Hq, {args.d}]")
     T, Hq, d = shape
     strides = _rows("q", q, shape, dtype, device)
-    if Hq % args.kv_heads != 0:
+    if args.kv_heads == 0 or Hq % args.kv_heads != 0:
         raise ValueError(f"{Hq} query heads are no multiple of {args.kv_heads} key/value heads")
     offsets = _offsets(cu_q, args.B, T, device)
     if out_dtype is None:
