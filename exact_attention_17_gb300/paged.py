@@ -111,8 +111,16 @@ def _answer(r, where):
     return r
 
 
+def _sizes(*sizes):
+    """Sizes that go to the library as C ints: ctypes would keep the low 32 bits of larger ones."""
+    for n in sizes:
+        if not -1 << 31 <= n < 1 << 31:
+            raise ValueError(f"a size of {n} does not fit the library's 32-bit integers")
+
+
 def _ints(name, t, shape, device):
     """An int32 CUDA tensor of `shape`, rows dense."""
+    _sizes(*shape)
     if t.dtype is not torch.int32 or t.shape != shape or t.device != device or (shape[-1] > 1 and t.stride(-1) != 1):
         raise ValueError(f"{name} must be a dense int32 tensor of shape {tuple(shape)} on {device}")
 
@@ -122,6 +130,7 @@ def _rows(name, t, shape, dtype, device):
     strides = t.stride()
     if t.dtype is not dtype or t.shape != shape or t.device != device or strides[-1] != 1:
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device} with a dense last dimension")
+    _sizes(*shape)
     return strides
 
 
@@ -133,6 +142,7 @@ def _cache_args(k_pages, v_pages, page_table, kv_lens, device, dtype):
         raise ValueError("k_pages must be a 4-D CUDA tensor with a dense last dimension")
     if v_pages.dtype is not dtype or v_pages.shape != shape or v_pages.stride() != strides or v_pages.device != device:
         raise ValueError("v_pages must match k_pages in type, shape, strides and device")
+    _sizes(*shape)
     table_shape = page_table.shape
     if len(table_shape) != 2:
         raise ValueError("page_table must be [B, M]")
@@ -350,6 +360,7 @@ def _rope(x, positions, inv_freq, interleaved, mscale, out, stream, transposed):
         B = 1
     else:
         B, H, N, d = shape
+    _sizes(*shape)
     ps = positions.shape
     if positions.device != device or (positions.dtype is not torch.int32 and positions.dtype is not torch.int64):
         raise ValueError(f"positions must be int32 or int64 on {device}")
@@ -402,6 +413,7 @@ def _tables(page_table, lens, refs, page_size):
     _ints("page_table", page_table, shape, device)
     _ints("lens", lens, (B,), device)
     _ints("refs", refs, pages, device)
+    _sizes(page_size)
     return fa2.PageTablesArgs(page_table.data_ptr(), page_table.stride(0), M, B, lens.data_ptr(), refs.data_ptr(),
                               pages[0], page_size), device
 
@@ -430,6 +442,7 @@ def _pools(pools):
             planes = [p + i * st * size for p in planes for i in range(n)]
         pointers += planes
     P, Hkv, S, d = first.shape[-4:]
+    _sizes(P, Hkv, S, d)
     strides = first.stride()
     if strides[-1] != 1 or strides[-2] != d or strides[-3] != S * d:
         dense = 1   # in another order, perhaps
