@@ -12,6 +12,7 @@ from __future__ import annotations
 import glob
 import importlib.util
 import os
+import shutil
 import subprocess
 import sysconfig
 import tempfile
@@ -46,11 +47,13 @@ def _inputs():
     return files
 
 
+def _newer(path, files):
+    t = os.path.getmtime(path)
+    return all(os.path.getmtime(f) <= t for f in files)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
-        return False
-    t = os.path.getmtime(LIB_PATH)
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    return os.path.exists(LIB_PATH) and _newer(LIB_PATH, _inputs())
 
 
 def _replace(path, make):
@@ -67,17 +70,32 @@ def _replace(path, make):
             os.remove(tmp)
 
 
-def build_binding(force: bool = False) -> str:
-    """Build _binding.so unless it is newer than its sources and the torch it is built against."""
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)   # found, not imported
-    inputs = [BINDING_SOURCE, os.path.join(INCLUDE, "fa2.h"), os.path.join(torch_dir, "version.py")]
-    if (not force and os.path.exists(BINDING_PATH)
-            and all(os.path.getmtime(f) <= os.path.getmtime(BINDING_PATH) for f in inputs)):
+def build_binding(force: bool = False) -> str | None:
+    """Build _binding.so unless it is newer than its sources and the torch it is built against.
+
+    Returns its path, or None where something that it alone needs is not there:
+    torch with its headers and CUDA libraries, Python's headers, g++.  The
+    library works without it (paged.py then goes through ctypes).
+    """
+    spec = importlib.util.find_spec("torch")   # found, not imported
+    torch_dir = os.path.dirname(spec.origin) if spec is not None and spec.origin else None
+    sources = [BINDING_SOURCE, os.path.join(INCLUDE, "fa2.h")]
+    python_include = sysconfig.get_paths()["include"]
+    needed = [os.path.join(python_include, "Python.h")]
+    if torch_dir is not None:
+        libs = os.path.join(torch_dir, "lib")
+        needed += [os.path.join(libs, "libtorch_python.so"), os.path.join(libs, "libc10_cuda.so"),
+                   os.path.join(torch_dir, "include", "ATen", "core", "Tensor.h")]
+    there = os.path.exists(BINDING_PATH)
+    if torch_dir is None or shutil.which("g++") is None or not all(os.path.exists(f) for f in needed):
+        if there and not _newer(BINDING_PATH, sources):
+            os.remove(BINDING_PATH)            # made for another interface of the library
+        return None
+    if not force and there and _newer(BINDING_PATH, sources + [os.path.join(torch_dir, "version.py")]):
         return BINDING_PATH
     includes = [INCLUDE, os.path.join(torch_dir, "include"),
                 os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
-                sysconfig.get_paths()["include"], os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")]
-    libs = os.path.join(torch_dir, "lib")
+                python_include, os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")]
     _replace(BINDING_PATH, lambda tmp: ["g++", "-O2", "-std=c++17", "-fPIC", "-shared"] + ["-I" + i for i in includes]
              + [BINDING_SOURCE, "-o", tmp, "-L" + libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
                 "-Wl,-rpath," + libs])
@@ -85,7 +103,8 @@ def build_binding(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Build libfa2.so and the binding next to this file unless they are newer than their sources."""
+    """Build libfa2.so and, where torch is there, the binding next to this file unless they are newer than their
+    sources."""
     if not force and up_to_date():
         build_binding()
         return LIB_PATH
