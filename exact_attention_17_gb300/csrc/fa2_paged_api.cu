@@ -43,6 +43,27 @@ long long extent(const long long (&sizes)[N], const long long (&strides)[N], lon
   return e;
 }
 
+// The rows of an array that is written lie apart: with its outer dimensions (those
+// of more than one step) in the order of their strides, each steps past all that
+// the smaller ones reach.  Strides that interleave dimensions without a common
+// element are refused too; no view of a dense array has such.
+template <int N>
+bool rows_apart(const long long (&sizes)[N], const long long (&strides)[N], long long inner) {
+  bool taken[N] = {};
+  long long reach = inner;
+  for (int n = 0; n < N; ++n) {
+    int least = -1;
+    for (int i = 0; i < N; ++i)
+      if (!taken[i] && sizes[i] > 1 && (least < 0 || strides[i] < strides[least])) least = i;
+    if (least < 0) return true;
+    if (strides[least] < reach) return false;
+    if (strides[least] > (1ll << 60) / sizes[least]) return false;
+    reach += (sizes[least] - 1) * strides[least];
+    taken[least] = true;
+  }
+  return true;
+}
+
 bool range_ok(const void* p, long long elems, int size) {
   return elems >= 0 && fa2host::device_memory_ok(p, static_cast<size_t>(elems) * size);
 }
@@ -306,6 +327,7 @@ extern "C" int fa2_rope(const void* X, const long long* x_strides, void* Y, cons
   if (misaligned(X, elem - 1) || misaligned(Y, elem - 1) || misaligned(positions, positions_int64 ? 7 : 3) ||
       (interleaved && !wide && !pairs))
     return FA2_ERR_ALIGN;
+  if (!rows_apart(sizes, ys, d)) return FA2_ERR_SHAPE;
   const long long ps = B > 1 ? positions_batch_stride : 0;
   if (ps < 0 || ps > kMaxStride) return FA2_ERR_SHAPE;
   if ((rc = fa2host::require_device()) != FA2_OK) return rc;
@@ -366,6 +388,13 @@ extern "C" int fa2_append_paged(const fa2_paged_cache* cache, const void* K, con
     if ((rc = check_rows(Q_out, q_out_strides[0], q_out_strides[1], T, Hq, c.d)) != FA2_OK) return rc;
   }
   if (misaligned(cu_q, 3)) return FA2_ERR_ALIGN;
+  const long long page_sizes[3] = {c.num_pages, c.kv_heads, c.page_size};
+  const long long page_strides[3] = {c.page_stride, c.head_stride, c.slot_stride};
+  if (!rows_apart(page_sizes, page_strides, c.d)) return FA2_ERR_SHAPE;
+  if (Hq > 0) {
+    const long long out_sizes[2] = {T, Hq}, out_strides[2] = {q_out_strides[0], q_out_strides[1]};
+    if (!rows_apart(out_sizes, out_strides, c.d)) return FA2_ERR_SHAPE;
+  }
   if ((rc = fa2host::require_device()) != FA2_OK) return rc;
   if ((rc = check_cache_memory(cache)) != FA2_OK) return rc;
   if (!rows_in_memory(K, k_strides[0], k_strides[1], T, c.kv_heads, c.d) ||

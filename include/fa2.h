@@ -379,7 +379,8 @@ size_t fa2_forward_paged_workspace_bytes(int B, int T, int Hq, int kv_heads, int
  * products are fp32 and rounded once.
  *   X, Y       [B, H, N, d], strides {batch, head, token} in elements; Y = X
  *              (same strides) works in place, other overlaps are refused
- *              (FA2_ERR_MEMORY).  d is even, at most 1024.  Interleaved
+ *              (FA2_ERR_MEMORY), and a Y whose own rows overlap (FA2_ERR_SHAPE;
+ *              X's may).  d is even, at most 1024.  Interleaved
  *              pairs must be aligned to two elements.
  *   positions  int32, or int64 (positions_int64), [N] or [B, N]
  *              (positions_batch_stride 0 or N)
@@ -397,8 +398,10 @@ int fa2_rope(const void *X, const long long *x_strides, void *Y, const long long
  * K, V [T, kv_heads, d]; strides {token, head} in elements, multiples of 8.
  * Tokens at negative positions (c_b > kv_lens[b]) are not written, and none of a
  * sequence whose length or offsets lie outside the cache or the tokens, or whose
- * offsets descend (FA2_ERR_PAGE).  The pages written must not be shared by
- * sequences, and K, V and Q not lie in them.
+ * offsets descend (FA2_ERR_PAGE).  Rows of Q_out and slots of the pages that
+ * overlap each other are refused (FA2_ERR_SHAPE).  The pages written must not be
+ * shared by sequences; K's pages, V's and Q_out overlap neither each other nor K, V
+ * and Q (but Q_out = Q).
  */
 int fa2_append_paged(const fa2_paged_cache *cache, const void *K, const long long *k_strides,
                      const void *V, const long long *v_strides, const void *Q,
