@@ -17,9 +17,11 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <exception>
 #include <vector>
 
 #include "fa2.h"
@@ -74,15 +76,14 @@ PyObject* none() { Py_RETURN_NONE; }
 
 PyObject* result(int rc, at::Tensor&& t) { return rc == FA2_OK ? THPVariable_Wrap(std::move(t)) : PyLong_FromLong(rc); }
 
-// C++ exceptions (torch's out-of-memory error among them) become Python's
+// C++ exceptions become the Python exceptions that torch's own functions raise
+// (torch.OutOfMemoryError, where a server may free pages and go on).
 template <typename F>
 PyObject* guarded(F f) {
   try {
     return f();
-  } catch (const c10::Error& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {
+    torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }
