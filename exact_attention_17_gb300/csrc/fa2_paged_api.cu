@@ -253,7 +253,6 @@ extern "C" int fa2_forward_paged(const fa2_paged_cache* cache, const void* Q, lo
   p.box_tokens = plan.box_tokens;
   p.page_log2 = page_log2(c.page_size);
   p.num_pages = c.num_pages;
-  p.table_width = c.table_width;
   p.table_stride = c.table_stride;
   p.max_len = c.table_width << p.page_log2;
   p.even = plan.even ? 1 : 0;

@@ -94,7 +94,6 @@ struct PagedParams {
   int box_tokens;          // tokens per Q box (divides sub_tokens)
   int page_log2;           // log2 of the slots per page
   int num_pages;
-  int table_width;
   long long table_stride;
   int max_len;             // table_width << page_log2, at most 2^30
   int even;                // equal ranges of the work, one per CTA (else whole items)
