@@ -16,8 +16,12 @@ namespace fa2host {
 
 // Launches a kernel that may start while the one before it on the stream still
 // runs (when that one allows it, griddepcontrol.launch_dependents).  Every block
-// waits for the one before to end (griddepcontrol.wait) before it reads or
-// writes what others may, so that "complete" reaches back along the stream.
+// waits for the one before to end (griddepcontrol.wait) before it writes, and
+// before it reads what others may write, so that "complete" reaches back along the
+// stream.  One kernel reads earlier: the merge of the paged attention looks up
+// lengths and offsets first.  They are complete by then, because the kernel before
+// it, which writes neither, lets it start only behind its own wait; a kernel that
+// is to do the same has to be behind one that keeps this order.
 template <typename... Params, typename... Args>
 cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int threads, unsigned smem, cudaStream_t s,
                           const Args&... args) {

@@ -136,21 +136,26 @@ int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 // mean 1.1; above 0.77 to 1.07, mean 0.9.
 constexpr int kItemWaves = 4;
 constexpr int kItemWaves256 = 2;
-// Least key tiles of a range: two single tokens over 1000 keys took 16.5 us with
-// one, 18.3 with two, 20.5 with four and 26.6 with eight (13.8 with one since
-// launches overlap and shares merge in wider passes, which changes all alike).
+// The three below from 40 random batches each (1 to 300 sequences of 20 to 60000
+// keys, every head size, groups of 1 to 8; geometric mean of the times against the
+// value taken, worst and best batch).
+// Least key tiles of a range: two 1.03 (0.94 to 1.20), four 1.07 (0.85 to 1.40).
 constexpr int kMinTiles = 1;
-// What an item costs besides its keys (pipeline fill, epilogue), in keys.  Of
-// 128, 256, 384, 512 and 768: ragged chunks of 12 sequences take 68.8, 60.1, 59.4,
-// 57.6 and 60.7 us, two single tokens over 1000 keys (a range is at least an
-// item's cost and a tile) 17.2, 16.5, 18.4, 19.8 and 22.5 (all before launches
-// overlapped).
+// What an item costs besides its keys (pipeline fill, epilogue), in keys; a range
+// is at least that and a tile.  Chunks: 128 1.05 (0.86 to 1.27), 256 1.01 (0.91 to
+// 1.13), 384 1.00 (0.93 to 1.08), 768 1.02 (0.94 to 1.09), 1024 1.04 (0.94 to 1.16).
+// Single tokens: none 1.16 (1.00 to 1.87), 128 1.02 (0.91 to 1.11), 384 1.01 (0.91 to
+// 1.21), 512 1.02 (0.88 to 1.21).
 constexpr int kItemKeys = 512;
 constexpr int kItemKeysNarrow = 256;
 
 // Sub-tiles per CTA: two (256 rows on one K/V stream) where the sequences'
 // average chunk fills more than one sub-tile, else one with two CTAs per SM, of
-// at most 32 rows where the average chunk has no more.
+// at most 32 rows where the average chunk has no more.  The host knows the sizes
+// alone, so one form serves the whole batch: 64 single tokens and a chunk of 512
+// take 149 us together, 109 and 58 apart, but a chunk that is long for the average
+// is cut into blocks of 32 rows (1024 single tokens over 100-500 keys and a chunk of
+// 7000: 1497 us, 252 and 319 apart).
 PagedPlan plan_paged(int B, int T, int Hq, int Hkv, int d, bool has_cu, int sms) {
   PagedPlan q;
   q.G = Hq / Hkv;
@@ -545,7 +550,10 @@ size_t copy_ints(int n) { return 1 + 2 * static_cast<size_t>(n); }
 
 int launched(cudaError_t e) { return e == cudaSuccess ? FA2_OK : FA2_ERR_LAUNCH; }
 
-constexpr int kMaxPairs = 1 << 16;   // the lists are searched for indices named twice
+// The lists are searched for indices named twice, each entry against all: copies of
+// 1 KB take 22 us for 1024 pairs, 52 for 4096, 294 for 16384 and 3.6 ms for 65536;
+// freeing as many sequences 10 us, 14, 55 and 0.76 ms.
+constexpr int kMaxPairs = 1 << 16;
 
 }  // namespace
 

@@ -61,13 +61,14 @@
 //    slower: 1115 -> 1158 us for those 8192 tokens.
 //
 // Bound and measured.  Single tokens: bytes (64 sequences of 1000-8192 keys, 8
-// key/value heads of 128: 1.11 GB in 171.6 us, 6.49 TB/s; four of 100000-131072
-// keys, d = 64: 84.3 us, 5.74 TB/s).  Chunks: the tensor pipe, fed by one issuing
-// thread per SM, and the K/V tiles that the SMs read from L2 (8192 tokens over
-// 16384 keys, 32 heads of 128, causal: 1115 us, 1480 TFLOP/s; d = 256: 159 us for
-// 146 GFLOP, each SM reading 128 KB a tile).  Small calls: latency, 4 us from the
-// launch to the first S, 2 us a tile, and the merge (two tokens over 1000 keys:
-// 13.8 us, the merge's launch included).
+// key/value heads of 128: 1.11 GB in 169.5-172 us, 6.48-6.57 TB/s; four of
+// 100000-131072 keys, d = 64: 84.3-85.7 us, 5.6-5.7 TB/s).  Chunks: the tensor pipe,
+// fed by one issuing thread per SM, and the K/V tiles that the SMs read from L2
+// (8192 tokens over 16384 keys, 32 heads of 128, causal: 1115-1150 us on different
+// GPUs, 1435-1480 TFLOP/s; d = 256: 159-160 us for 146 GFLOP, each SM reading 128 KB
+// a tile).  Small calls: latency, 4 us from the launch to the first S, 2 us a tile,
+// and the merge (two tokens over 1000 keys: 13.8-14.1 us, the merge's launch
+// included).
 #pragma once
 
 #include <type_traits>
@@ -1390,6 +1391,8 @@ __global__ void __launch_bounds__(kPagedMergeWarps * 32) fa2_paged_merge_kernel(
   const int index = static_cast<int>(blockIdx.x);
   const PagedParts w = p.even ? paged_parts_even<SUBS>(p, index) : paged_item<SUBS>(p, index, true, D);
   // launched while the partial results are computed: they are complete from here on
+  // (what was read above the kernel before this one does not write, and that one lets
+  // this one start behind its own wait for what came before it)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!w.u.valid || w.first < 0 || w.first >= p.slots || w.rest + (w.parts - 2) * w.step >= p.slots) return;

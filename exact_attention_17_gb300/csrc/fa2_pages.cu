@@ -13,9 +13,9 @@
 // behind it on the same stream (made ready while the block plans), which reads
 // the planned list: nothing returns to the host.  Bound: planning by the latency
 // of one block's passes over refs, copying by bytes (each page read and written
-// once): compacting 4096 pages of 32 KB in 8 planes, 543 MB moved, takes 94.7 us, 5.7
-// TB/s; a beam step of 8 groups of 4 sequences (free, fork, reserve), 23.6 us, is
-// four dependent launches.
+// once): compacting 4096 pages of 32 KB in 8 planes, 543 MB moved, takes 94.7-94.9
+// us, 5.7 TB/s; a beam step of 8 groups of 4 sequences (free, fork, reserve),
+// 23.6-28.6 us, is four dependent launches.
 #include "fa2_launch.h"
 #include "fa2_pages.h"
 

@@ -17,9 +17,9 @@
 // 2e-9 and 2e-10): about 30 instructions a pair, a third of a library call.
 //
 // Bound: bytes (each row read and written once); 16 heads of 128 columns at 4 x
-// 4096 positions in bf16, 134 MB, take 23 us, 5.8 TB/s (24.5 us from one call to
-// the next), a chunk append of 10,500 tokens (32 + 4 + 4 heads of 64, 32 columns
-// rotated) 23.1 us, one token of 64 sequences 5.6 us (latency).  A thread keeps one unit of the
+// 4096 positions in bf16, 134 MB, take 23 us, 5.8 TB/s (24.5-25.2 us from one call
+// to the next), a chunk append of 10,500 tokens (32 + 4 + 4 heads of 64, 32 columns
+// rotated) 23.1-24.3 us, one token of 64 sequences 5.5-6.3 us (latency).  A thread keeps one unit of the
 // head (two 8-byte vectors of 16-bit elements whose columns are rotated against
 // each other, or one 16-byte vector of neighbouring pairs) at one token: it
 // computes the unit's four sines once, in registers, and then runs over the

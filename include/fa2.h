@@ -357,6 +357,9 @@ typedef struct {
  * depend on timing: repeated calls give the same bits.  A value of a live token
  * that is not finite may reach every row of its sequence (a masked weight of 0
  * times infinity is NaN), as in the formula.
+ * The blocks' shape is taken from the sizes (T, B, the heads), not from the
+ * lengths, for all sequences of a call: with many single tokens and one chunk of
+ * several times B tokens two calls, one for each kind, may take less time.
  * T = 0, Hq = 0 or B = 0 is a valid empty problem.  Errors as fa2_forward.
  */
 int fa2_forward_paged(const fa2_paged_cache *cache, const void *Q, long long q_token_stride,
@@ -417,7 +420,9 @@ int fa2_append_paged(const fa2_paged_cache *cache, const void *K, const long lon
  * most 2^21 - 1.  Entries that contradict each other (a page number outside the
  * pool, a freed page freed again, a sequence index outside [0, B)) are skipped
  * and reported as FA2_ERR_PAGE by the device status word.  Lists (src, dst, seqs)
- * hold at most 65536 indices.  Calls on the same tables go on one stream.
+ * hold at most 65536 indices; those of pages_copy and pages_free are searched for
+ * repeated ones, which beyond some thousand costs the square of their length.
+ * Calls on the same tables go on one stream.
  */
 typedef struct {
   int *page_table;
@@ -430,7 +435,8 @@ typedef struct {
 /*
  * The page data that moves with the tables: num_planes (0 .. 256) arrays of
  * num_pages pages of page_bytes dense bytes (a multiple of 16), page_stride
- * bytes apart; `planes` is a host array of device pointers.
+ * bytes apart, no two of which share a page's bytes; `planes` is a host array of
+ * device pointers.
  */
 typedef struct {
   void *const *planes;
@@ -475,8 +481,9 @@ int fa2_pages_compact(const fa2_page_tables *tables, const fa2_page_pools *pools
 
 /*
  * Copies page src[i] to page dst[i], i < n (device lists).  Of several pairs
- * with one destination the last counts.  A pair whose source is another pair's
- * destination, or with a number outside the pool, is skipped (FA2_ERR_PAGE).
+ * with one destination the last counts, also where it is skipped.  A pair whose
+ * source is another pair's destination, or with a number outside the pool, is
+ * skipped (FA2_ERR_PAGE).
  */
 int fa2_pages_copy(const fa2_page_pools *pools, const int *src, const int *dst, int n,
                    void *workspace, size_t workspace_size, fa2_stream_t stream);
