@@ -422,6 +422,8 @@ int fa2_append_paged(const fa2_paged_cache *cache, const void *K, const long lon
  * and reported as FA2_ERR_PAGE by the device status word.  Lists (src, dst, seqs)
  * hold at most 65536 indices; those of pages_copy and pages_free are searched for
  * repeated ones, which beyond some thousand costs the square of their length.
+ * In these functions a length below zero counts as 0; one past its table row makes
+ * reserve answer -1, and fork take the row's.
  * Calls on the same tables go on one stream.
  */
 typedef struct {
