@@ -53,6 +53,10 @@ SIGNATURES = {
     "fa2_forward_paged_workspace_bytes": (_Z, [_I] * 6),
     "fa2_rope": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _LL, _P, _I, _I, _F, _I, _I, _P]),
     "fa2_append_paged": (_I, [_P] * 9 + [_I, _P, _I, _P, _I, _I, _F, _P]),
+    "fa2_norm_rope": (_I, [_P] * 4 + [_I] * 4 + [_P, _I, _F, _P, _I, _LL, _P, _I, _I, _F, _I, _P]),
+    "fa2_norm_rope_backward": (_I, [_P] * 6 + [_I] * 4 + [_P, _I, _F, _P, _I, _LL, _P, _I, _I, _F, _I, _P, _P, _Z, _P]),
+    "fa2_norm_rope_backward_workspace_bytes": (_Z, [_I]),
+    "fa2_append_paged_norm": (_I, [_P] * 9 + [_I, _P, _I, _P, _P, _I, _F, _P, _I, _I, _F, _P]),
     "fa2_pages_workspace_bytes": (_Z, [_I, _I]),
     "fa2_pages_reserve": (_I, [_P, _P, _P, _P, _Z, _P]),
     "fa2_pages_fork": (_I, [_P, _P, _P, _P, _I, _P, _P, _Z, _P]),
@@ -437,5 +441,6 @@ def backward(q, k, v, o, lse, do, causal: bool = False, scale: float | None = No
     return dq, dk, dv
 
 
+from .norm import norm_rope, norm_rope_backward  # noqa: E402
 from .paged import (append_paged, forward_paged, pages_compact, pages_copy, pages_fork, pages_free,  # noqa: E402
                     pages_reserve, rope, rope_backward, rope_inv_freq)

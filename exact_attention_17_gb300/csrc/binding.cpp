@@ -38,6 +38,10 @@ decltype(&fa2_pages_fork) fork_fn;
 decltype(&fa2_pages_free) free_fn;
 decltype(&fa2_pages_compact) compact_fn;
 decltype(&fa2_pages_copy) copy_fn;
+decltype(&fa2_append_paged_norm) append_norm_fn;
+decltype(&fa2_norm_rope) norm_fn;
+decltype(&fa2_norm_rope_backward) norm_backward_fn;
+decltype(&fa2_norm_rope_backward_workspace_bytes) norm_workspace_fn;
 
 const at::Tensor* tensor(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
 
@@ -156,6 +160,29 @@ bool frequencies(PyObject* o, at::Device device, int64_t d, const double** out, 
   return true;
 }
 
+PyObject* pair_of(at::Tensor&& a, at::Tensor&& b) {
+  PyObject* pair = PyTuple_New(2);
+  if (!pair) return nullptr;
+  PyTuple_SET_ITEM(pair, 0, THPVariable_Wrap(std::move(a)));
+  PyTuple_SET_ITEM(pair, 1, THPVariable_Wrap(std::move(b)));
+  return pair;
+}
+
+// A norm's weights of the rows' type or fp32 (null for None); *code: their type, left as it is for None
+bool weights(PyObject* o, int64_t d, at::ScalarType type, at::Device device, const void** out, int* code) {
+  *out = nullptr;
+  if (o == Py_None) return true;
+  const at::Tensor* t = tensor(o);
+  if (!t || (t->scalar_type() != type && t->scalar_type() != at::kFloat) || t->dim() != 1 || t->size(0) != d ||
+      !t->is_contiguous() || t->device() != device)
+    return false;
+  const int own = type_code(*t);
+  if (*code >= 0 && *code != own) return false;
+  *code = own;
+  *out = t->data_ptr();
+  return true;
+}
+
 // (q, k_pages, v_pages, page_table, kv_lens, cu_q, causal, scale)
 PyObject* forward_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
@@ -182,20 +209,16 @@ PyObject* forward_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
                               static_cast<float>(scale), c.dtype, ws.data_ptr(), size, s);
     });
     if (rc != FA2_OK) return PyLong_FromLong(rc);
-    PyObject* pair = PyTuple_New(2);
-    if (!pair) return nullptr;
-    PyTuple_SET_ITEM(pair, 0, THPVariable_Wrap(std::move(o)));
-    PyTuple_SET_ITEM(pair, 1, THPVariable_Wrap(std::move(lse)));
-    return pair;
+    return pair_of(std::move(o), std::move(lse));
   });
 }
 
-// (k, v, k_pages, v_pages, page_table, kv_lens, cu_q, q, inv_freq, interleaved, mscale)
+// (k, v, k_pages, v_pages, page_table, kv_lens, cu_q, q, inv_freq, interleaved, mscale, q_weight, k_weight, eps)
 PyObject* append_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     fa2_paged_cache c;
     at::Device device(at::kCPU);
-    const at::Tensor *k = n == 11 ? tensor(a[0]) : nullptr, *v = n == 11 ? tensor(a[1]) : nullptr;
+    const at::Tensor *k = n == 14 ? tensor(a[0]) : nullptr, *v = n == 14 ? tensor(a[1]) : nullptr;
     const at::Tensor* q = k ? tensor(a[7]) : nullptr;
     if (!k || !v || !q || k->dim() != 3 || q->dim() != 3 || !cache_of(a + 2, &c, &device)) return none();
     const int64_t T = k->size(0), Hq = q->size(1);
@@ -209,12 +232,21 @@ PyObject* append_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
       return none();
     const int interleaved = PyObject_IsTrue(a[9]);
     const double mscale = PyFloat_AsDouble(a[10]);
+    const void *q_weight, *k_weight;
+    int code = -1;
+    if (!weights(a[11], c.d, type, device, &q_weight, &code) || !weights(a[12], c.d, type, device, &k_weight, &code))
+      return none();
+    const double eps = PyFloat_AsDouble(a[13]);
     if (interleaved < 0 || PyErr_Occurred()) return nullptr;
     at::Tensor out = make(q->sizes(), type, device);
     const long long ks[2] = {k->stride(0), k->stride(1)}, vs[2] = {v->stride(0), v->stride(1)};
     const long long qs[2] = {q->stride(0), q->stride(1)}, os[2] = {out.stride(0), out.stride(1)};
     const fa2_stream_t s = stream_of(device);
     const int rc = call([&] {
+      if (q_weight || k_weight)
+        return append_norm_fn(&c, k->data_ptr(), ks, v->data_ptr(), vs, q->data_ptr(), qs, out.data_ptr(), os,
+                              static_cast<int>(Hq), cu, static_cast<int>(T), q_weight, k_weight, code,
+                              static_cast<float>(eps), freq, rotary, interleaved, static_cast<float>(mscale), s);
       return append_fn(&c, k->data_ptr(), ks, v->data_ptr(), vs, q->data_ptr(), qs, out.data_ptr(), os,
                        static_cast<int>(Hq), cu, static_cast<int>(T), freq, rotary, interleaved,
                        static_cast<float>(mscale), s);
@@ -223,37 +255,126 @@ PyObject* append_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// Rows of heads, [B, H, N, d] or packed [T, H, d], with their positions.
+struct Heads {
+  int64_t B, H, N, d;
+  long long s[3];   // {batch, head, token}
+  const void* positions;
+  int wide;
+  long long batch_stride;
+};
+
+void strides_of(const at::Tensor& x, long long (&s)[3]) {
+  const bool packed = x.dim() == 3;
+  s[0] = packed ? 0 : x.stride(0);
+  s[1] = x.stride(1);
+  s[2] = packed ? x.stride(0) : x.stride(2);
+}
+
+bool heads_of(const at::Tensor* x, const at::Tensor* pos, Heads* h) {
+  if (!x || !pos || (x->dim() != 3 && x->dim() != 4) || !current(x->device()) || type_code(*x) < 0 ||
+      x->stride(-1) != 1 || !fits_int(x->sizes()))
+    return false;
+  const bool packed = x->dim() == 3;
+  h->B = packed ? 1 : x->size(0);
+  h->H = x->size(1);
+  h->N = packed ? x->size(0) : x->size(2);
+  h->d = x->size(-1);
+  strides_of(*x, h->s);
+  h->wide = pos->scalar_type() == at::kLong;
+  if ((!h->wide && pos->scalar_type() != at::kInt) || pos->device() != x->device() ||
+      !(pos->sizes() == c10::IntArrayRef({h->N}) || pos->sizes() == c10::IntArrayRef({h->B, h->N})) ||
+      (h->N > 1 && pos->stride(-1) != 1))
+    return false;
+  h->positions = pos->data_ptr();
+  h->batch_stride = pos->dim() == 2 ? pos->stride(0) : 0;
+  return true;
+}
+
 // (x, positions, inv_freq, interleaved, mscale, transposed)
 PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     const at::Tensor *x = n == 6 ? tensor(a[0]) : nullptr, *pos = x ? tensor(a[1]) : nullptr;
-    if (!x || !pos || (x->dim() != 3 && x->dim() != 4) || !current(x->device()) || type_code(*x) < 0 ||
-        x->stride(-1) != 1 || !fits_int(x->sizes()))
-      return none();
-    const bool packed = x->dim() == 3;
-    const int64_t B = packed ? 1 : x->size(0), H = x->size(1), N = packed ? x->size(0) : x->size(2), d = x->size(-1);
-    const bool wide = pos->scalar_type() == at::kLong;
-    if ((!wide && pos->scalar_type() != at::kInt) || pos->device() != x->device() ||
-        !(pos->sizes() == c10::IntArrayRef({N}) || pos->sizes() == c10::IntArrayRef({B, N})) ||
-        (N > 1 && pos->stride(-1) != 1))
-      return none();
+    Heads h;
     const double* freq;
     int rotary;
-    if (!frequencies(a[2], x->device(), d, &freq, &rotary)) return none();
+    if (!heads_of(x, pos, &h) || !frequencies(a[2], x->device(), h.d, &freq, &rotary)) return none();
     const int interleaved = PyObject_IsTrue(a[3]), transposed = PyObject_IsTrue(a[5]);
     const double mscale = PyFloat_AsDouble(a[4]);
     if (interleaved < 0 || transposed < 0 || PyErr_Occurred()) return nullptr;
     at::Tensor y = make(x->sizes(), x->scalar_type(), x->device());
-    // {batch, head, token}
-    const long long xs[3] = {packed ? 0 : x->stride(0), x->stride(1), packed ? x->stride(0) : x->stride(2)};
-    const long long ys[3] = {packed ? 0 : y.stride(0), y.stride(1), packed ? y.stride(0) : y.stride(2)};
+    long long ys[3];
+    strides_of(y, ys);
     const fa2_stream_t s = stream_of(x->device());
     const int rc = call([&] {
-      return rope_fn(x->data_ptr(), xs, y.data_ptr(), ys, static_cast<int>(B), static_cast<int>(H), static_cast<int>(N),
-                     static_cast<int>(d), pos->data_ptr(), wide, pos->dim() == 2 ? pos->stride(0) : 0, freq, rotary,
+      return rope_fn(x->data_ptr(), h.s, y.data_ptr(), ys, static_cast<int>(h.B), static_cast<int>(h.H),
+                     static_cast<int>(h.N), static_cast<int>(h.d), h.positions, h.wide, h.batch_stride, freq, rotary,
                      interleaved, static_cast<float>(mscale), transposed, type_code(*x), s);
     });
     return result(rc, std::move(y));
+  });
+}
+
+// (x, weight, positions, inv_freq, eps, interleaved, mscale)
+PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const at::Tensor *x = n == 7 ? tensor(a[0]) : nullptr, *pos = x ? tensor(a[2]) : nullptr;
+    Heads h;
+    const double* freq;
+    const void* weight;
+    int rotary, code = -1;
+    if (!heads_of(x, pos, &h) || !weights(a[1], h.d, x->scalar_type(), x->device(), &weight, &code) || !weight ||
+        !frequencies(a[3], x->device(), h.d, &freq, &rotary))
+      return none();
+    const double eps = PyFloat_AsDouble(a[4]), mscale = PyFloat_AsDouble(a[6]);
+    const int interleaved = PyObject_IsTrue(a[5]);
+    if (interleaved < 0 || PyErr_Occurred()) return nullptr;
+    at::Tensor y = make(x->sizes(), x->scalar_type(), x->device());
+    long long ys[3];
+    strides_of(y, ys);
+    const fa2_stream_t s = stream_of(x->device());
+    const int rc = call([&] {
+      return norm_fn(x->data_ptr(), h.s, y.data_ptr(), ys, static_cast<int>(h.B), static_cast<int>(h.H),
+                     static_cast<int>(h.N), static_cast<int>(h.d), weight, code, static_cast<float>(eps), h.positions,
+                     h.wide, h.batch_stride, freq, rotary, interleaved, static_cast<float>(mscale), type_code(*x), s);
+    });
+    return result(rc, std::move(y));
+  });
+}
+
+// (dy, x, weight, positions, inv_freq, eps, interleaved, mscale)
+PyObject* norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const at::Tensor *dy = n == 8 ? tensor(a[0]) : nullptr, *x = dy ? tensor(a[1]) : nullptr;
+    const at::Tensor* pos = x ? tensor(a[3]) : nullptr;
+    Heads h;
+    const double* freq;
+    const void* weight;
+    int rotary, code = -1;
+    if (!heads_of(x, pos, &h) || dy->scalar_type() != x->scalar_type() || dy->sizes() != x->sizes() ||
+        dy->device() != x->device() || dy->stride(-1) != 1 ||
+        !weights(a[2], h.d, x->scalar_type(), x->device(), &weight, &code) || !weight ||
+        !frequencies(a[4], x->device(), h.d, &freq, &rotary))
+      return none();
+    const double eps = PyFloat_AsDouble(a[5]), mscale = PyFloat_AsDouble(a[7]);
+    const int interleaved = PyObject_IsTrue(a[6]);
+    if (interleaved < 0 || PyErr_Occurred()) return nullptr;
+    at::Tensor dx = make(x->sizes(), x->scalar_type(), x->device()), dw = make({h.d}, at::kFloat, x->device());
+    const size_t size = norm_workspace_fn(static_cast<int>(h.d));
+    at::Tensor ws = make({static_cast<int64_t>(size > 0 ? size : 1)}, at::kByte, x->device());
+    long long gs[3], ys[3];
+    strides_of(*dy, gs);
+    strides_of(dx, ys);
+    const fa2_stream_t s = stream_of(x->device());
+    const int rc = call([&] {
+      return norm_backward_fn(dy->data_ptr(), gs, x->data_ptr(), h.s, dx.data_ptr(), ys, static_cast<int>(h.B),
+                              static_cast<int>(h.H), static_cast<int>(h.N), static_cast<int>(h.d), weight, code,
+                              static_cast<float>(eps), h.positions, h.wide, h.batch_stride, freq, rotary, interleaved,
+                              static_cast<float>(mscale), type_code(*x), static_cast<float*>(dw.data_ptr()),
+                              ws.data_ptr(), size, s);
+    });
+    if (rc != FA2_OK) return PyLong_FromLong(rc);
+    return pair_of(std::move(dx), std::move(dw));
   });
 }
 
@@ -433,7 +554,9 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
                  reinterpret_cast<void**>(&rope_fn), reinterpret_cast<void**>(&append_fn),
                  reinterpret_cast<void**>(&pages_workspace_fn), reinterpret_cast<void**>(&reserve_fn),
                  reinterpret_cast<void**>(&fork_fn), reinterpret_cast<void**>(&free_fn),
-                 reinterpret_cast<void**>(&compact_fn), reinterpret_cast<void**>(&copy_fn)};
+                 reinterpret_cast<void**>(&compact_fn), reinterpret_cast<void**>(&copy_fn),
+                 reinterpret_cast<void**>(&append_norm_fn), reinterpret_cast<void**>(&norm_fn),
+                 reinterpret_cast<void**>(&norm_backward_fn), reinterpret_cast<void**>(&norm_workspace_fn)};
   constexpr Py_ssize_t count = sizeof to / sizeof to[0];
   if (n != count) {
     PyErr_SetString(PyExc_ValueError, "init takes one address for each function");
@@ -452,6 +575,7 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef methods[] = {FA2_METHOD(init),          FA2_METHOD(forward_paged), FA2_METHOD(append_paged),
                          FA2_METHOD(rope),          FA2_METHOD(pages_reserve), FA2_METHOD(pages_fork),
                          FA2_METHOD(pages_free),    FA2_METHOD(pages_compact), FA2_METHOD(pages_copy),
+                         FA2_METHOD(norm_rope),     FA2_METHOD(norm_rope_backward),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

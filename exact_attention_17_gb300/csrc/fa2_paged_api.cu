@@ -1,119 +1,11 @@
 // Host side of the paged-cache entry points (include/fa2.h): argument
 // validation, tensor maps, launch plans.
-#include <cmath>
-#include <cstdint>
-
-#include "fa2.h"
-#include "fa2_host.h"
+#include "fa2_checks.h"
 #include "fa2_launch.h"
+#include "fa2_norm.h"
 #include "fa2_pages.h"
-#include "fa2_rope.h"
 
 namespace {
-
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr long long kMaxStride = 1ll << 38;   // elements; TMA strides stay below 2^40 bytes
-
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-
-bool misaligned(const void* p, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; }
-
-int log2_exact(int x) {
-  int l = 0;
-  while ((1 << l) < x) ++l;
-  return (1 << l) == x ? l : -1;
-}
-
-int page_log2(int page_size) {
-  return page_size >= 16 && page_size <= 1024 ? log2_exact(page_size) : -1;
-}
-
-// Elements that a strided array reaches, or -1: sizes and strides of its outer
-// dimensions, the last dimension of `inner` neighbouring elements.
-template <int N>
-long long extent(const long long (&sizes)[N], const long long (&strides)[N], long long inner) {
-  long long e = inner;
-  for (int i = 0; i < N; ++i) {
-    if (strides[i] < 0 || strides[i] > kMaxStride || sizes[i] < 0 || sizes[i] > 0x7fffffffll) return -1;
-    if (sizes[i] > 1) {
-      if (strides[i] > (1ll << 60) / sizes[i]) return -1;
-      e += (sizes[i] - 1) * strides[i];
-    }
-  }
-  return e;
-}
-
-// The rows of an array that is written lie apart: with its outer dimensions (those
-// of more than one step) in the order of their strides, each steps past all that
-// the smaller ones reach.  Strides that interleave dimensions without a common
-// element are refused too; no view of a dense array has such.
-template <int N>
-bool rows_apart(const long long (&sizes)[N], const long long (&strides)[N], long long inner) {
-  bool taken[N] = {};
-  long long reach = inner;
-  for (int n = 0; n < N; ++n) {
-    int least = -1;
-    for (int i = 0; i < N; ++i)
-      if (!taken[i] && sizes[i] > 1 && (least < 0 || strides[i] < strides[least])) least = i;
-    if (least < 0) return true;
-    if (strides[least] < reach) return false;
-    if (strides[least] > (1ll << 60) / sizes[least]) return false;
-    reach += (sizes[least] - 1) * strides[least];
-    taken[least] = true;
-  }
-  return true;
-}
-
-bool range_ok(const void* p, long long elems, int size) {
-  return elems >= 0 && fa2host::device_memory_ok(p, static_cast<size_t>(elems) * size);
-}
-
-// Everything about a cache that can be checked on the host without a device.
-int check_cache(const fa2_paged_cache* c) {
-  if (!c) return FA2_ERR_NULL;
-  if (c->dtype != FA2_DTYPE_BF16 && c->dtype != FA2_DTYPE_FP16) return FA2_ERR_DTYPE;
-  if (c->num_pages < 1 || c->kv_heads < 1 || c->B < 0 || c->table_width < 1 || page_log2(c->page_size) < 0)
-    return FA2_ERR_SHAPE;
-  if (c->d != 64 && c->d != 128 && c->d != 256) return FA2_ERR_HEADDIM;
-  if (static_cast<long long>(c->table_width) * c->page_size > (1ll << 30)) return FA2_ERR_SHAPE;
-  // a slot, a head and a page may not overlap the next
-  if (c->slot_stride < c->d || c->slot_stride > kMaxStride) return FA2_ERR_SHAPE;
-  if (c->kv_heads > 1 && (c->head_stride < c->d || c->head_stride > kMaxStride)) return FA2_ERR_SHAPE;
-  if (c->num_pages > 1 && (c->page_stride < c->d || c->page_stride > kMaxStride)) return FA2_ERR_SHAPE;
-  if (c->B > 1 && (c->table_stride < c->table_width || c->table_stride > kMaxStride)) return FA2_ERR_SHAPE;
-  if (!c->k_pages || !c->v_pages || !c->page_table || !c->kv_lens) return FA2_ERR_NULL;
-  if (misaligned(c->k_pages, 15) || misaligned(c->v_pages, 15) || c->slot_stride % 8 != 0 ||
-      (c->kv_heads > 1 && c->head_stride % 8 != 0) || (c->num_pages > 1 && c->page_stride % 8 != 0) ||
-      misaligned(c->page_table, 3) || misaligned(c->kv_lens, 3))
-    return FA2_ERR_ALIGN;
-  return FA2_OK;
-}
-
-int check_cache_memory(const fa2_paged_cache* c) {
-  const long long sizes[3] = {c->num_pages, c->kv_heads, c->page_size};
-  const long long strides[3] = {c->num_pages > 1 ? c->page_stride : 0, c->kv_heads > 1 ? c->head_stride : 0,
-                                c->slot_stride};
-  const long long e = extent(sizes, strides, c->d);
-  const long long ts[1] = {c->B}, tr[1] = {c->B > 1 ? c->table_stride : 0};
-  if (!range_ok(c->k_pages, e, 2) || !range_ok(c->v_pages, e, 2) ||
-      !range_ok(c->page_table, extent(ts, tr, c->table_width), 4) || !range_ok(c->kv_lens, c->B, 4))
-    return FA2_ERR_MEMORY;
-  return FA2_OK;
-}
-
-// Packed rows [T, H, d]: token and head strides in elements.
-int check_rows(const void* p, long long token, long long head, long long T, int H, int d) {
-  if ((T > 1 && (token < d || token > kMaxStride)) || (H > 1 && (head < d || head > kMaxStride))) return FA2_ERR_SHAPE;
-  if (!p) return FA2_ERR_NULL;
-  if (misaligned(p, 15) || (T > 1 && token % 8 != 0) || (H > 1 && head % 8 != 0)) return FA2_ERR_ALIGN;
-  return FA2_OK;
-}
-
-bool rows_in_memory(const void* p, long long token, long long head, long long T, int H, int d) {
-  const long long sizes[2] = {T, H};
-  const long long strides[2] = {T > 1 ? token : 0, H > 1 ? head : 0};
-  return range_ok(p, extent(sizes, strides, d), 2);
-}
 
 // How a call of fa2_forward_paged is laid out; depends on sizes alone.
 struct PagedPlan {
@@ -285,24 +177,6 @@ extern "C" int fa2_forward_paged(const fa2_paged_cache* cache, const void* Q, lo
              : FA2_ERR_LAUNCH;
 }
 
-namespace {
-
-int check_rotary(const double* inv_freq, int rotary_dim, int d, float mscale) {
-  if (rotary_dim < 0 || rotary_dim > d || rotary_dim % 2 != 0) return FA2_ERR_SHAPE;
-  if (!std::isfinite(mscale)) return FA2_ERR_SCALE;
-  if (rotary_dim > 0 && !inv_freq) return FA2_ERR_NULL;
-  if (misaligned(inv_freq, 7)) return FA2_ERR_ALIGN;
-  return FA2_OK;
-}
-
-// Whole vectors fill the rotated columns (their halves, unless interleaved) and the rest.
-bool wide_rotary(int d, int r, bool interleaved, int elem) {
-  const int w = fa2host::rope_width(elem, interleaved);
-  return d % w == 0 && (interleaved ? r % w == 0 : r % (2 * w) == 0);
-}
-
-}  // namespace
-
 extern "C" int fa2_rope(const void* X, const long long* x_strides, void* Y, const long long* y_strides, int B, int H,
                         int N, int d, const void* positions, int positions_int64, long long positions_batch_stride,
                         const double* inv_freq, int rotary_dim, int interleaved, float mscale, int transposed,
@@ -369,11 +243,19 @@ extern "C" int fa2_rope(const void* X, const long long* x_strides, void* Y, cons
              : FA2_ERR_LAUNCH;
 }
 
-extern "C" int fa2_append_paged(const fa2_paged_cache* cache, const void* K, const long long* k_strides, const void* V,
-                                const long long* v_strides, const void* Q, const long long* q_strides, void* Q_out,
-                                const long long* q_out_strides, int Hq, const int* cu_q, int T,
-                                const double* inv_freq, int rotary_dim, int interleaved, float mscale,
-                                fa2_stream_t stream) {
+namespace {
+
+// The weights of the append's norms; both null: none is asked for.
+struct AppendNorm {
+  const void *q_weight, *k_weight;
+  int weight_dtype;
+  float eps;
+};
+
+int append_paged(const fa2_paged_cache* cache, const void* K, const long long* k_strides, const void* V,
+                 const long long* v_strides, const void* Q, const long long* q_strides, void* Q_out,
+                 const long long* q_out_strides, int Hq, const int* cu_q, int T, const double* inv_freq,
+                 int rotary_dim, int interleaved, float mscale, const AppendNorm& norm, fa2_stream_t stream) {
   if (!cache) return FA2_ERR_NULL;
   if (T < 0 || Hq < 0) return FA2_ERR_SHAPE;
   if (T == 0 || cache->B == 0) return FA2_OK;
@@ -383,6 +265,10 @@ extern "C" int fa2_append_paged(const fa2_paged_cache* cache, const void* K, con
   if (!cu_q && T != c.B) return FA2_ERR_SHAPE;
   if (Hq > (1 << 20) || c.kv_heads > (1 << 20)) return FA2_ERR_SHAPE;
   if ((rc = check_rotary(inv_freq, rotary_dim, c.d, mscale)) != FA2_OK) return rc;
+  const bool normed = norm.q_weight || norm.k_weight;
+  if (normed && (rc = check_norm(norm.weight_dtype, c.dtype, norm.eps)) != FA2_OK) return rc;
+  const int weight_size = norm.weight_dtype == FA2_DTYPE_FP32 ? 4 : 2;
+  if (misaligned(norm.q_weight, weight_size - 1) || misaligned(norm.k_weight, weight_size - 1)) return FA2_ERR_ALIGN;
   if (!k_strides || !v_strides) return FA2_ERR_NULL;
   if ((rc = check_rows(K, k_strides[0], k_strides[1], T, c.kv_heads, c.d)) != FA2_OK) return rc;
   if ((rc = check_rows(V, v_strides[0], v_strides[1], T, c.kv_heads, c.d)) != FA2_OK) return rc;
@@ -405,7 +291,9 @@ extern "C" int fa2_append_paged(const fa2_paged_cache* cache, const void* K, con
       !rows_in_memory(V, v_strides[0], v_strides[1], T, c.kv_heads, c.d) ||
       (Hq > 0 && (!rows_in_memory(Q, q_strides[0], q_strides[1], T, Hq, c.d) ||
                   !rows_in_memory(Q_out, q_out_strides[0], q_out_strides[1], T, Hq, c.d))) ||
-      (cu_q && !range_ok(cu_q, c.B + 1ll, 4)) || (rotary_dim > 0 && !range_ok(inv_freq, rotary_dim / 2, 8)))
+      (cu_q && !range_ok(cu_q, c.B + 1ll, 4)) || (rotary_dim > 0 && !range_ok(inv_freq, rotary_dim / 2, 8)) ||
+      (norm.q_weight && !range_ok(norm.q_weight, c.d, weight_size)) ||
+      (norm.k_weight && !range_ok(norm.k_weight, c.d, weight_size)))
     return FA2_ERR_MEMORY;
   fa2dev::RopeParams p = {};
   p.q = Q;
@@ -449,11 +337,41 @@ extern "C" int fa2_append_paged(const fa2_paged_cache* cache, const void* K, con
   p.mscale = mscale;
   p.total_tokens = T;
   p.total_rows = Hq + 2 * c.kv_heads;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (normed) {
+    fa2dev::NormParams np = {};
+    np.r = p;
+    np.weight = norm.q_weight;
+    np.k_weight = norm.k_weight;
+    np.weight32 = norm.weight_dtype == FA2_DTYPE_FP32;
+    np.eps = norm.eps;
+    const bool wide = wide_norm(rotary_dim, interleaved != 0, 2);
+    return fa2host::launch_norm_rope(np, true, c.dtype, wide, fa2host::device_sms(), s) == cudaSuccess ? FA2_OK
+                                                                                                      : FA2_ERR_LAUNCH;
+  }
   const bool wide = wide_rotary(c.d, rotary_dim, interleaved != 0, 2);
-  return fa2host::launch_rope(p, true, c.dtype, wide, fa2host::device_sms(),
-                              reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? FA2_OK
-             : FA2_ERR_LAUNCH;
+  return fa2host::launch_rope(p, true, c.dtype, wide, fa2host::device_sms(), s) == cudaSuccess ? FA2_OK : FA2_ERR_LAUNCH;
+}
+
+}  // namespace
+
+extern "C" int fa2_append_paged(const fa2_paged_cache* cache, const void* K, const long long* k_strides, const void* V,
+                                const long long* v_strides, const void* Q, const long long* q_strides, void* Q_out,
+                                const long long* q_out_strides, int Hq, const int* cu_q, int T,
+                                const double* inv_freq, int rotary_dim, int interleaved, float mscale,
+                                fa2_stream_t stream) {
+  return append_paged(cache, K, k_strides, V, v_strides, Q, q_strides, Q_out, q_out_strides, Hq, cu_q, T, inv_freq,
+                      rotary_dim, interleaved, mscale, {}, stream);
+}
+
+extern "C" int fa2_append_paged_norm(const fa2_paged_cache* cache, const void* K, const long long* k_strides,
+                                     const void* V, const long long* v_strides, const void* Q,
+                                     const long long* q_strides, void* Q_out, const long long* q_out_strides, int Hq,
+                                     const int* cu_q, int T, const void* q_weight, const void* k_weight,
+                                     int weight_dtype, float eps, const double* inv_freq, int rotary_dim,
+                                     int interleaved, float mscale, fa2_stream_t stream) {
+  return append_paged(cache, K, k_strides, V, v_strides, Q, q_strides, Q_out, q_out_strides, Hq, cu_q, T, inv_freq,
+                      rotary_dim, interleaved, mscale, {q_weight, k_weight, weight_dtype, eps}, stream);
 }
 
 namespace {

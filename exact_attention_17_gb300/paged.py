@@ -58,7 +58,8 @@ def _load():
         _binding.init(*(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in (
             "fa2_forward_paged", "fa2_forward_paged_workspace_bytes", "fa2_rope", "fa2_append_paged",
             "fa2_pages_workspace_bytes", "fa2_pages_reserve", "fa2_pages_fork", "fa2_pages_free", "fa2_pages_compact",
-            "fa2_pages_copy")))
+            "fa2_pages_copy", "fa2_append_paged_norm", "fa2_norm_rope", "fa2_norm_rope_backward",
+            "fa2_norm_rope_backward_workspace_bytes")))
         _fast = _binding
     _codes = fa2._dtype_codes()
     _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None) or (lambda i: t.cuda.current_stream(i).cuda_stream)
@@ -254,19 +255,25 @@ def _inv_freq_args(inv_freq, device, d):
 
 
 def append_paged(k, v, k_pages, v_pages, page_table, kv_lens, cu_q=None, q=None, q_out=None, inv_freq=None,
-                 interleaved: bool = False, mscale: float = 1.0, stream=None):
-    """Write new tokens into a paged cache (fa2_append_paged).
+                 interleaved: bool = False, mscale: float = 1.0, stream=None, q_weight=None, k_weight=None,
+                 eps: float = 1e-6):
+    """Write new tokens into a paged cache (fa2_append_paged, fa2_append_paged_norm).
 
     k, v [T, Hkv, d] go to their sequences' pages at positions kv_lens[b] - c_b
     + i (the pages must be there: ``pages_reserve``), k rotated at its position
     when ``inv_freq`` is given (see ``rope``).  With ``q`` [T, Hq, d] the
     queries are rotated in the same launch and returned (``q_out``; pass
     ``q_out=q`` to rotate in place).  Rows behind cu_q[B] are not touched.
+
+    ``q_weight`` and ``k_weight`` [d] (both of the cache's type, or both fp32) norm
+    each query's and key's row before it is rotated, as ``norm_rope`` does with
+    ``eps``; either may be None.
     """
     if torch is None:
         _load()
     if _fast is not None and q is not None and q_out is None and stream is None:
-        r = _fast.append_paged(k, v, k_pages, v_pages, page_table, kv_lens, cu_q, q, inv_freq, interleaved, mscale)
+        r = _fast.append_paged(k, v, k_pages, v_pages, page_table, kv_lens, cu_q, q, inv_freq, interleaved, mscale,
+                               q_weight, k_weight, eps)
         if r is not None:
             return _answer(r, "fa2_append_paged")
     dtype, device = k_pages.dtype, k_pages.device
@@ -280,6 +287,15 @@ def append_paged(k, v, k_pages, v_pages, page_table, kv_lens, cu_q=None, q=None,
     vs = _rows("v", v, shape, dtype, device)
     offsets = _offsets(cu_q, args.B, T, device)
     freq, rotary_dim = _inv_freq_args(inv_freq, device, d)
+    normed = q_weight is not None or k_weight is not None
+    if normed:
+        if q_weight is not None and q is None:
+            raise ValueError("q_weight without q")
+        if q_weight is not None and k_weight is not None and q_weight.dtype is not k_weight.dtype:
+            raise ValueError("q_weight and k_weight must have the same type")
+        q_norm, _ = _weight_args("q_weight", q_weight, d, dtype, device)
+        k_norm, _ = _weight_args("k_weight", k_weight, d, dtype, device)
+        code = _codes[(k_weight if q_weight is None else q_weight).dtype]
     with _Call(device, stream) as handle:
         if q is None:
             if q_out is not None:
@@ -295,12 +311,26 @@ def append_paged(k, v, k_pages, v_pages, page_table, kv_lens, cu_q=None, q=None,
             so = _rows("q_out", q_out, (T, Hq, d), dtype, device)
             queries, queries_out = q.data_ptr(), q_out.data_ptr()
             qs, qos = _LL2(st[0], st[1]), _LL2(so[0], so[1])
-        rc = _lib.fa2_append_paged(ctypes.byref(args), k.data_ptr(), _LL2(ks[0], ks[1]), v.data_ptr(),
-                                   _LL2(vs[0], vs[1]), queries, qs, queries_out, qos, Hq, offsets, T, freq, rotary_dim,
-                                   1 if interleaved else 0, mscale, handle)
+        arrays = (ctypes.byref(args), k.data_ptr(), _LL2(ks[0], ks[1]), v.data_ptr(), _LL2(vs[0], vs[1]), queries, qs,
+                  queries_out, qos, Hq, offsets, T)
+        rotary = (freq, rotary_dim, 1 if interleaved else 0, mscale, handle)
+        if normed:
+            rc = _lib.fa2_append_paged_norm(*arrays, q_norm, k_norm, code, eps, *rotary)
+        else:
+            rc = _lib.fa2_append_paged(*arrays, *rotary)
     if rc:
-        _fail(rc, "fa2_append_paged")
+        _fail(rc, "fa2_append_paged_norm" if normed else "fa2_append_paged")
     return q_out
+
+
+def _weight_args(name, weight, d, dtype, device):
+    """Pointer of a norm's weights (None for none) and the code of their type."""
+    if weight is None:
+        return None, None
+    if ((weight.dtype is not dtype and weight.dtype is not torch.float32) or weight.shape != (d,)
+            or not weight.is_contiguous() or weight.device != device):
+        raise ValueError(f"{name} must be a contiguous {dtype} or fp32 tensor of shape {(d,)} on {device}")
+    return weight.data_ptr(), _codes[weight.dtype]
 
 
 def rope_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
@@ -345,6 +375,41 @@ def rope_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: str | None = 
     return torch.tensor(freq, dtype=torch.float64, device=device)
 
 
+def _strides3(t):
+    """Strides {batch, head, token} of [B, H, N, d], or of packed [T, H, d]: one batch, tokens outside the heads."""
+    s = t.stride()
+    return _LL3(s[0], s[1], s[2]) if len(s) == 4 else _LL3(0, s[1], s[0])
+
+
+def _heads(name, x):
+    """Rows of heads, [B, H, N, d] or [T, H, d]: their sizes B, H, N, d and strides."""
+    dim = x.dim()
+    if x.dtype not in _codes or not x.is_cuda or (dim != 4 and dim != 3) or x.stride(-1) != 1:
+        raise ValueError(f"{name} must be a bf16, fp16 or fp32 CUDA tensor [T, H, d] or [B, H, N, d], last dimension dense")
+    _sizes(*x.shape)
+    if dim == 3:
+        N, H, d = x.shape
+        return 1, H, N, d, _strides3(x)
+    return (*x.shape, _strides3(x))
+
+
+def _like(name, t, x):
+    """Strides of an array that must match x in type, shape and device, last dimension dense."""
+    if t.dtype is not x.dtype or t.shape != x.shape or t.device != x.device or t.stride(-1) != 1:
+        raise ValueError(f"{name} must be a {x.dtype} tensor of shape {tuple(x.shape)} on {x.device}, last dimension dense")
+    return _strides3(t)
+
+
+def _position_args(positions, B, N, dim, device):
+    """Positions' pointer, whether they are 64-bit, and the stride of a batch."""
+    ps = positions.shape
+    if positions.device != device or (positions.dtype is not torch.int32 and positions.dtype is not torch.int64):
+        raise ValueError(f"positions must be int32 or int64 on {device}")
+    if (ps != (N,) and ps != (B, N)) or (N > 1 and positions.stride(-1) != 1):
+        raise ValueError(f"positions must be a dense [{N}]" + (f" or [{B}, {N}]" if dim == 4 else ""))
+    return positions.data_ptr(), 1 if positions.dtype is torch.int64 else 0, positions.stride(0) if len(ps) == 2 else 0
+
+
 def _rope(x, positions, inv_freq, interleaved, mscale, out, stream, transposed):
     if torch is None:
         _load()
@@ -352,35 +417,16 @@ def _rope(x, positions, inv_freq, interleaved, mscale, out, stream, transposed):
         r = _fast.rope(x, positions, inv_freq, interleaved, mscale, transposed)
         if r is not None:
             return _answer(r, "fa2_rope")
-    dtype, device, shape, xs = x.dtype, x.device, x.shape, x.stride()
-    code = _codes.get(dtype)
-    dim = len(shape)
-    if code is None or not x.is_cuda or (dim != 4 and dim != 3) or xs[-1] != 1:
-        raise ValueError("x must be a bf16, fp16 or fp32 CUDA tensor [T, H, d] or [B, H, N, d], last dimension dense")
-    if dim == 3:     # [T, H, d]: one batch, tokens outside the heads
-        N, H, d = shape
-        B = 1
-    else:
-        B, H, N, d = shape
-    _sizes(*shape)
-    ps = positions.shape
-    if positions.device != device or (positions.dtype is not torch.int32 and positions.dtype is not torch.int64):
-        raise ValueError(f"positions must be int32 or int64 on {device}")
-    if (ps != (N,) and ps != (B, N)) or (N > 1 and positions.stride(-1) != 1):
-        raise ValueError(f"positions must be a dense [{N}]" + (f" or [{B}, {N}]" if dim == 4 else ""))
+    B, H, N, d, xs = _heads("x", x)
+    dtype, device, shape = x.dtype, x.device, x.shape
+    place = _position_args(positions, B, N, len(shape), device)
     freq, rotary_dim = _inv_freq_args(inv_freq, device, d)
     with _Call(device, stream) as handle:
         if out is None:
             out = torch.empty(shape, dtype=dtype, device=device)
-        ys = out.stride()
-        if out.dtype is not dtype or out.shape != shape or out.device != device or ys[-1] != 1:
-            raise ValueError(f"out must be a {dtype} tensor of shape {tuple(shape)} on {device}, last dimension dense")
-        # {batch, head, token}
-        xs, ys = (_LL3(xs[0], xs[1], xs[2]), _LL3(ys[0], ys[1], ys[2])) if dim == 4 else (
-            _LL3(0, xs[1], xs[0]), _LL3(0, ys[1], ys[0]))
-        rc = _lib.fa2_rope(x.data_ptr(), xs, out.data_ptr(), ys, B, H, N, d, positions.data_ptr(),
-                           1 if positions.dtype is torch.int64 else 0, positions.stride(0) if len(ps) == 2 else 0, freq,
-                           rotary_dim, 1 if interleaved else 0, mscale, transposed, code, handle)
+        ys = _like("out", out, x)
+        rc = _lib.fa2_rope(x.data_ptr(), xs, out.data_ptr(), ys, B, H, N, d, *place, freq, rotary_dim,
+                           1 if interleaved else 0, mscale, transposed, _codes[dtype], handle)
     if rc:
         _fail(rc, "fa2_rope")
     return out

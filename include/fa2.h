@@ -413,6 +413,57 @@ int fa2_append_paged(const fa2_paged_cache *cache, const void *K, const long lon
                      float mscale, fa2_stream_t stream);
 
 /*
+ * Each head's row normed and rotated in one pass.  The row x of d columns at
+ * position t becomes
+ *     y = R(t) (w x r),  r = 1 / sqrt(sum_c x_c^2 / d + eps),
+ * R(t) being the rotation of fa2_rope (mscale and columns beyond rotary_dim as
+ * there).  Sums are fp32 (of squares too: rows of elements beyond 1e18 overflow
+ * it), products are fp32 and rounded once.
+ *   X, Y       as fa2_rope, but d = 64, 128 or 256 and pairs without an alignment of their own
+ *   weight     [d] of the rows' type or fp32 (weight_dtype)
+ *   eps        finite, not negative
+ * Rows whose starts and strides are multiples of 16 bytes, with whole 16-byte
+ * vectors of rotated columns (rotary_dim a multiple of 16 elements of 16 bits, of
+ * 8 interleaved or in fp32, of 4 in fp32 interleaved), take the fast way.
+ */
+int fa2_norm_rope(const void *X, const long long *x_strides, void *Y, const long long *y_strides,
+                  int B, int H, int N, int d, const void *weight, int weight_dtype, float eps,
+                  const void *positions, int positions_int64, long long positions_batch_stride,
+                  const double *inv_freq, int rotary_dim, int interleaved, float mscale, int dtype,
+                  fa2_stream_t stream);
+
+/*
+ * Gradients of fa2_norm_rope for the upstream gradient dY.  With g = R(t)^T dY:
+ *     dX = r (w g - x r (sum_c w_c g_c x_c r) / d),   dweight = sum over all rows of g x r
+ *   dX         as Y; may be dY or X (the same strides)
+ *   dweight    fp32 [d]; zeros where there are no rows.  The same bits on every call on one kind of device.
+ *   workspace  256-byte aligned device memory of fa2_norm_rope_backward_workspace_bytes(d) bytes;
+ *              its contents do not matter.  Calls that may run at the same time need one each.
+ */
+int fa2_norm_rope_backward(const void *dY, const long long *dy_strides, const void *X,
+                           const long long *x_strides, void *dX, const long long *dx_strides, int B,
+                           int H, int N, int d, const void *weight, int weight_dtype, float eps,
+                           const void *positions, int positions_int64,
+                           long long positions_batch_stride, const double *inv_freq, int rotary_dim,
+                           int interleaved, float mscale, int dtype, float *dweight, void *workspace,
+                           size_t workspace_size, fa2_stream_t stream);
+
+/* Workspace of fa2_norm_rope_backward on the current device; 0 for another head dimension. */
+size_t fa2_norm_rope_backward_workspace_bytes(int d);
+
+/*
+ * fa2_append_paged with normed heads: rows of Q by q_weight and of K by k_weight
+ * ([d] each, of the cache's type or fp32; NULL: not normed), then rotated, as
+ * fa2_norm_rope does.  Values are copied.
+ */
+int fa2_append_paged_norm(const fa2_paged_cache *cache, const void *K, const long long *k_strides,
+                          const void *V, const long long *v_strides, const void *Q,
+                          const long long *q_strides, void *Q_out, const long long *q_out_strides,
+                          int Hq, const int *cu_q, int T, const void *q_weight, const void *k_weight,
+                          int weight_dtype, float eps, const double *inv_freq, int rotary_dim,
+                          int interleaved, float mscale, fa2_stream_t stream);
+
+/*
  * The tables that the page functions manage: page_table [B, table_width] (-1:
  * no page), lens [B] (tokens of each sequence) and refs [num_pages] (how many
  * table entries name the page; 0: free).  All int32 on the device; start with
