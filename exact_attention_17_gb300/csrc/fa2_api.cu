@@ -73,6 +73,8 @@ int device_ready() {
         fa2host::prepare_tc_d256_bf16() != cudaSuccess || fa2host::prepare_tc_d256_f16() != cudaSuccess ||
         fa2host::prepare_tc_pair_d128() != cudaSuccess || fa2host::prepare_simt() != cudaSuccess ||
         fa2host::prepare_bwd() != cudaSuccess || fa2host::prepare_bwd2() != cudaSuccess ||
+        fa2host::prepare_window_bf16() != cudaSuccess || fa2host::prepare_window_f16() != cudaSuccess ||
+        fa2host::prepare_bwd_window() != cudaSuccess ||
         fa2host::prepare_paged_bf16() != cudaSuccess || fa2host::prepare_paged_f16() != cudaSuccess)
       return;
     st.usable = true;
@@ -242,6 +244,14 @@ bool encode_tiled(CUtensorMap* map, bool f16, int rank, const void* base, const 
                          static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, st, b, estr,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_heads(CUtensorMap* map, const void* base, int d, int N, int Z, bool f16) {
+  return encode_map(map, base, d, N, Z, f16);
+}
+bool encode_heads_f32(CUtensorMap* map, const void* base, int d, int N, int Z) { return encode_map_f32(map, base, d, N, Z); }
+bool encode_heads_out(CUtensorMap* map, const void* base, int d, int N, long long Z, int elem_bytes, bool f16) {
+  return encode_map_out(map, base, d, N, Z, elem_bytes, f16);
 }
 
 // Multiplier and shift of fa2dev::fast_div for a divisor d >= 1.

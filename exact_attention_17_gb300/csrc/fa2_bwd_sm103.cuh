@@ -54,6 +54,13 @@ struct BwdParams {
   float scale_log2;     // scale * log2(e)
   int* status;
   unsigned long long timeout_ns;
+  // Window kernels (see the kernel): BH counts the key/value heads, each shared by `shared` query heads.
+  int window, sinks, shared;
+  int sink_blocks;              // key blocks that hold sinks
+  int parts, sink_parts;        // items of a key block without sinks, and of one with
+  int chunk, sink_chunk;        // most query tiles of an item
+  float* part;                  // dK, dV [128][D] each of the items of blocks cut into several
+  int grad_half;                // dK and dV in the input type instead of fp32
 };
 
 constexpr int kBwdThreads = 384;   // 8 elementwise warps, producer, MMA, 2 idle
@@ -96,8 +103,9 @@ struct alignas(8) BwdBarriers {
 // Pre-pass: one warp per query row.  D_i = dO_i . O_i, L2_i = LSE_i log2(e),
 // and the row of dQ set to zero.  Entries past Nq in each head's padded
 // arrays are set to zero.
-template <int D, bool F16>
-__global__ void __launch_bounds__(256) fa2_bwd_pre_kernel(const float* __restrict__ O,
+// O_HALF: O has the input type instead of fp32.
+template <int D, bool F16, bool O_HALF = false>
+__global__ void __launch_bounds__(256) fa2_bwd_pre_kernel(const void* __restrict__ O_any,
                                                           const uint16_t* __restrict__ dO,
                                                           const float* __restrict__ LSE,
                                                           float* __restrict__ dQ,
@@ -108,15 +116,16 @@ __global__ void __launch_bounds__(256) fa2_bwd_pre_kernel(const float* __restric
   const long long r = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   if (r >= rows) return;
-  const float* o = O + r * D + lane * E;
   const uint16_t* g = dO + r * D + lane * E;
+  auto wide = [](uint32_t bits) {
+    return F16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(bits))) : __uint_as_float(bits << 16);
+  };
   float acc = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const uint32_t bits = g[e];
-    const float gv = F16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(bits)))
-                         : __uint_as_float(bits << 16);
-    acc = fmaf(gv, o[e], acc);
+    const float ov = O_HALF ? wide(static_cast<const uint16_t*>(O_any)[r * D + lane * E + e])
+                            : static_cast<const float*>(O_any)[r * D + lane * E + e];
+    acc = fmaf(wide(g[e]), ov, acc);
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
@@ -138,7 +147,15 @@ __global__ void __launch_bounds__(256) fa2_bwd_pre_kernel(const float* __restric
   }
 }
 
-template <int D, bool CAUSAL, bool F16>
+// WINDOW (with CAUSAL): query i sees the keys j <= i with i - j < window or j <
+// sinks, and `shared` query heads read one key/value head.  A key block's query
+// tiles are those of its window, for a block with sinks all that follow it, once
+// for every query head of the group: dK and dV of the group add up in TMEM.  The
+// tiles are cut into items of at most `chunk` (`sink_chunk`); the items of a block that has several
+// leave their dK and dV in the workspace, and the kernel behind this one adds them
+// up in order.  Scores outside the mask are zeroed from one word of bits for
+// every 32 queries of a key, only in tiles that the mask cuts.
+template <int D, bool CAUSAL, bool F16, bool WINDOW = false>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     fa2_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k,
@@ -170,18 +187,58 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // Work item: (key block jb, b*H + h), grouped like the forward kernel;
   // under the causal mask the first key blocks see the most query tiles and
   // run first.
-  const int U = p.key_blocks;
-  const int per_group = p.item_group * U;
-  const int group = blockIdx.x / per_group;
-  const int in_group = blockIdx.x - group * per_group;
-  const int g0 = group * p.item_group;
-  const int g_items = min(p.item_group, p.BH - g0);
-  const int jb = in_group / g_items;
-  const int bh = g0 + (in_group - jb * g_items);
+  int jb, bh;                  // key block, b*H + h (of the keys)
+  int i0, n_tiles;             // first query tile, tiles of this item
+  int head0 = 0, row_tiles = 0, first = 0;   // WINDOW: first query head, tiles of a head, this item's first tile
+  int slot = -1;               // WINDOW: workspace slot, -1: the block's only item
   const int q_tiles = (p.Nq + 127) / 128;
-  const int i0 = CAUSAL ? jb : 0;               // first query tile with a query >= the first key
-  const int n_tiles = max(0, q_tiles - i0);
+  if constexpr (WINDOW) {
+    // blocks with sinks first (the longest lists); heads innermost but for a block's items
+    const int sink_items = p.BH * p.sink_blocks * p.sink_parts;
+    const bool with_sinks = static_cast<int>(blockIdx.x) < sink_items;
+    const int x = blockIdx.x - (with_sinks ? 0 : sink_items), n_parts = with_sinks ? p.sink_parts : p.parts;
+    const int part = x % n_parts, y = x / n_parts;
+    jb = y / p.BH;
+    bh = y - jb * p.BH;
+    if (!with_sinks) jb += p.sink_blocks;
+    i0 = min(jb, q_tiles);
+    const long long last = min(jb * 128 + 127, p.Nk - 1) + static_cast<long long>(p.window) - 1;   // query
+    const int end = with_sinks ? q_tiles : static_cast<int>(min(static_cast<long long>(q_tiles), last / 128 + 1));
+    row_tiles = max(0, end - i0);
+    const int chunk = with_sinks ? p.sink_chunk : p.chunk;
+    first = part * chunk;
+    n_tiles = max(0, min(chunk, row_tiles * p.shared - first));
+    head0 = bh * p.shared;
+    if (n_parts > 1) slot = blockIdx.x;
+  } else {
+    const int U = p.key_blocks;
+    const int per_group = p.item_group * U;
+    const int group = blockIdx.x / per_group;
+    const int in_group = blockIdx.x - group * per_group;
+    const int g0 = group * p.item_group;
+    const int g_items = min(p.item_group, p.BH - g0);
+    jb = in_group / g_items;
+    bh = g0 + (in_group - jb * g_items);
+    i0 = CAUSAL ? jb : 0;               // first query tile with a query >= the first key
+    n_tiles = max(0, q_tiles - i0);
+  }
   const int key0 = jb * 128;
+  // query tile and head of this item's tile t, for t = 0, 1, ...
+  struct Place {
+    int i, head;
+  };
+  auto place0 = [&]() {
+    if (!WINDOW) return Place{i0, bh};
+    const int g = row_tiles > 0 ? first / row_tiles : 0;
+    return Place{i0 + first - g * row_tiles, head0 + g};
+  };
+  auto advance = [&](Place& at) {
+    ++at.i;
+    if (WINDOW && at.i == i0 + row_tiles) {
+      at.i = i0;
+      ++at.head;
+    }
+  };
 
   if (threadIdx.x == 0) {
     bar_init(&bars->kv_full, 1);
@@ -224,7 +281,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           tma_load_3d(sV + c * kChunkBytes, &tm_v, &bars->kv_full, c * 64, key0, bh);
         }
         bool ok = true;
-        for (int t = 0; t < n_tiles && ok; ++t) {
+        Place at = place0();
+        for (int t = 0; t < n_tiles && ok; ++t, advance(at)) {
           const int slot = t % STAGES;
           const int lap = t / STAGES;   // laps of the ring completed
           if (lap > 0 && !wait_bar(&bars->q_empty[slot], (lap - 1) & 1, abort, p.timeout_ns)) {
@@ -233,10 +291,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             break;
           }
           bar_arrive_expect_tx(&bars->q_full[slot], 2 * TILE);
-          const int row = (i0 + t) * 128;
+          const int row = at.i * 128;
           for (int c = 0; c < NCH; ++c) {
-            tma_load_3d(sQ + slot * TILE + c * kChunkBytes, &tm_q, &bars->q_full[slot], c * 64, row, bh);
-            tma_load_3d(sdO + slot * TILE + c * kChunkBytes, &tm_do, &bars->q_full[slot], c * 64, row, bh);
+            tma_load_3d(sQ + slot * TILE + c * kChunkBytes, &tm_q, &bars->q_full[slot], c * 64, row, at.head);
+            tma_load_3d(sdO + slot * TILE + c * kChunkBytes, &tm_do, &bars->q_full[slot], c * 64, row, at.head);
           }
         }
         // every copy this CTA started must land before it exits
@@ -324,14 +382,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int key = key0 + row;
     const uint32_t lane_bits = static_cast<uint32_t>(wq * 32) << 16;
     const float sl2 = p.scale_log2;
-    const float* L2h = p.L2 + static_cast<size_t>(bh) * p.Nq_pad;
-    const float* Drh = p.Dr + static_cast<size_t>(bh) * p.Nq_pad;
     const uint32_t ds_base = smem_addr(sdS) + wg * kChunkBytes + row * 128;
     bool ok = true;
     const bool leader = (threadIdx.x & 127) == 0;
-    for (int t = 0; t < n_tiles; ++t) {
+    Place at = place0();
+    for (int t = 0; t < n_tiles; ++t, advance(at)) {
+      const float* L2h = p.L2 + static_cast<size_t>(at.head) * p.Nq_pad;
+      const float* Drh = p.Dr + static_cast<size_t>(at.head) * p.Nq_pad;
       const int slot = t % STAGES;
-      const int qbase = (i0 + t) * 128;
+      const int qbase = at.i * 128;
       const int qcol0 = qbase + 64 * wg;      // first query of this warpgroup's columns
       // this tile's LSE log2(e) for the warpgroup's columns, fetched while S^T is computed
       float4 l4v[16];
@@ -345,6 +404,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // P^T = exp2(s * scale log2e - LSE log2e) on kept (key, query) pairs
       float P[64];
       uint32_t pk[32];
+      // WINDOW: every (key, query) pair of the tile is seen
+      const bool whole = WINDOW && qbase >= key0 + 127 && qbase + 128 <= p.Nq && key0 + 128 <= p.Nk &&
+                         (qbase + 127 < key0 + p.window || key0 + 128 <= p.sinks);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t s[32];
@@ -358,9 +420,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           for (int u = 0; u < 4; ++u) {
             const int e = 4 * e4 + u;
             const int q = qcol0 + 32 * h + e;
-            const bool keep = q < p.Nq && key < p.Nk && (!CAUSAL || key <= q);
+            const bool keep = WINDOW || (q < p.Nq && key < p.Nk && (!CAUSAL || key <= q));
             P[32 * h + e] = keep ? ex2_approx(fmaf(__uint_as_float(s[e]), sl2, -lv[u])) : 0.f;
           }
+        }
+        if (WINDOW && !whole) {
+          // this key's queries: from its own on, as far as its window or, for a sink, to the end
+          const int at_q = qcol0 + 32 * h;
+          const int end = key >= p.Nk ? 0 : key < p.sinks ? p.Nq : static_cast<int>(min(static_cast<long long>(p.Nq),
+                                                                        static_cast<long long>(key) + p.window));
+          const uint32_t keep = low_bits(end - at_q) & ~low_bits(key - at_q);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!(keep >> e & 1u)) P[32 * h + e] = 0.f;
         }
       }
 #pragma unroll
@@ -448,7 +520,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         } else {
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
-            tma_reduce_add_3d(&tm_dq, stage + c * 16384, (D / 2) * wg + 32 * c, qbase, bh);
+            tma_reduce_add_3d(&tm_dq, stage + c * 16384, (D / 2) * wg + 32 * c, qbase, at.head);
           bulk_commit();
         }
       }
@@ -465,8 +537,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // are warp-collective, so every lane runs them and only the stores are
     // limited to keys < Nk.
     if (ok) {
-      float* dk = p.dK + (static_cast<size_t>(bh) * p.Nk + key) * D;
-      float* dv = p.dV + (static_cast<size_t>(bh) * p.Nk + key) * D;
+      const bool partial = WINDOW && slot >= 0;
+      const size_t out = (static_cast<size_t>(bh) * p.Nk + key) * D;
+      float* dk = partial ? p.part + (static_cast<size_t>(slot) * 256 + row) * D : p.dK + out;
+      float* dv = partial ? dk + 128 * D : p.dV + out;
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
         const int col = (D / 2) * wg + 32 * c;
@@ -481,6 +555,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           for (int e = 0; e < 32; ++e) a[e] = b[e] = 0u;
         }
         if (key >= p.Nk) continue;
+        if (WINDOW && p.grad_half && !partial) {
+          uint32_t* hk = reinterpret_cast<uint32_t*>(p.dK) + (out + col) / 2;
+          uint32_t* hv = reinterpret_cast<uint32_t*>(p.dV) + (out + col) / 2;
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t x[4], y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x[i] = pack_x2<F16>(__uint_as_float(a[e + 2 * i]) * p.scale, __uint_as_float(a[e + 2 * i + 1]) * p.scale);
+              y[i] = pack_x2<F16>(__uint_as_float(b[e + 2 * i]), __uint_as_float(b[e + 2 * i + 1]));
+            }
+            *reinterpret_cast<uint4*>(hk + e / 2) = make_uint4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<uint4*>(hv + e / 2) = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+          continue;
+        }
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
           *reinterpret_cast<float4*>(dk + col + e) =

@@ -1,0 +1,109 @@
+// Backward kernels of windows (head dimensions 64 and 128, bf16 or fp16), and the
+// kernel behind them.
+#include "fa2_launch.h"
+
+namespace fa2dev {
+
+// dQ from fp32 to the input type (blocks from `key_blocks_from` on: see the launch), and
+// sums of the items of the key blocks that were cut: key row, four columns a thread.
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) fa2_bwd_window_end_kernel(const __grid_constant__ BwdParams p,
+                                                                 uint2* __restrict__ dq_out, long long q_quads,
+                                                                 int dq_blocks, long long sum_quads) {
+  if (static_cast<int>(blockIdx.x) < dq_blocks) {
+    const float4* in = reinterpret_cast<const float4*>(p.dQ);
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < q_quads; i += dq_blocks * 256ll) {
+      const float4 x = in[i];
+      dq_out[i] = make_uint2(pack_x2<F16>(x.x, x.y), pack_x2<F16>(x.z, x.w));
+    }
+    return;
+  }
+  const long long at = (static_cast<long long>(blockIdx.x) - dq_blocks) * 256 + threadIdx.x;
+  if (at >= sum_quads) return;
+  constexpr int kQuads = D / 4;
+  const int c = static_cast<int>(at % kQuads);
+  const long long row = at / kQuads;                  // (block, head, key of the block)
+  const int y = static_cast<int>(row >> 7), key_row = static_cast<int>(row & 127);
+  const int jb = y / p.BH, bh = y - jb * p.BH, key = jb * 128 + key_row;
+  if (key >= p.Nk) return;
+  const bool with_sinks = jb < p.sink_blocks;
+  const int n = with_sinks ? p.sink_parts : p.parts;
+  if (n == 1) return;
+  const long long slot = with_sinks ? static_cast<long long>(y) * n
+                                    : static_cast<long long>(p.BH) * p.sink_blocks * p.sink_parts +
+                                          (y - static_cast<long long>(p.BH) * p.sink_blocks) * n;
+  const float* from = p.part + (slot * 256 + key_row) * D + c * 4;
+  float4 dk = make_float4(0.f, 0.f, 0.f, 0.f), dv = dk;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float4 a = *reinterpret_cast<const float4*>(from + static_cast<long long>(i) * 256 * D);
+    const float4 b = *reinterpret_cast<const float4*>(from + static_cast<long long>(i) * 256 * D + 128 * D);
+    dk.x += a.x; dk.y += a.y; dk.z += a.z; dk.w += a.w;
+    dv.x += b.x; dv.y += b.y; dv.z += b.z; dv.w += b.w;
+  }
+  const long long out = (static_cast<long long>(bh) * p.Nk + key) * kQuads + c;
+  if (p.grad_half) {
+    reinterpret_cast<uint2*>(p.dK)[out] = make_uint2(pack_x2<F16>(dk.x, dk.y), pack_x2<F16>(dk.z, dk.w));
+    reinterpret_cast<uint2*>(p.dV)[out] = make_uint2(pack_x2<F16>(dv.x, dv.y), pack_x2<F16>(dv.z, dv.w));
+  } else {
+    reinterpret_cast<float4*>(p.dK)[out] = dk;
+    reinterpret_cast<float4*>(p.dV)[out] = dv;
+  }
+}
+
+}  // namespace fa2dev
+
+namespace fa2host {
+
+namespace {
+template <int D, bool F16>
+cudaError_t set_limits() {
+  return cudaFuncSetAttribute(fa2dev::fa2_bwd_tc_kernel<D, true, F16, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              fa2dev::BwdConfig<D>::kSmemBytes);
+}
+
+template <int D, bool F16>
+cudaError_t run(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo,
+                const CUtensorMap& mdq, const fa2dev::BwdParams& p, unsigned grid, cudaStream_t s) {
+  fa2dev::fa2_bwd_tc_kernel<D, true, F16, true>
+      <<<grid, fa2dev::kBwdThreads, fa2dev::BwdConfig<D>::kSmemBytes, s>>>(mq, mk, mv, mdo, mdq, p);
+  return cudaGetLastError();
+}
+
+template <int D, bool F16>
+cudaError_t run_end(const fa2dev::BwdParams& p, void* dq_out, long long q_elems, cudaStream_t s) {
+  const long long quads = dq_out ? q_elems / 4 : 0;
+  const int dq_blocks = static_cast<int>(quads > 0 ? (quads + 2047) / 2048 < 4096 ? (quads + 2047) / 2048 : 4096 : 0);
+  const int cut_blocks = p.parts > 1 ? p.key_blocks : p.sink_parts > 1 ? p.sink_blocks : 0;
+  const long long sum_quads = static_cast<long long>(cut_blocks) * p.BH * 128 * (D / 4);
+  const long long sum_blocks = (sum_quads + 255) / 256;
+  if (dq_blocks + sum_blocks == 0) return cudaSuccess;
+  if (dq_blocks + sum_blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  fa2dev::fa2_bwd_window_end_kernel<D, F16><<<static_cast<unsigned>(dq_blocks + sum_blocks), 256, 0, s>>>(
+      p, static_cast<uint2*>(dq_out), quads, dq_blocks, sum_quads);
+  return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t prepare_bwd_window() {
+  cudaError_t e;
+  if ((e = set_limits<64, false>()) != cudaSuccess || (e = set_limits<64, true>()) != cudaSuccess ||
+      (e = set_limits<128, false>()) != cudaSuccess)
+    return e;
+  return set_limits<128, true>();
+}
+
+cudaError_t launch_bwd_window(int d, bool f16, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                              const CUtensorMap& mdo, const CUtensorMap& mdq, const fa2dev::BwdParams& p, unsigned grid,
+                              cudaStream_t s) {
+  const auto f = d == 64 ? (f16 ? run<64, true> : run<64, false>) : f16 ? run<128, true> : run<128, false>;
+  return f(mq, mk, mv, mdo, mdq, p, grid, s);
+}
+
+cudaError_t launch_bwd_window_end(int d, bool f16, const fa2dev::BwdParams& p, void* dq_out, long long q_elems,
+                                  cudaStream_t s) {
+  const auto f = d == 64 ? (f16 ? run_end<64, true> : run_end<64, false>) : f16 ? run_end<128, true> : run_end<128, false>;
+  return f(p, dq_out, q_elems, s);
+}
+
+}  // namespace fa2host

@@ -99,6 +99,11 @@ struct FwdParams {
   FastDiv div_per_group;  // by item_group * q_blocks
   FastDiv div_group;      // by item_group
   FastDiv div_splits;     // by num_splits
+  // Window kernels: query i sees the keys j <= i with i - j < window or j < sinks; `shared` query heads of BH read
+  // one key/value head.
+  int window;
+  int sinks;
+  FastDiv div_shared;
 };
 
 constexpr int kRowsPerSub = 128;   // tcgen05 M
@@ -259,8 +264,31 @@ __device__ __forceinline__ int kv_tiles_for(int u, int sub, int Nq, int t_begin,
   return max(0, stop - t_begin);
 }
 
+// Key tiles of a window kernel's CTA, whose first query is q_row0: the tiles that hold sinks, then those from the
+// first key of that query's window on.  Tile v of this list is tile v (v < sink_tiles) or v + skip of the keys.
+struct WindowTiles {
+  int sink_tiles, skip;
+  __device__ __forceinline__ int tile(int v) const { return v < sink_tiles ? v : v + skip; }
+};
+
+__device__ __forceinline__ WindowTiles window_tiles(int q_row0, int window, int sinks, int all_tiles) {
+  WindowTiles w;
+  const int lo = min(max(0, q_row0 - window + 1) / kKeysPerTile, all_tiles);
+  w.sink_tiles = min((sinks + kKeysPerTile - 1) / kKeysPerTile, lo);
+  w.skip = lo - w.sink_tiles;
+  return w;
+}
+
+// Bits 0 .. n-1, n cut to 0 .. 32.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
 // F16: Q, K, V (and P) are fp16 instead of bf16.  SUBS: query sub-tiles per CTA.
-template <int D, bool CAUSAL, bool F16, int SUBS>
+//
+// WINDOW (with CAUSAL): a query sees the last `window` keys up to its own and the first `sinks`.  Both sub-tiles
+// stream the tiles of the first one's list and what the second needs behind it; scores outside a row's keys
+// are masked from one word of bits for every 32 keys.  Every sub-tile with rows visits a tile, so that rows without
+// a key (far behind the last one) get their O = 0 and LSE = -inf on the ordinary way.
+template <int D, bool CAUSAL, bool F16, int SUBS, bool WINDOW = false>
 __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCtasPerSm)
     fa2_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k,
@@ -309,10 +337,19 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
   const int all_tiles = (p.Nk + kKeysPerTile - 1) / kKeysPerTile;
   const int t_begin = split * p.tiles_per_split;
   const int t_end = min(all_tiles, t_begin + p.tiles_per_split);
-  const int n0 = kv_tiles_for<CAUSAL, SUBS>(u, 0, p.Nq, t_begin, t_end);
-  const int n1 = SUBS == 2 ? kv_tiles_for<CAUSAL, SUBS>(u, 1, p.Nq, t_begin, t_end) : 0;
-  const int nmax = max(n0, n1);
   const int q_row0 = u * SUBS * kRowsPerSub;
+  int n0 = kv_tiles_for<CAUSAL, SUBS>(u, 0, p.Nq, t_begin, t_end);
+  int n1 = SUBS == 2 ? kv_tiles_for<CAUSAL, SUBS>(u, 1, p.Nq, t_begin, t_end) : 0;
+  WindowTiles wt = {0, 0};
+  if constexpr (WINDOW) {
+    wt = window_tiles(q_row0, p.window, p.sinks, all_tiles);
+    n0 = max(1, n0 - wt.skip);   // (the first sub-tile always has rows)
+    n1 = SUBS == 2 && q_row0 + kRowsPerSub < p.Nq ? max(1, n1 - wt.skip) : 0;
+  }
+  const int kv_head = WINDOW ? fast_div(bh, p.div_shared) : bh;
+  const int nmax = max(n0, n1);
+  // first row of tile j of this CTA
+  auto key_row = [&](int j) { return (WINDOW ? wt.tile(j) : t_begin + j) * kKeysPerTile; };
 
   // The producer thread sets up the barriers and starts the first loads (Q
   // and the first ring slots) before the CTA-wide synchronisation, so that
@@ -352,7 +389,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
       const CUtensorMap* map = (g & 1) == 0 ? &tm_k : &tm_v;
       for (int c = 0; c < NCH; ++c)
         tma_load_3d(sKV + g * TILE + c * kChunkBytes, map, &bars->kv_full[g], c * 64,
-                    (t_begin + g / 2) * kKeysPerTile, bh);
+                    key_row(g / 2), kv_head);
     }
     // The CTA one wave later (probably the next to run on some SM) reads a Q
     // block nobody has touched yet: start bringing it into L2 now.
@@ -404,7 +441,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
             const CUtensorMap* map = kind == 0 ? &tm_k : &tm_v;
             for (int c = 0; c < NCH; ++c)
               tma_load_3d(sKV + slot * TILE + c * kChunkBytes, map, &bars->kv_full[slot], c * 64,
-                          (t_begin + j) * kKeysPerTile, bh);
+                          key_row(j), kv_head);
             ++issued;
           }
         }
@@ -679,8 +716,10 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
       // S of this tile, with the masks for keys past the end and keys after
       // the query under the causal mask
       uint32_t s[4][32];
-      const int key0 = (t_begin + j) * kKeysPerTile;
+      const int key0 = key_row(j);
       const bool tail = key0 + kKeysPerTile > p.Nk;
+      // some row's window begins behind the tile's first key, and not all its keys are sinks
+      const bool low = WINDOW && key0 < sub_row0 + kRowsPerSub - p.window && key0 + kKeysPerTile > p.sinks;
       const bool diag = CAUSAL && key0 + kKeysPerTile - 1 > sub_row0;
       auto load_s = [&]() {
 #pragma unroll
@@ -690,7 +729,19 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
         tmem_ld_wait(s[0]);
 #pragma unroll
         for (int c = 1; c < 4; ++c) regs_after_wait(s[c]);
-        if (tail || diag) {
+        if constexpr (WINDOW) {
+          if (tail || diag || low) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int at = key0 + c * 32;
+              const uint32_t keep = low_bits(min(p.Nk, qi + 1) - at) &
+                                    (~low_bits(qi - p.window + 1 - at) | low_bits(p.sinks - at));
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(keep >> e & 1u)) s[c][e] = __float_as_uint(-INFINITY);
+            }
+          }
+        } else if (tail || diag) {
           const int lim = CAUSAL ? min(p.Nk, qi + 1) : p.Nk;  // keys [0, lim) are kept
 #pragma unroll
           for (int c = 0; c < 4; ++c)
@@ -835,7 +886,8 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
     }
     if (n_tiles > 0 && ok) {
       // l == 0 only for a row whose every key in this range is masked
-      if (store) *lse_out = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+      const bool none = WINDOW ? l == 0.f : !(l > 0.f);
+      if (store) *lse_out = none ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
       if (!__all_sync(0xffffffffu,
                       wait_bar(&bars->o_done[sub], Cfg::kOutDoneLast ? 0u : (n_tiles - 1) & 1, abort,
                                p.timeout_ns))) {
@@ -852,7 +904,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
         // free once every MMA has completed (no load is in flight by then),
         // so that both halves are staged without waiting for the first
         // stores; otherwise it reuses the Q buffer once those have read it.
-        const float inv_l = l > 0.f ? 1.f / l : 0.f;
+        const float inv_l = none ? 0.f : 1.f / l;
         const bool use_ring = n_tiles == nmax;
         const int zrow = (p.num_splits > 1 ? split * p.BH : 0) + bh;
         const bool leader = (threadIdx.x & (kRowsPerSub - 1)) == 0;
@@ -875,6 +927,10 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
               uint32_t o[32];
               tmem_ld32(tO + r * (D / 2) + 32 * b, o);
               tmem_ld_wait(o);
+              if (WINDOW && none) {   // a row without keys: 0, whatever V holds
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = 0u;
+              }
 #pragma unroll
               for (int u = 0; u < 8; ++u)
                 st_shared_v4(box + ((u ^ (row & 7)) << 4), __float_as_uint(__uint_as_float(o[4 * u]) * inv_l),
@@ -887,6 +943,10 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
               tmem_ld32(tO + 64 * b + 32, o[1]);
               tmem_ld_wait(o[0]);
               tmem_ld_wait(o[1]);
+              if (WINDOW && none) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[0][e] = o[1][e] = 0u;
+              }
               uint32_t h[32];
 #pragma unroll
               for (int e = 0; e < 32; ++e)

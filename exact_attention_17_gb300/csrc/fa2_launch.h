@@ -81,8 +81,10 @@ cudaError_t launch_bwd(int d, bool causal, bool f16, const CUtensorMap& mq, cons
                        const CUtensorMap& mv, const CUtensorMap& mdo, const CUtensorMap& mdq,
                        const fa2dev::BwdParams& p, unsigned grid, cudaStream_t s);
 // D_i = dO_i . O_i and LSE_i log2(e) into [BH][Nq_pad] arrays; dQ rows zeroed.
-cudaError_t launch_bwd_pre(int d, bool f16, const float* O, const void* dO, const float* LSE, float* dQ,
-                           float* L2, float* Dr, long long rows, int Nq, int Nq_pad, cudaStream_t s);
+// o_half: O has the input type (else fp32).
+cudaError_t launch_bwd_pre(int d, bool f16, const void* O, const void* dO, const float* LSE, float* dQ,
+                           float* L2, float* Dr, long long rows, int Nq, int Nq_pad, cudaStream_t s,
+                           bool o_half = false);
 cudaError_t launch_zero(float* p, long long n, cudaStream_t s);
 
 // Two-tile backward kernel (fa2_bwd2.cu), head dimension 128.  mq64, mdo64:
@@ -91,6 +93,22 @@ cudaError_t prepare_bwd2();
 cudaError_t launch_bwd2(bool causal, bool f16, const CUtensorMap& mq64, const CUtensorMap& mk,
                         const CUtensorMap& mv, const CUtensorMap& mdo64, const CUtensorMap& mdq32,
                         const fa2dev::BwdParams& p, unsigned grid, cudaStream_t s);
+
+// Windows (fa2_window_bf16.cu, fa2_window_f16.cu, fa2_bwd_window.cu).
+cudaError_t prepare_window_bf16();
+cudaError_t prepare_window_f16();
+cudaError_t launch_window_bf16(int d, int subs, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                               const CUtensorMap& mo, const fa2dev::FwdParams& p, unsigned grid, cudaStream_t s);
+cudaError_t launch_window_f16(int d, int subs, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                              const CUtensorMap& mo, const fa2dev::FwdParams& p, unsigned grid, cudaStream_t s);
+cudaError_t prepare_bwd_window();
+cudaError_t launch_bwd_window(int d, bool f16, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                              const CUtensorMap& mdo, const CUtensorMap& mdq, const fa2dev::BwdParams& p, unsigned grid,
+                              cudaStream_t s);
+// Behind it: dK and dV of key blocks cut into several items, and dQ (fp32, q_elems) into the 16-bit dq_out
+// unless that is null.
+cudaError_t launch_bwd_window_end(int d, bool f16, const fa2dev::BwdParams& p, void* dq_out, long long q_elems,
+                                  cudaStream_t s);
 
 // Attention over a paged cache (fa2_paged_bf16.cu, fa2_paged_f16.cu): the
 // partial or final results, then the merge of items cut into key ranges

@@ -295,6 +295,45 @@ int fa2_backward_typed(const void *Q, const void *K, const void *V, const float 
                        size_t workspace_size, fa2_stream_t stream);
 
 /*
+ * Causal attention with a window: query i sees the keys j <= i with i - j <
+ * window or j < sinks (its last `window` keys, its own among them, and the first
+ * `sinks` of all; key and query 0 are the same position, as under fa2_forward's causal
+ * mask).  Query heads share key/value heads in groups of H / Hkv: head h reads head
+ * h / (H / Hkv).
+ *   Q, O       [B, H, Nq, d], K, V [B, Hkv, Nk, d], LSE [B, H, Nq], all dense
+ *   window     at least 1; sinks at least 0 (either may exceed the lengths)
+ * Types, alignment and limits as fa2_forward_typed.  A row without keys (i - window
+ * >= Nk - 1, no sinks) gets O = 0 and LSE = -inf.  Only the 128-key tiles that some row of a
+ * block of queries sees are read; within them a key that a row does not see has
+ * weight 0 (which times a V that is not finite is NaN).
+ */
+int fa2_forward_window(const void *Q, const void *K, const void *V, void *O, float *LSE, int B,
+                       int H, int Hkv, int Nq, int Nk, int d, int window, int sinks, float scale,
+                       int qkv_dtype, int o_dtype, fa2_stream_t stream);
+
+/*
+ * Gradients of fa2_forward_window: the formulas of fa2_backward over the keys that
+ * are seen, dK and dV summed over the query heads that share them.
+ *   O          fp32 or the type of Q (o_dtype); LSE fp32, both as fa2_forward_window returned them
+ *   dO         of Q's type
+ *   dQ, dK, dV fp32 or Q's type (grad_dtype), sums in fp32 either way
+ *   workspace  256-byte aligned device memory of fa2_backward_window_workspace_bytes bytes; its
+ *              contents do not matter.  Calls that may run at the same time need one each.
+ *   d          64 or 128
+ * dK and dV have the same bits on every call; dQ is added up in fp32 from blocks of
+ * keys in the order in which they finish, as in fa2_backward.
+ */
+int fa2_backward_window(const void *Q, const void *K, const void *V, const void *O, const void *dO,
+                        const float *LSE, void *dQ, void *dK, void *dV, int B, int H, int Hkv,
+                        int Nq, int Nk, int d, int window, int sinks, float scale, int qkv_dtype,
+                        int o_dtype, int grad_dtype, void *workspace, size_t workspace_size,
+                        fa2_stream_t stream);
+
+/* Workspace of fa2_backward_window on the current device; 0 for invalid arguments or no queries. */
+size_t fa2_backward_window_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, int window,
+                                           int sinks, int grad_dtype);
+
+/*
  * ---------------------------------------------------------------------------
  * A paged key/value cache: rotary positions, writing new tokens, attention of
  * new tokens over the cache, and the pages' management.
