@@ -54,6 +54,9 @@ SIGNATURES = {
     "fa2_backward_window_workspace_bytes": (_Z, [_I] * 9),
     "fa2_forward_paged": (_I, [_P, _P, _LL, _LL, _P, _P, _P, _I, _I, _I, _F, _I, _P, _Z, _P]),
     "fa2_forward_paged_workspace_bytes": (_Z, [_I] * 6),
+    "fa2_forward_paged_window": (_I, [_P, _P, _LL, _LL, _P, _P, _P, _I, _I, _I, _I, _F, _I, _P, _Z, _P]),
+    "fa2_forward_paged_prefix": (_I, [_P, _P, _LL, _LL, _P, _P, _P, _I, _I, _P, _P, _I, _I, _F, _I, _P, _Z, _P]),
+    "fa2_forward_paged_prefix_workspace_bytes": (_Z, [_I] * 7),
     "fa2_rope": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _LL, _P, _I, _I, _F, _I, _I, _P]),
     "fa2_append_paged": (_I, [_P] * 9 + [_I, _P, _I, _P, _I, _I, _F, _P]),
     "fa2_norm_rope": (_I, [_P] * 4 + [_I] * 4 + [_P, _I, _F, _P, _I, _LL, _P, _I, _I, _F, _I, _P]),
@@ -445,6 +448,6 @@ def backward(q, k, v, o, lse, do, causal: bool = False, scale: float | None = No
 
 
 from .norm import norm_rope, norm_rope_backward  # noqa: E402
-from .paged import (append_paged, forward_paged, pages_compact, pages_copy, pages_fork, pages_free,  # noqa: E402
+from .paged import (append_paged, forward_paged, forward_paged_prefix, forward_paged_window, pages_compact, pages_copy, pages_fork, pages_free,  # noqa: E402
                     pages_reserve, rope, rope_backward, rope_inv_freq)
 from .window import backward_window, forward_window  # noqa: E402

@@ -33,7 +33,7 @@ SOURCES = ["fa2_api.cu", "fa2_tc_d64_bf16.cu", "fa2_tc_d128_bf16.cu", "fa2_tc_d2
            "fa2_combine.cu", "fa2_bwd.cu", "fa2_tc_pair_d128.cu", "fa2_bwd2.cu",
            "fa2_paged_api.cu", "fa2_paged_bf16.cu", "fa2_paged_f16.cu", "fa2_rope.cu", "fa2_pages.cu",
            "fa2_norm_api.cu", "fa2_norm.cu", "fa2_window_api.cu", "fa2_window_bf16.cu", "fa2_window_f16.cu",
-           "fa2_bwd_window.cu"]
+           "fa2_bwd_window.cu", "fa2_paged_ext_bf16.cu", "fa2_paged_ext_f16.cu", "fa2_paged_prefix.cu"]
 
 
 def nvcc() -> str:

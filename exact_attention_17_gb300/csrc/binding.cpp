@@ -42,6 +42,12 @@ decltype(&fa2_append_paged_norm) append_norm_fn;
 decltype(&fa2_norm_rope) norm_fn;
 decltype(&fa2_norm_rope_backward) norm_backward_fn;
 decltype(&fa2_norm_rope_backward_workspace_bytes) norm_workspace_fn;
+decltype(&fa2_forward_paged_window) paged_window_fn;
+decltype(&fa2_forward_paged_prefix) paged_prefix_fn;
+decltype(&fa2_forward_paged_prefix_workspace_bytes) prefix_workspace_fn;
+decltype(&fa2_forward_window) window_fn;
+decltype(&fa2_backward_window) window_backward_fn;
+decltype(&fa2_backward_window_workspace_bytes) window_workspace_fn;
 
 const at::Tensor* tensor(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
 
@@ -183,33 +189,191 @@ bool weights(PyObject* o, int64_t d, at::ScalarType type, at::Device device, con
   return true;
 }
 
+// The queries of an attention call over a cache: (q, k_pages, v_pages, page_table, kv_lens, cu_q, ...).
+struct Queries {
+  fa2_paged_cache c;
+  at::Device device = at::Device(at::kCPU);
+  const at::Tensor* q;
+  int T, Hq;
+  const int* cu;
+};
+
+bool queries_of(PyObject* const* a, Queries* x) {
+  x->q = tensor(a[0]);
+  if (!x->q || x->q->dim() != 3 || !cache_of(a + 1, &x->c, &x->device)) return false;
+  const int64_t T = x->q->size(0), Hq = x->q->size(1);
+  if (!rows(x->q, T, Hq, x->c.d, x->c.dtype == FA2_DTYPE_BF16 ? at::kBFloat16 : at::kHalf, x->device) ||
+      Hq % x->c.kv_heads != 0 || !offsets_of(a[5], x->c.B, T, x->device, &x->cu))
+    return false;
+  x->T = static_cast<int>(T);
+  x->Hq = static_cast<int>(Hq);
+  return true;
+}
+
+// 1/sqrt(d) rounded to fp32 for None; sets a Python error where it is no number.
+double scale_of(PyObject* o, int64_t d) {
+  return o == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(d))) : PyFloat_AsDouble(o);
+}
+
+// Outputs and workspace, and the call: f(O, LSE, workspace, its size, stream)
+template <typename F>
+PyObject* attend(const Queries& x, size_t size, F f) {
+  at::Tensor o = make(x.q->sizes(), x.q->scalar_type(), x.device), lse = make({x.T, x.Hq}, at::kFloat, x.device);
+  at::Tensor ws = make({static_cast<int64_t>(size > 0 ? size : 1)}, at::kByte, x.device);
+  const fa2_stream_t s = stream_of(x.device);
+  const int rc = call([&] { return f(o.data_ptr(), static_cast<float*>(lse.data_ptr()), ws.data_ptr(), size, s); });
+  if (rc != FA2_OK) return PyLong_FromLong(rc);
+  return pair_of(std::move(o), std::move(lse));
+}
+
 // (q, k_pages, v_pages, page_table, kv_lens, cu_q, causal, scale)
 PyObject* forward_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    fa2_paged_cache c;
-    at::Device device(at::kCPU);
-    const at::Tensor* q = n == 8 ? tensor(a[0]) : nullptr;
-    if (!q || q->dim() != 3 || !cache_of(a + 1, &c, &device)) return none();
-    const int64_t T = q->size(0), Hq = q->size(1);
-    const int* cu;
-    if (!rows(q, T, Hq, c.d, c.dtype == FA2_DTYPE_BF16 ? at::kBFloat16 : at::kHalf, device) || Hq % c.kv_heads != 0 ||
-        !offsets_of(a[5], c.B, T, device, &cu))
-      return none();
+    Queries x;
+    if (n != 8 || !queries_of(a, &x)) return none();
     const int causal = PyObject_IsTrue(a[6]);
-    const double scale = a[7] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(c.d)))
-                                         : PyFloat_AsDouble(a[7]);
+    const double scale = scale_of(a[7], x.c.d);
     if (causal < 0 || PyErr_Occurred()) return nullptr;
-    const size_t size = workspace_bytes_fn(c.B, T, Hq, c.kv_heads, c.d, cu != nullptr);
-    at::Tensor o = make(q->sizes(), q->scalar_type(), device), lse = make({T, Hq}, at::kFloat, device);
-    at::Tensor ws = make({static_cast<int64_t>(size > 0 ? size : 1)}, at::kByte, device);
+    return attend(x, workspace_bytes_fn(x.c.B, x.T, x.Hq, x.c.kv_heads, x.c.d, x.cu != nullptr),
+                  [&](void* o, float* lse, void* ws, size_t size, fa2_stream_t s) {
+                    return forward_paged_fn(&x.c, x.q->data_ptr(), x.q->stride(0), x.q->stride(1), o, lse, x.cu, x.T,
+                                            x.Hq, causal, static_cast<float>(scale), x.c.dtype, ws, size, s);
+                  });
+  });
+}
+
+// (q, k_pages, v_pages, page_table, kv_lens, cu_q, window, sinks, scale); window and sinks fit C ints
+PyObject* forward_paged_window(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Queries x;
+    if (n != 9 || !queries_of(a, &x)) return none();
+    const long window = PyLong_AsLong(a[6]), sinks = PyLong_AsLong(a[7]);
+    const double scale = scale_of(a[8], x.c.d);
+    if (PyErr_Occurred()) return nullptr;
+    return attend(x, workspace_bytes_fn(x.c.B, x.T, x.Hq, x.c.kv_heads, x.c.d, x.cu != nullptr),
+                  [&](void* o, float* lse, void* ws, size_t size, fa2_stream_t s) {
+                    return paged_window_fn(&x.c, x.q->data_ptr(), x.q->stride(0), x.q->stride(1), o, lse, x.cu, x.T,
+                                           x.Hq, static_cast<int>(window), static_cast<int>(sinks),
+                                           static_cast<float>(scale), x.c.dtype, ws, size, s);
+                  });
+  });
+}
+
+// (q, k_pages, v_pages, page_table, kv_lens, cu_q, cu_groups, prefix_lens, causal, scale)
+PyObject* forward_paged_prefix(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Queries x;
+    if (n != 10 || !queries_of(a, &x)) return none();
+    const at::Tensor *first = tensor(a[6]), *lens = tensor(a[7]);
+    if (!lens || lens->dim() != 1 || lens->size(0) < 1 || !fits_int(lens->sizes()) || !ints(lens, lens->sizes(), x.device) ||
+        !ints(first, {lens->size(0) + 1}, x.device))
+      return none();
+    const int groups = static_cast<int>(lens->size(0)), causal = PyObject_IsTrue(a[8]);
+    const double scale = scale_of(a[9], x.c.d);
+    if (causal < 0 || PyErr_Occurred()) return nullptr;
+    return attend(x, prefix_workspace_fn(x.c.B, groups, x.T, x.Hq, x.c.kv_heads, x.c.d, x.cu != nullptr),
+                  [&](void* o, float* lse, void* ws, size_t size, fa2_stream_t s) {
+                    return paged_prefix_fn(&x.c, x.q->data_ptr(), x.q->stride(0), x.q->stride(1), o, lse, x.cu, x.T,
+                                           x.Hq, static_cast<const int*>(first->data_ptr()),
+                                           static_cast<const int*>(lens->data_ptr()), groups, causal,
+                                           static_cast<float>(scale), x.c.dtype, ws, size, s);
+                  });
+  });
+}
+
+// The arguments of the window calls: q [B, H, Nq, d], k and v [B, Hkv, Nk, d], dense.
+struct Windowed {
+  const at::Tensor *q, *k, *v;
+  int B, H, Hkv, Nq, Nk, d, code;
+  long window, sinks;
+};
+
+bool dense(const at::Tensor* t, c10::IntArrayRef shape, at::ScalarType type, at::Device device) {
+  return t && t->sizes() == shape && t->scalar_type() == type && t->device() == device && t->is_contiguous();
+}
+
+bool windowed(PyObject* q, PyObject* k, PyObject* v, PyObject* window, PyObject* sinks, Windowed* x) {
+  x->q = tensor(q);
+  x->k = tensor(k);
+  x->v = tensor(v);
+  if (!x->q || !x->k || !x->v || x->q->dim() != 4 || x->k->dim() != 4 || !current(x->q->device())) return false;
+  x->code = type_code(*x->q);
+  const at::ScalarType type = x->q->scalar_type();
+  if ((x->code != FA2_DTYPE_BF16 && x->code != FA2_DTYPE_FP16) || !fits_int(x->q->sizes()) || !fits_int(x->k->sizes()) ||
+      x->k->size(0) != x->q->size(0) || x->k->size(3) != x->q->size(3) ||
+      !dense(x->q, x->q->sizes(), type, x->q->device()) || !dense(x->k, x->k->sizes(), type, x->q->device()) ||
+      !dense(x->v, x->k->sizes(), type, x->q->device()))
+    return false;
+  x->B = static_cast<int>(x->q->size(0));
+  x->H = static_cast<int>(x->q->size(1));
+  x->Nq = static_cast<int>(x->q->size(2));
+  x->d = static_cast<int>(x->q->size(3));
+  x->Hkv = static_cast<int>(x->k->size(1));
+  x->Nk = static_cast<int>(x->k->size(2));
+  x->window = PyLong_AsLong(window);
+  x->sinks = PyLong_AsLong(sinks);
+  return x->Hkv > 0 && x->H % x->Hkv == 0;
+}
+
+// (q, k, v, window, sinks, scale, half): half: O of q's type instead of fp32
+PyObject* forward_window(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Windowed x;
+    if (n != 7 || !windowed(a[0], a[1], a[2], a[3], a[4], &x)) return PyErr_Occurred() ? nullptr : none();
+    const int half = PyObject_IsTrue(a[6]);
+    const double scale = scale_of(a[5], x.d);
+    if (half < 0 || PyErr_Occurred()) return nullptr;
+    const at::Device device = x.q->device();
+    at::Tensor o = make(x.q->sizes(), half ? x.q->scalar_type() : at::kFloat, device);
+    at::Tensor lse = make(x.q->sizes().slice(0, 3), at::kFloat, device);
     const fa2_stream_t s = stream_of(device);
     const int rc = call([&] {
-      return forward_paged_fn(&c, q->data_ptr(), q->stride(0), q->stride(1), o.data_ptr(),
-                              static_cast<float*>(lse.data_ptr()), cu, static_cast<int>(T), static_cast<int>(Hq), causal,
-                              static_cast<float>(scale), c.dtype, ws.data_ptr(), size, s);
+      return window_fn(x.q->data_ptr(), x.k->data_ptr(), x.v->data_ptr(), o.data_ptr(),
+                       static_cast<float*>(lse.data_ptr()), x.B, x.H, x.Hkv, x.Nq, x.Nk, x.d,
+                       static_cast<int>(x.window), static_cast<int>(x.sinks), static_cast<float>(scale), x.code,
+                       half ? x.code : static_cast<int>(FA2_DTYPE_FP32), s);
     });
     if (rc != FA2_OK) return PyLong_FromLong(rc);
     return pair_of(std::move(o), std::move(lse));
+  });
+}
+
+// (q, k, v, o, lse, do, window, sinks, scale, half): half: gradients of q's type instead of fp32
+PyObject* backward_window(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Windowed x;
+    if (n != 10 || !windowed(a[0], a[1], a[2], a[6], a[7], &x)) return PyErr_Occurred() ? nullptr : none();
+    const at::Tensor *o = tensor(a[3]), *lse = tensor(a[4]), *g = tensor(a[5]);
+    const at::Device device = x.q->device();
+    const at::ScalarType type = x.q->scalar_type();
+    if (!o || (o->scalar_type() != at::kFloat && o->scalar_type() != type) ||
+        !dense(o, x.q->sizes(), o->scalar_type(), device) || !dense(lse, x.q->sizes().slice(0, 3), at::kFloat, device) ||
+        !dense(g, x.q->sizes(), type, device))
+      return none();
+    const int half = PyObject_IsTrue(a[9]);
+    const double scale = scale_of(a[8], x.d);
+    if (half < 0 || PyErr_Occurred()) return nullptr;
+    const at::ScalarType kind = half ? type : at::kFloat;
+    const int code = half ? x.code : static_cast<int>(FA2_DTYPE_FP32);
+    const int window = static_cast<int>(x.window), sinks = static_cast<int>(x.sinks);
+    const size_t size = window_workspace_fn(x.B, x.H, x.Hkv, x.Nq, x.Nk, x.d, window, sinks, code);
+    at::Tensor dq = make(x.q->sizes(), kind, device), dk = make(x.k->sizes(), kind, device);
+    at::Tensor dv = make(x.k->sizes(), kind, device);
+    at::Tensor ws = make({static_cast<int64_t>(size > 0 ? size : 1)}, at::kByte, device);
+    const fa2_stream_t s = stream_of(device);
+    const int rc = call([&] {
+      return window_backward_fn(x.q->data_ptr(), x.k->data_ptr(), x.v->data_ptr(), o->data_ptr(), g->data_ptr(),
+                                static_cast<const float*>(lse->data_ptr()), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                x.B, x.H, x.Hkv, x.Nq, x.Nk, x.d, window, sinks, static_cast<float>(scale), x.code,
+                                type_code(*o), code, ws.data_ptr(), size, s);
+    });
+    if (rc != FA2_OK) return PyLong_FromLong(rc);
+    PyObject* three = PyTuple_New(3);
+    if (!three) return nullptr;
+    PyTuple_SET_ITEM(three, 0, THPVariable_Wrap(std::move(dq)));
+    PyTuple_SET_ITEM(three, 1, THPVariable_Wrap(std::move(dk)));
+    PyTuple_SET_ITEM(three, 2, THPVariable_Wrap(std::move(dv)));
+    return three;
   });
 }
 
@@ -556,7 +720,10 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
                  reinterpret_cast<void**>(&fork_fn), reinterpret_cast<void**>(&free_fn),
                  reinterpret_cast<void**>(&compact_fn), reinterpret_cast<void**>(&copy_fn),
                  reinterpret_cast<void**>(&append_norm_fn), reinterpret_cast<void**>(&norm_fn),
-                 reinterpret_cast<void**>(&norm_backward_fn), reinterpret_cast<void**>(&norm_workspace_fn)};
+                 reinterpret_cast<void**>(&norm_backward_fn), reinterpret_cast<void**>(&norm_workspace_fn),
+                 reinterpret_cast<void**>(&paged_window_fn), reinterpret_cast<void**>(&paged_prefix_fn),
+                 reinterpret_cast<void**>(&prefix_workspace_fn), reinterpret_cast<void**>(&window_fn),
+                 reinterpret_cast<void**>(&window_backward_fn), reinterpret_cast<void**>(&window_workspace_fn)};
   constexpr Py_ssize_t count = sizeof to / sizeof to[0];
   if (n != count) {
     PyErr_SetString(PyExc_ValueError, "init takes one address for each function");
@@ -576,6 +743,8 @@ PyMethodDef methods[] = {FA2_METHOD(init),          FA2_METHOD(forward_paged), F
                          FA2_METHOD(rope),          FA2_METHOD(pages_reserve), FA2_METHOD(pages_fork),
                          FA2_METHOD(pages_free),    FA2_METHOD(pages_compact), FA2_METHOD(pages_copy),
                          FA2_METHOD(norm_rope),     FA2_METHOD(norm_rope_backward),
+                         FA2_METHOD(forward_paged_window), FA2_METHOD(forward_paged_prefix),
+                         FA2_METHOD(forward_window), FA2_METHOD(backward_window),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

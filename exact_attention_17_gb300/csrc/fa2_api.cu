@@ -75,6 +75,7 @@ int device_ready() {
         fa2host::prepare_bwd() != cudaSuccess || fa2host::prepare_bwd2() != cudaSuccess ||
         fa2host::prepare_window_bf16() != cudaSuccess || fa2host::prepare_window_f16() != cudaSuccess ||
         fa2host::prepare_bwd_window() != cudaSuccess ||
+        fa2host::prepare_paged_ext_bf16() != cudaSuccess || fa2host::prepare_paged_ext_f16() != cudaSuccess ||
         fa2host::prepare_paged_bf16() != cudaSuccess || fa2host::prepare_paged_f16() != cudaSuccess)
       return;
     st.usable = true;

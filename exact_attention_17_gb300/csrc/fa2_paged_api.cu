@@ -86,39 +86,68 @@ extern "C" size_t fa2_forward_paged_workspace_bytes(int B, int T, int Hq, int kv
   return plan_paged(B, T, Hq, kv_heads, d, has_cu_q != 0, sms).bytes;
 }
 
-extern "C" int fa2_forward_paged(const fa2_paged_cache* cache, const void* Q, long long q_token_stride,
-                                 long long q_head_stride, void* O, float* LSE, const int* cu_q, int T, int Hq,
-                                 int causal, float scale, int o_dtype, void* workspace, size_t workspace_size,
-                                 fa2_stream_t stream) {
-  if (!cache) return FA2_ERR_NULL;
-  if (T < 0 || Hq < 0) return FA2_ERR_SHAPE;
-  if (T == 0 || Hq == 0 || cache->B == 0) return FA2_OK;
-  int rc = check_cache(cache);
-  if (rc != FA2_OK) return rc;
-  const fa2_paged_cache& c = *cache;
-  if (o_dtype != FA2_DTYPE_FP32 && o_dtype != c.dtype) return FA2_ERR_DTYPE;
-  if (Hq % c.kv_heads != 0 || Hq / c.kv_heads > 128 || (!cu_q && T != c.B)) return FA2_ERR_SHAPE;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return FA2_ERR_SCALE;
-  if ((rc = check_rows(Q, q_token_stride, q_head_stride, T, Hq, c.d)) != FA2_OK) return rc;
-  if (!O || !LSE || !workspace) return FA2_ERR_NULL;
-  if (misaligned(O, 15) || misaligned(LSE, 3) || misaligned(cu_q, 3) || misaligned(workspace, 255)) return FA2_ERR_ALIGN;
-  if ((rc = fa2host::require_device()) != FA2_OK) return rc;
-  const bool half_out = o_dtype != FA2_DTYPE_FP32, f16 = c.dtype == FA2_DTYPE_FP16;
-  const long long rows = static_cast<long long>(T) * Hq;
-  const PagedPlan plan = plan_paged(c.B, T, Hq, c.kv_heads, c.d, cu_q != nullptr, fa2host::device_sms());
-  if ((rc = check_cache_memory(cache)) != FA2_OK) return rc;
-  if (!rows_in_memory(Q, q_token_stride, q_head_stride, T, Hq, c.d) || !range_ok(O, rows * c.d, half_out ? 2 : 4) ||
-      !range_ok(LSE, rows, 4) || (cu_q && !range_ok(cu_q, c.B + 1ll, 4)) || workspace_size < plan.bytes ||
-      !fa2host::device_memory_ok(workspace, plan.bytes))
-    return FA2_ERR_MEMORY;
-  if (plan.items + 2ll * plan.ctas > 0x7fffffffll) return FA2_ERR_SHAPE;
+namespace {
 
+// The arguments that the attention calls over a cache share.
+struct PagedCall {
+  const fa2_paged_cache* cache;
+  const void* Q;
+  long long q_token_stride, q_head_stride;
+  void* O;
+  float* LSE;
+  const int* cu_q;
+  int T, Hq, causal;
+  float scale;
+  int o_dtype;
+  void* workspace;
+  size_t workspace_size;
+};
+
+bool empty_call(const PagedCall& a) { return a.T == 0 || a.Hq == 0 || a.cache->B == 0; }
+
+// What can be checked without a device, of a call that is not empty.
+int check_call(const PagedCall& a) {
+  int rc = check_cache(a.cache);
+  if (rc != FA2_OK) return rc;
+  const fa2_paged_cache& c = *a.cache;
+  if (a.o_dtype != FA2_DTYPE_FP32 && a.o_dtype != c.dtype) return FA2_ERR_DTYPE;
+  if (a.Hq % c.kv_heads != 0 || a.Hq / c.kv_heads > 128 || (!a.cu_q && a.T != c.B)) return FA2_ERR_SHAPE;
+  if (!(a.scale > 0.f) || !std::isfinite(a.scale)) return FA2_ERR_SCALE;
+  if ((rc = check_rows(a.Q, a.q_token_stride, a.q_head_stride, a.T, a.Hq, c.d)) != FA2_OK) return rc;
+  if (!a.O || !a.LSE || !a.workspace) return FA2_ERR_NULL;
+  if (misaligned(a.O, 15) || misaligned(a.LSE, 3) || misaligned(a.cu_q, 3) || misaligned(a.workspace, 255))
+    return FA2_ERR_ALIGN;
+  return FA2_OK;
+}
+
+int check_call_memory(const PagedCall& a, size_t workspace_bytes) {
+  const fa2_paged_cache& c = *a.cache;
+  const int rc = check_cache_memory(a.cache);
+  if (rc != FA2_OK) return rc;
+  const long long rows = static_cast<long long>(a.T) * a.Hq;
+  return rows_in_memory(a.Q, a.q_token_stride, a.q_head_stride, a.T, a.Hq, c.d) &&
+                 range_ok(a.O, rows * c.d, a.o_dtype != FA2_DTYPE_FP32 ? 2 : 4) && range_ok(a.LSE, rows, 4) &&
+                 (!a.cu_q || range_ok(a.cu_q, c.B + 1ll, 4)) && a.workspace_size >= workspace_bytes &&
+                 fa2host::device_memory_ok(a.workspace, workspace_bytes)
+             ? FA2_OK
+             : FA2_ERR_MEMORY;
+}
+
+struct PagedMaps {
+  CUtensorMap q, k, v;
+};
+
+// Maps and parameters of one launch over `B` sequences as `plan` lays it out, its
+// workspace at `ws`; without a window.
+int prepare_launch(const PagedCall& a, const PagedPlan& plan, int B, char* ws, PagedMaps* maps, fa2dev::PagedParams* out) {
+  const fa2_paged_cache& c = *a.cache;
+  if (plan.items + 2ll * plan.ctas > 0x7fffffffll) return FA2_ERR_SHAPE;
+  const bool f16 = c.dtype == FA2_DTYPE_FP16;
   using ull = unsigned long long;
-  CUtensorMap mq, mk, mv;
-  const ull qd[3] = {static_cast<ull>(c.d), static_cast<ull>(Hq), static_cast<ull>(T)};
+  const ull qd[3] = {static_cast<ull>(c.d), static_cast<ull>(a.Hq), static_cast<ull>(a.T)};
   const ull row_bytes = static_cast<ull>(c.d) * 2;
-  const ull qs[2] = {Hq > 1 ? static_cast<ull>(q_head_stride) * 2 : row_bytes,
-                     T > 1 ? static_cast<ull>(q_token_stride) * 2 : row_bytes};
+  const ull qs[2] = {a.Hq > 1 ? static_cast<ull>(a.q_head_stride) * 2 : row_bytes,
+                     a.T > 1 ? static_cast<ull>(a.q_token_stride) * 2 : row_bytes};
   const unsigned qb[3] = {64, static_cast<unsigned>(plan.G), static_cast<unsigned>(plan.box_tokens)};
   const ull kd[4] = {static_cast<ull>(c.d), static_cast<ull>(c.page_size), static_cast<ull>(c.kv_heads),
                      static_cast<ull>(c.num_pages)};
@@ -126,24 +155,25 @@ extern "C" int fa2_forward_paged(const fa2_paged_cache* cache, const void* Q, lo
                      c.kv_heads > 1 ? static_cast<ull>(c.head_stride) * 2 : row_bytes,
                      c.num_pages > 1 ? static_cast<ull>(c.page_stride) * 2 : row_bytes};
   const unsigned kb[4] = {64, static_cast<unsigned>(c.page_size < 128 ? c.page_size : 128), 1, 1};
-  if (!fa2host::encode_tiled(&mq, f16, 3, Q, qd, qs, qb) || !fa2host::encode_tiled(&mk, f16, 4, c.k_pages, kd, ks, kb) ||
-      !fa2host::encode_tiled(&mv, f16, 4, c.v_pages, kd, ks, kb))
+  if (!fa2host::encode_tiled(&maps->q, f16, 3, a.Q, qd, qs, qb) ||
+      !fa2host::encode_tiled(&maps->k, f16, 4, c.k_pages, kd, ks, kb) ||
+      !fa2host::encode_tiled(&maps->v, f16, 4, c.v_pages, kd, ks, kb))
     return FA2_ERR_SHAPE;
-
-  fa2dev::PagedParams p;
+  fa2dev::PagedParams& p = *out;
+  p = {};
   p.page_table = c.page_table;
   p.kv_lens = c.kv_lens;
-  p.cu_q = cu_q;
-  p.O = O;
-  p.LSE = LSE;
-  p.O_part = static_cast<float*>(workspace);
-  p.LSE_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.lse_at);
-  p.counter = reinterpret_cast<int*>(static_cast<char*>(workspace) + plan.counter_at);
+  p.cu_q = a.cu_q;
+  p.O = a.O;
+  p.LSE = a.LSE;
+  p.O_part = reinterpret_cast<float*>(ws);
+  p.LSE_part = reinterpret_cast<float*>(ws + plan.lse_at);
+  p.counter = reinterpret_cast<int*>(ws + plan.counter_at);
   p.slots = plan.slots;
   p.part_rows = plan.part_rows;
-  p.B = c.B;
-  p.T = T;
-  p.Hq = Hq;
+  p.B = B;
+  p.T = a.T;
+  p.Hq = a.Hq;
   p.Hkv = c.kv_heads;
   p.G = plan.G;
   p.sub_tokens = plan.sub_tokens;
@@ -157,22 +187,166 @@ extern "C" int fa2_forward_paged(const fa2_paged_cache* cache, const void* Q, lo
   p.inv_ctas = 1.0 / plan.ctas;
   p.min_tiles = kMinTiles;
   p.item_keys = plan.narrow ? kItemKeysNarrow : kItemKeys;
-  p.causal = causal != 0;
-  p.o_half = half_out ? 1 : 0;
+  p.causal = a.causal != 0;
+  p.o_half = a.o_dtype != FA2_DTYPE_FP32 ? 1 : 0;
   p.narrow = plan.narrow ? 1 : 0;
-  p.scale_log2 = scale * kLog2e;
+  p.scale_log2 = a.scale * kLog2e;
   p.status = fa2host::device_status_word();
   p.timeout_ns = fa2host::wait_timeout_ns();
-  if (p.status == nullptr) return FA2_ERR_LAUNCH;
-  // columns: items that may be cut; rows: warps for their rows
+  p.window = 1 << 30;
+  p.most_keys = 1 << 30;
+  return p.status == nullptr ? FA2_ERR_LAUNCH : FA2_OK;
+}
+
+// The merge's grid: columns: items that may be cut; rows: warps for their rows.
+dim3 merge_grid(const PagedPlan& plan) {
   constexpr int kMergeRows = fa2dev::kPagedMergeWarps * fa2dev::kPagedMergeRows;
-  dim3 merge(static_cast<unsigned>(plan.even ? plan.ctas - 1 : plan.ctas),
-             static_cast<unsigned>((plan.part_rows + kMergeRows - 1) / kMergeRows));
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return dim3(static_cast<unsigned>(plan.even ? plan.ctas - 1 : plan.ctas),
+              static_cast<unsigned>((plan.part_rows + kMergeRows - 1) / kMergeRows));
+}
+
+// window 0: none.
+int forward_paged(const PagedCall& a, int window, int sinks, cudaStream_t s) {
+  int rc;
+  if ((rc = fa2host::require_device()) != FA2_OK) return rc;
+  const fa2_paged_cache& c = *a.cache;
+  const PagedPlan plan = plan_paged(c.B, a.T, a.Hq, c.kv_heads, c.d, a.cu_q != nullptr, fa2host::device_sms());
+  if ((rc = check_call_memory(a, plan.bytes)) != FA2_OK) return rc;
+  PagedMaps maps;
+  fa2dev::PagedParams p;
+  if ((rc = prepare_launch(a, plan, c.B, static_cast<char*>(a.workspace), &maps, &p)) != FA2_OK) return rc;
   if (!plan.even && cudaMemsetAsync(p.counter, 0, sizeof(int), s) != cudaSuccess) return FA2_ERR_LAUNCH;
-  const auto launch = f16 ? fa2host::launch_paged_f16 : fa2host::launch_paged_bf16;
-  return launch(c.d, plan.subs, mq, mk, mv, p, static_cast<unsigned>(plan.ctas), merge, s) ==
+  const bool f16 = c.dtype == FA2_DTYPE_FP16;
+  auto launch = f16 ? fa2host::launch_paged_f16 : fa2host::launch_paged_bf16;
+  if (window > 0) {
+    launch = f16 ? fa2host::launch_paged_ext_f16 : fa2host::launch_paged_ext_bf16;
+    // what lies beyond the longest sequence means the same as it
+    p.window = window < p.max_len ? window : p.max_len;
+    p.sinks = sinks < p.max_len ? sinks : p.max_len;
+    // tiles that hold sinks, and most that a block's windows reach over (n keys lie in at most (n + 126) / 128 + 1)
+    const long long tiles = (p.sinks + 127) / 128 + (static_cast<long long>(plan.sub_tokens) * plan.subs - 1 + p.window + 126) / 128 + 1;
+    if (tiles * 128 < p.most_keys) p.most_keys = static_cast<int>(tiles * 128);
+  }
+  return launch(c.d, plan.subs, maps.q, maps.k, maps.v, p, static_cast<unsigned>(plan.ctas), merge_grid(plan), s) ==
                  cudaSuccess
+             ? FA2_OK
+             : FA2_ERR_LAUNCH;
+}
+
+}  // namespace
+
+extern "C" int fa2_forward_paged(const fa2_paged_cache* cache, const void* Q, long long q_token_stride,
+                                 long long q_head_stride, void* O, float* LSE, const int* cu_q, int T, int Hq,
+                                 int causal, float scale, int o_dtype, void* workspace, size_t workspace_size,
+                                 fa2_stream_t stream) {
+  if (!cache) return FA2_ERR_NULL;
+  if (T < 0 || Hq < 0) return FA2_ERR_SHAPE;
+  const PagedCall a = {cache, Q, q_token_stride, q_head_stride, O, LSE, cu_q, T, Hq, causal, scale, o_dtype, workspace,
+                       workspace_size};
+  if (empty_call(a)) return FA2_OK;
+  const int rc = check_call(a);
+  return rc != FA2_OK ? rc : forward_paged(a, 0, 0, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int fa2_forward_paged_window(const fa2_paged_cache* cache, const void* Q, long long q_token_stride,
+                                        long long q_head_stride, void* O, float* LSE, const int* cu_q, int T, int Hq,
+                                        int window, int sinks, float scale, int o_dtype, void* workspace,
+                                        size_t workspace_size, fa2_stream_t stream) {
+  if (!cache) return FA2_ERR_NULL;
+  if (T < 0 || Hq < 0 || window < 1 || sinks < 0) return FA2_ERR_SHAPE;
+  const PagedCall a = {cache, Q, q_token_stride, q_head_stride, O, LSE, cu_q, T, Hq, 1, scale, o_dtype, workspace,
+                       workspace_size};
+  if (empty_call(a)) return FA2_OK;
+  const int rc = check_call(a);
+  return rc != FA2_OK ? rc : forward_paged(a, window, sinks, reinterpret_cast<cudaStream_t>(stream));
+}
+
+namespace {
+
+// A call with shared prefixes: the groups' launch, the sequences' own, and what
+// joins their results.
+struct PrefixPlan {
+  PagedPlan prefix, own;
+  size_t own_at, o_at[2], lse_at[2], bytes;   // workspace; O and LSE of the two launches in fp32
+};
+
+PrefixPlan plan_prefix(int B, int groups, int T, int Hq, int Hkv, int d, bool has_cu, int sms) {
+  PrefixPlan q;
+  q.prefix = plan_paged(groups, T, Hq, Hkv, d, true, sms);
+  q.own = plan_paged(B, T, Hq, Hkv, d, has_cu, sms);
+  q.prefix.even = q.own.even = true;   // (a counter would need clearing between two launches that run side by side)
+  q.own_at = align256(q.prefix.bytes);
+  size_t at = q.own_at + align256(q.own.bytes);
+  const size_t rows = static_cast<size_t>(T) * Hq;
+  for (int i = 0; i < 2; ++i) {
+    q.o_at[i] = at;
+    at += align256(rows * d * 4);
+    q.lse_at[i] = at;
+    at += align256(rows * 4);
+  }
+  q.bytes = at;
+  return q;
+}
+
+}  // namespace
+
+extern "C" size_t fa2_forward_paged_prefix_workspace_bytes(int B, int groups, int T, int Hq, int kv_heads, int d,
+                                                           int has_cu_q) {
+  if (B < 1 || groups < 1 || T < 1 || Hq < 1 || kv_heads < 1 || Hq % kv_heads != 0 || Hq / kv_heads > 128) return 0;
+  if (d != 64 && d != 128 && d != 256) return 0;
+  int sms = 0, dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return plan_prefix(B, groups, T, Hq, kv_heads, d, has_cu_q != 0, sms).bytes;
+}
+
+extern "C" int fa2_forward_paged_prefix(const fa2_paged_cache* cache, const void* Q, long long q_token_stride,
+                                        long long q_head_stride, void* O, float* LSE, const int* cu_q, int T, int Hq,
+                                        const int* cu_groups, const int* prefix_lens, int groups, int causal,
+                                        float scale, int o_dtype, void* workspace, size_t workspace_size,
+                                        fa2_stream_t stream) {
+  if (!cache) return FA2_ERR_NULL;
+  if (T < 0 || Hq < 0 || groups < 0) return FA2_ERR_SHAPE;
+  const PagedCall a = {cache, Q, q_token_stride, q_head_stride, O, LSE, cu_q, T, Hq, causal, scale, o_dtype, workspace,
+                       workspace_size};
+  if (empty_call(a)) return FA2_OK;
+  int rc = check_call(a);
+  if (rc != FA2_OK) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (groups == 0) return forward_paged(a, 0, 0, s);   // nothing is shared
+  const fa2_paged_cache& c = *cache;
+  if (groups > c.B) return FA2_ERR_SHAPE;
+  if (!cu_groups || !prefix_lens) return FA2_ERR_NULL;
+  if (misaligned(cu_groups, 3) || misaligned(prefix_lens, 3)) return FA2_ERR_ALIGN;
+  if ((rc = fa2host::require_device()) != FA2_OK) return rc;
+  const PrefixPlan plan = plan_prefix(c.B, groups, T, Hq, c.kv_heads, c.d, cu_q != nullptr, fa2host::device_sms());
+  if ((rc = check_call_memory(a, plan.bytes)) != FA2_OK) return rc;
+  if (!range_ok(cu_groups, groups + 1ll, 4) || !range_ok(prefix_lens, groups, 4)) return FA2_ERR_MEMORY;
+  char* ws = static_cast<char*>(workspace);
+  PagedCall part = a;
+  part.o_dtype = FA2_DTYPE_FP32;
+  PagedMaps maps[2];
+  fa2dev::PagedParams p[2];
+  for (int i = 0; i < 2; ++i) {
+    part.O = ws + plan.o_at[i];
+    part.LSE = reinterpret_cast<float*>(ws + plan.lse_at[i]);
+    part.causal = i == 0 ? 0 : causal;
+    rc = i == 0 ? prepare_launch(part, plan.prefix, groups, ws, &maps[0], &p[0])
+                : prepare_launch(part, plan.own, c.B, ws + plan.own_at, &maps[1], &p[1]);
+    if (rc != FA2_OK) return rc;
+    p[i].role = i == 0 ? fa2dev::kPagedPrefix : fa2dev::kPagedOwn;
+    p[i].seqs = c.B;
+    p[i].groups = groups;
+    p[i].cu_groups = cu_groups;
+    p[i].prefix_lens = prefix_lens;
+  }
+  const bool f16 = c.dtype == FA2_DTYPE_FP16;
+  return fa2host::launch_paged_prefix(c.d, f16, plan.prefix.subs, maps[0].q, maps[0].k, maps[0].v, p[0],
+                                      merge_grid(plan.prefix), plan.own.subs, maps[1].q, maps[1].k, maps[1].v, p[1],
+                                      merge_grid(plan.own), O, LSE, o_dtype != FA2_DTYPE_FP32, s) == cudaSuccess
              ? FA2_OK
              : FA2_ERR_LAUNCH;
 }

@@ -60,6 +60,19 @@
 //    of it).  A ring of descriptions that each role reads at its own pace was
 //    slower: 1115 -> 1158 us for those 8192 tokens.
 //
+//  * Windows, shared prefixes (EXT; the other kernels do not have their code).  With
+//    a window a token at position t sees the keys j <= t with t - j < window or j <
+//    sinks.  The tiles of a block are those with sinks and those from its first
+//    token's window on: a list with one gap, whose numbers the schedule and the
+//    pipeline count in; only the copies and the masks look up which tile of the keys it
+//    is.  A page without a key that some row of the block sees is not read (its number
+//    may be anything: zeros are copied from outside the pool).  The cost of a block is
+//    that of its keys, at most the longest list there can be, so that sums of
+//    costs stay closed forms.
+//    With a shared prefix one launch has the groups of sequences as its sequences (all
+//    their new tokens over the shared pages, without a mask) and the next the sequences
+//    over their own pages; see fa2_paged_api.cu.
+//
 // Bound and measured.  Single tokens: bytes (64 sequences of 1000-8192 keys, 8
 // key/value heads of 128: 1.11 GB in 169.5-172 us, 6.48-6.57 TB/s; four of
 // 100000-131072 keys, d = 64: 84.3-85.7 us, 5.6-5.7 TB/s).  Chunks: the tensor pipe,
@@ -72,6 +85,8 @@
 #pragma once
 
 #include <type_traits>
+
+#include <climits>
 
 #include "fa2_fwd_sm103.cuh"
 
@@ -109,9 +124,21 @@ struct PagedParams {
   float scale_log2;
   int* status;
   unsigned long long timeout_ns;
+  // EXT
+  int window, sinks;       // window 2^30: none
+  int most_keys;           // bound of the keys of a block's list, in whole tiles
+  int role;                // kPagedPlain, kPagedPrefix or kPagedOwn
+  int seqs;                // kPagedPrefix: sequences (B counts the groups)
+  int groups;
+  const int* cu_groups;    // [groups + 1]: first sequence of each group
+  const int* prefix_lens;  // [groups]: tokens that a group's sequences share
 };
 
-// Key tiles [t_begin, t_end) of an item.
+constexpr int kPagedPlain = 0;
+constexpr int kPagedPrefix = 1;   // the new tokens of groups of sequences over the groups' shared pages
+constexpr int kPagedOwn = 2;      // the new tokens of each sequence over its pages behind the shared ones
+
+// Key tiles [t_begin, t_end) of an item; EXT: numbers of its list (see tile).
 struct PagedUnit {
   int valid;
   int head;
@@ -122,6 +149,11 @@ struct PagedUnit {
   int t_begin, t_end;
   int slot;       // workspace slot of this part, -1: the whole item
   long long table;   // offset of the sequence's row in the page table
+  int sink_tiles, skip;   // EXT: list entry v is tile v (v < sink_tiles) or v + skip
+  template <bool EXT>
+  __device__ __forceinline__ int tile(int v) const {
+    return !EXT || v < sink_tiles ? v : v + skip;
+  }
 };
 
 // Keys that the token `tok` of a sequence keeps: [0, kept).
@@ -134,23 +166,98 @@ __device__ __forceinline__ int key_tiles_of(int keys) { return (keys + kKeysPerT
 // Sequence b's new tokens and keys.
 struct PagedSeq {
   int q0, q_len, kv_len, blocks;
+  int row, page0;   // EXT: row of the page table, its first entry
 };
 
+// Whole pages that the sequences of group g share (0 for a lone sequence), in tokens, and the group's sequences
+// [first, last); what is out of order counts as nothing and is reported.
+struct PagedGroup {
+  int first, last, prefix;
+  bool bad;
+};
+
+__device__ __forceinline__ PagedGroup paged_group(const PagedParams& p, int seqs, int g) {
+  PagedGroup o;
+  o.first = p.cu_groups[g];
+  o.last = p.cu_groups[g + 1];
+  o.prefix = p.prefix_lens[g];
+  o.bad = o.first < 0 || o.last < o.first || o.last > seqs || o.prefix < 0 || o.prefix > p.max_len;
+  if (o.bad) o.first = o.last = 0;
+  o.prefix = o.last - o.first < 2 ? 0 : o.prefix >> p.page_log2 << p.page_log2;
+  return o;
+}
+
+// Tokens of sequence b that its group holds together (0: none).
+__device__ __forceinline__ int paged_shared(const PagedParams& p, int seqs, int b, bool* bad) {
+  int lo = 0, n = p.groups;   // the last group that begins at or before b
+  while (n > 1) {
+    const int half = n / 2;
+    if (p.cu_groups[lo + half] <= b) {
+      lo += half;
+      n -= half;
+    } else {
+      n = half;
+    }
+  }
+  if (n < 1) return 0;
+  const PagedGroup g = paged_group(p, seqs, lo);
+  *bad = g.bad;
+  return g.first <= b && b < g.last ? g.prefix : 0;
+}
+
+template <bool EXT>
 __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b, int block) {
+  PagedSeq s;
+  if constexpr (EXT) {
+    s.row = b;
+    s.page0 = 0;
+    if (p.role == kPagedPrefix) {
+      PagedGroup g = {0, 0, 0, false};
+      if (b < p.B) g = paged_group(p, p.seqs, b);
+      s.q0 = s.q_len = 0;
+      if (g.prefix > 0) {
+        const int begin = p.cu_q ? p.cu_q[g.first] : g.first, end = p.cu_q ? p.cu_q[g.last] : g.last;
+        s.q0 = min(max(begin, 0), p.T);
+        s.q_len = max(0, min(end, p.T) - s.q0);
+      }
+      s.kv_len = g.prefix;
+      s.row = g.first;
+      if (blockIdx.x == 0 && g.bad) atomicOr(p.status, kDevErrPage);
+      s.blocks = (s.q_len + block - 1) / block;
+      return s;
+    }
+  }
   int begin = 0, end = 0, kv = 0;   // nothing for b >= B
   if (b < p.B) {
     begin = p.cu_q ? p.cu_q[b] : b;
     end = p.cu_q ? p.cu_q[b + 1] : b + 1;
     kv = p.kv_lens[b];
   }
-  PagedSeq s;
   s.q0 = min(max(begin, 0), p.T);
   s.q_len = max(0, min(end, p.T) - s.q0);
   s.kv_len = min(max(kv, 0), p.max_len);
   if (blockIdx.x == 0 && (begin < 0 || end < begin || end > p.T || kv < 0 || kv > p.max_len))
     atomicOr(p.status, kDevErrPage);
+  if constexpr (EXT) {
+    if (p.role == kPagedOwn && b < p.B) {
+      bool bad = false;
+      const int shared = paged_shared(p, p.B, b, &bad);
+      // the shared tokens lie before the new ones
+      if (blockIdx.x == 0 && (bad || shared > s.kv_len - s.q_len)) atomicOr(p.status, kDevErrPage);
+      s.kv_len = max(0, s.kv_len - shared);
+      s.page0 = shared >> p.page_log2;
+    }
+  }
   s.blocks = (s.q_len + block - 1) / block;
   return s;
+}
+
+// EXT: a block's list, whose first token is token tok0 of the sequence.
+__device__ __forceinline__ void paged_list(const PagedParams& p, const PagedSeq& s, int tok0, int* sink_tiles,
+                                           int* skip) {
+  const int lo = max(0, s.kv_len - s.q_len + tok0 - p.window + 1) / kKeysPerTile;
+  *sink_tiles = min(key_tiles_of(p.sinks), lo);
+  *skip = lo - *sink_tiles;
 }
 
 // Cost of an item: item_keys for its start and end, then its keys, at least one (a
@@ -163,7 +270,8 @@ __device__ __forceinline__ int block_keys(const PagedParams& p, const PagedSeq& 
 }
 
 // Cost of the blocks 0 .. i-1 of a sequence (0 <= i <= blocks).
-template <int SUBS>
+// EXT: a block costs at most most_keys.
+template <int SUBS, bool EXT>
 __device__ __forceinline__ long long cost_before(const PagedParams& p, const PagedSeq& s, int i) {
   if (i == 0) return 0;
   const int block = p.sub_tokens * SUBS;
@@ -173,13 +281,20 @@ __device__ __forceinline__ long long cost_before(const PagedParams& p, const Pag
   if (p.causal) {
     const long long lead = static_cast<long long>(s.kv_len) - s.q_len;
     const int none = lead >= 0 ? 0 : min(full, static_cast<int>(-lead) / block);   // blocks without a key count one
-    const long long n = full - none;
-    keys = none + n * (lead + none * static_cast<long long>(block)) + block * (n * (n + 1) / 2);
+    long long n = full - none;
+    keys = none;
+    if constexpr (EXT) {   // blocks whose keys are as many as any block's (lead + (k + 1) block > most_keys)
+      const long long below = lead > p.most_keys ? 0 : (p.most_keys - lead) / block;
+      const long long most = max(0ll, min(n, full - below));
+      keys += most * p.most_keys;
+      n -= most;
+    }
+    keys += n * (lead + none * static_cast<long long>(block)) + block * (n * (n + 1) / 2);
   } else {
-    keys = static_cast<long long>(full) * max(1, s.kv_len);
+    keys = static_cast<long long>(full) * max(1, EXT ? min(s.kv_len, p.most_keys) : s.kv_len);
   }
   keys += static_cast<long long>(i) * p.item_keys;
-  if (i == s.blocks) keys += max(1, s.kv_len);
+  if (i == s.blocks) keys += max(1, EXT ? min(s.kv_len, p.most_keys) : s.kv_len);
   return keys;
 }
 
@@ -199,8 +314,13 @@ __device__ __forceinline__ long long warp_scan(long long v) {   // inclusive
   return v;
 }
 
+template <bool EXT>
 __device__ __forceinline__ PagedSeq seq_from(const PagedSeq& s, int src) {
   PagedSeq r;
+  if constexpr (EXT) {
+    r.row = __shfl_sync(0xffffffffu, s.row, src);
+    r.page0 = __shfl_sync(0xffffffffu, s.page0, src);
+  }
   r.q0 = __shfl_sync(0xffffffffu, s.q0, src);
   r.q_len = __shfl_sync(0xffffffffu, s.q_len, src);
   r.kv_len = __shfl_sync(0xffffffffu, s.kv_len, src);
@@ -223,11 +343,17 @@ struct PagedPlace {
     if (pos >= start + cost) return tiles;
     return min(tiles, key_tiles_of(static_cast<int>(x)));
   }
-  template <int SUBS>
+  template <int SUBS, bool EXT>
   __device__ __forceinline__ void measure(const PagedParams& p) {
     const int keys = block_keys(p, s, p.sub_tokens * SUBS, i);
     tiles = key_tiles_of(keys);
     cost = p.item_keys + keys;
+    if constexpr (EXT) {
+      int sink_tiles, skip;
+      paged_list(p, s, i * p.sub_tokens * SUBS, &sink_tiles, &skip);
+      tiles -= skip;
+      cost = p.item_keys + min(keys, p.most_keys);
+    }
   }
 };
 
@@ -243,14 +369,14 @@ struct PagedStrips {
   long long cost;
 };
 
-template <int SUBS>
+template <int SUBS, bool EXT>
 __device__ __forceinline__ PagedStrips paged_strips(const PagedParams& p) {
   const int lane = threadIdx.x & 31, block = p.sub_tokens * SUBS;
   PagedStrips f;
   f.strip = (p.B + 31) / 32;
   if (f.strip == 1) {
-    f.s = paged_seq(p, lane, block);
-    f.cost = cost_before<SUBS>(p, f.s, f.s.blocks);
+    f.s = paged_seq<EXT>(p, lane, block);
+    f.cost = cost_before<SUBS, EXT>(p, f.s, f.s.blocks);
     return f;
   }
   const int end = min(p.B, (lane + 1) * f.strip);
@@ -258,8 +384,8 @@ __device__ __forceinline__ PagedStrips paged_strips(const PagedParams& p) {
   f.cost = 0;
 #pragma unroll 1
   for (int b = lane * f.strip; b < end; ++b) {
-    const PagedSeq s = paged_seq(p, b, block);
-    f.cost += cost_before<SUBS>(p, s, s.blocks);
+    const PagedSeq s = paged_seq<EXT>(p, b, block);
+    f.cost += cost_before<SUBS, EXT>(p, s, s.blocks);
   }
   return f;
 }
@@ -267,7 +393,7 @@ __device__ __forceinline__ PagedStrips paged_strips(const PagedParams& p) {
 // Whole warp: the length of one of p.ctas equal ranges of the list, at least an
 // item's fixed cost and one tile, so that an item's inner ranges all have tiles;
 // and the length of the list.
-template <int SUBS>
+template <int SUBS, bool EXT>
 __device__ __forceinline__ long long paged_share(const PagedParams& p, const PagedStrips& f, long long* total) {
   const long long sum = warp_sum(f.cost) * p.Hkv;
   *total = sum;
@@ -277,7 +403,7 @@ __device__ __forceinline__ long long paged_share(const PagedParams& p, const Pag
 }
 
 // Whole warp: the item that position `pos` (below the list's length) lies in.
-template <int SUBS>
+template <int SUBS, bool EXT>
 __device__ __forceinline__ PagedPlace paged_find(const PagedParams& p, const PagedStrips& f, long long pos) {
   const int lane = threadIdx.x & 31;
   PagedPlace w = {};
@@ -293,8 +419,8 @@ __device__ __forceinline__ PagedPlace paged_find(const PagedParams& p, const Pag
     end = min(p.B, begin + f.strip);
   }
   for (int b0 = begin; b0 < end; b0 += 32) {
-    const PagedSeq s = f.strip == 1 ? f.s : paged_seq(p, b0 + lane < end ? b0 + lane : p.B, p.sub_tokens * SUBS);
-    const long long per_head = f.strip == 1 ? f.cost : cost_before<SUBS>(p, s, s.blocks);
+    const PagedSeq s = f.strip == 1 ? f.s : paged_seq<EXT>(p, b0 + lane < end ? b0 + lane : p.B, p.sub_tokens * SUBS);
+    const long long per_head = f.strip == 1 ? f.cost : cost_before<SUBS, EXT>(p, s, s.blocks);
     const long long mine = per_head * p.Hkv, sum = warp_scan(mine) + before;
     const unsigned here = __ballot_sync(0xffffffffu, pos >= sum - mine && pos < sum);
     if (here == 0) {
@@ -305,7 +431,7 @@ __device__ __forceinline__ PagedPlace paged_find(const PagedParams& p, const Pag
     w.start = __shfl_sync(0xffffffffu, sum - mine, src);
     const long long each = __shfl_sync(0xffffffffu, per_head, src);
     w.b = b0 + src;
-    w.s = seq_from(s, src);
+    w.s = seq_from<EXT>(s, src);
     // heads and blocks that start at or before pos, 32 candidates at a time
     for (int h0 = 0; h0 < p.Hkv; h0 += 32) {
       const unsigned some =
@@ -318,19 +444,20 @@ __device__ __forceinline__ PagedPlace paged_find(const PagedParams& p, const Pag
     while (n > 1) {
       const int step = (n + 31) / 32;
       const bool below =
-          lane * step < n && w.start + cost_before<SUBS>(p, w.s, lo + min(lane * step, n)) <= pos;
+          lane * step < n && w.start + cost_before<SUBS, EXT>(p, w.s, lo + min(lane * step, n)) <= pos;
       const int last = 31 - __clz(__ballot_sync(0xffffffffu, below));
       n = min(step, n - last * step);
       lo += last * step;
     }
     w.i = lo;
-    w.start += cost_before<SUBS>(p, w.s, lo);
-    w.measure<SUBS>(p);
+    w.start += cost_before<SUBS, EXT>(p, w.s, lo);
+    w.measure<SUBS, EXT>(p);
     return w;
   }
   return w;
 }
 
+template <bool EXT>
 __device__ __forceinline__ PagedUnit paged_unit(const PagedParams& p, const PagedSeq& s, int b, int head, int block,
                                                 int i) {
   PagedUnit u;
@@ -342,6 +469,10 @@ __device__ __forceinline__ PagedUnit paged_unit(const PagedParams& p, const Page
   u.ntok = min(block, s.q_len - u.tok0);
   u.row0 = s.q0 + u.tok0;
   u.table = b * p.table_stride;
+  if constexpr (EXT) {
+    u.table = s.row * p.table_stride + s.page0;
+    paged_list(p, s, u.tok0, &u.sink_tiles, &u.skip);
+  }
   u.t_begin = u.t_end = 0;
   u.slot = -1;
   return u;
@@ -355,7 +486,7 @@ struct PagedWalk {
   long long lo, hi;   // the range
   int cta;
 
-  template <int SUBS>
+  template <int SUBS, bool EXT>
   __device__ __forceinline__ PagedUnit next(const PagedParams& p) {
     const int lane = threadIdx.x & 31;
     PagedUnit u;
@@ -363,7 +494,7 @@ struct PagedWalk {
     while (lo < hi && !u.valid) {
       const int from = at.tile(p, lo), to = at.tile(p, hi);
       if (from < to) {
-        u = paged_unit(p, at.s, at.b, at.head, p.sub_tokens * SUBS, at.i);
+        u = paged_unit<EXT>(p, at.s, at.b, at.head, p.sub_tokens * SUBS, at.i);
         u.t_begin = from;
         u.t_end = to;
         if (from > 0)
@@ -381,11 +512,11 @@ struct PagedWalk {
           at.head = 0;
           int b0 = at.b + 1;
           for (; b0 < p.B; b0 += 32) {
-            const PagedSeq s = paged_seq(p, b0 + lane, p.sub_tokens * SUBS);
+            const PagedSeq s = paged_seq<EXT>(p, b0 + lane, p.sub_tokens * SUBS);
             const unsigned some = __ballot_sync(0xffffffffu, s.blocks > 0);
             if (some != 0) {
               const int src = __ffs(some) - 1;
-              at.s = seq_from(s, src);
+              at.s = seq_from<EXT>(s, src);
               at.b = b0 + src;
               break;
             }
@@ -396,22 +527,22 @@ struct PagedWalk {
           }
         }
       }
-      at.measure<SUBS>(p);
+      at.measure<SUBS, EXT>(p);
     }
     return u;
   }
 };
 
-template <int SUBS>
+template <int SUBS, bool EXT>
 __device__ __forceinline__ PagedWalk paged_walk(const PagedParams& p, int cta) {
   PagedWalk w;
   long long total;
-  const PagedStrips f = paged_strips<SUBS>(p);
-  const long long share = paged_share<SUBS>(p, f, &total);
+  const PagedStrips f = paged_strips<SUBS, EXT>(p);
+  const long long share = paged_share<SUBS, EXT>(p, f, &total);
   w.cta = cta;
   w.lo = cta * share;
   w.hi = cta < p.ctas ? min(w.lo + share, total) : w.lo;
-  if (w.lo < w.hi) w.at = paged_find<SUBS>(p, f, w.lo);
+  if (w.lo < w.hi) w.at = paged_find<SUBS, EXT>(p, f, w.lo);
   return w;
 }
 
@@ -424,19 +555,19 @@ struct PagedParts {
 
 // Whole warp: the item that the boundary between the ranges `index` and `index`
 // + 1 cuts, when it is the first boundary to do so; otherwise u.valid = 0.
-template <int SUBS>
+template <int SUBS, bool EXT>
 __device__ __forceinline__ PagedParts paged_parts_even(const PagedParams& p, int index) {
   PagedParts r;
   r.u.valid = 0;
   long long total;
-  const PagedStrips f = paged_strips<SUBS>(p);
-  const long long share = paged_share<SUBS>(p, f, &total);
+  const PagedStrips f = paged_strips<SUBS, EXT>(p);
+  const long long share = paged_share<SUBS, EXT>(p, f, &total);
   const long long pos = (index + 1ll) * share;
   if (index + 1 >= p.ctas || pos >= total) return r;
-  const PagedPlace w = paged_find<SUBS>(p, f, pos);
+  const PagedPlace w = paged_find<SUBS, EXT>(p, f, pos);
   const int t = w.tile(p, pos);
   if (t == 0 || t == w.tiles || w.tile(p, pos - share) > 0) return r;
-  r.u = paged_unit(p, w.s, w.b, w.head, p.sub_tokens * SUBS, w.i);
+  r.u = paged_unit<EXT>(p, w.s, w.b, w.head, p.sub_tokens * SUBS, w.i);
   r.first = 2 * index + 1;
   r.rest = 2 * (index + 1);
   r.step = 2;
@@ -447,37 +578,62 @@ __device__ __forceinline__ PagedParts paged_parts_even(const PagedParams& p, int
 
 // Whole warp: the page numbers of a sequence's tiles, in ascending order of the
 // tiles, 32 table entries at a time (one per lane) and the next 32 on their way.
+// EXT: entries are numbered in the list of tiles, one for a page of a tile, or for a tile within a page.
+template <bool EXT>
 struct PageCursor {
   const int* table;
   int live;        // table entries that hold keys
   int chunk0;      // first entry in `pages`
   int pages, pages_next;
+  int log2_tile;   // EXT: log2 of a tile's entries
+  int entries;     // EXT: entries of the unit
+  int lo;          // EXT: first key of the block's windows
+  const PagedUnit* unit;
 
   __device__ __forceinline__ PageCursor(const PagedParams& p, const PagedUnit& w, int tiles) {
     table = p.page_table + (tiles > 0 ? w.table : 0);
     live = tiles > 0 ? (w.kv_len + (1 << p.page_log2) - 1) >> p.page_log2 : 0;
-    chunk0 = tiles > 0 ? (w.t_begin << 7) >> p.page_log2 : 0;
+    if constexpr (EXT) {
+      unit = &w;
+      log2_tile = max(0, 7 - p.page_log2);
+      entries = tiles > 0 ? (w.t_begin + tiles) << log2_tile : 0;
+      lo = w.kv_len - w.q_len + w.tok0 - p.window + 1;
+      chunk0 = tiles > 0 ? w.t_begin << log2_tile : 0;
+    } else {
+      chunk0 = tiles > 0 ? (w.t_begin << 7) >> p.page_log2 : 0;
+    }
     pages = fetch(p, chunk0);
     pages_next = fetch(p, chunk0 + 32);
   }
   __device__ __forceinline__ int fetch(const PagedParams& p, int first) const {
-    const int i = first + (threadIdx.x & 31);
+    int i = first + (threadIdx.x & 31);
     int id = 0;
+    if constexpr (EXT) {
+      if (i >= entries) return id;
+      i = page(p, i);
+      const int begin = i << p.page_log2;
+      if (begin + (1 << p.page_log2) <= lo && begin >= p.sinks) return p.num_pages;   // nobody sees it: zeros
+    }
     if (i < live) {
       id = table[i];
       if (id < 0 || id >= p.num_pages) atomicOr(p.status, kDevErrPage);
     }
     return id;
   }
+  // EXT: the page (number in the sequence) of an entry
+  __device__ __forceinline__ int page(const PagedParams& p, int entry) const {
+    const int t = unit->template tile<true>(entry >> log2_tile);
+    return p.page_log2 <= 7 ? (t << log2_tile) + (entry & ((1 << log2_tile) - 1)) : t >> (p.page_log2 - 7);
+  }
   // lane x: the tile's x-th page; *count: how many there are
   __device__ __forceinline__ int tile(const PagedParams& p, int t, int* count) {
-    const int first = (t << 7) >> p.page_log2;
+    const int first = EXT ? t << log2_tile : (t << 7) >> p.page_log2;
     if (first >= chunk0 + 32) {
       chunk0 += 32;
       pages = pages_next;
       pages_next = fetch(p, chunk0 + 32);
     }
-    *count = min(kKeysPerTile >> min(p.page_log2, 7), live - first);
+    *count = min(kKeysPerTile >> min(p.page_log2, 7), live - (EXT ? page(p, first) : first));
     return __shfl_sync(0xffffffffu, pages, (first - chunk0 + (threadIdx.x & 31)) & 31);
   }
 };
@@ -488,14 +644,14 @@ constexpr long long kPagedL2Bytes = 64ll << 20;
 // Whole warp, items from a counter: unit `index` (items = false), or the item of
 // rank `index` among those cut into several units (items = true; its parts are
 // in slots first, first + 1, ...).
-template <int SUBS>
+template <int SUBS, bool EXT>
 __device__ __forceinline__ PagedParts paged_item(const PagedParams& p, int index, bool items, int D) {
   const int lane = threadIdx.x & 31;
   const int block = p.sub_tokens * SUBS;
   long long total = 0;
   for (int b = lane; b < p.B; b += 32) {
-    const PagedSeq s = paged_seq(p, b, block);
-    total += static_cast<long long>(s.blocks) * key_tiles_of(s.kv_len);
+    const PagedSeq s = paged_seq<EXT>(p, b, block);
+    total += static_cast<long long>(s.blocks) * key_tiles_of(EXT ? min(s.kv_len, p.most_keys) : s.kv_len);
   }
   total = warp_sum(total) * p.Hkv;
   const int per_unit = static_cast<int>(
@@ -506,8 +662,8 @@ __device__ __forceinline__ PagedParts paged_item(const PagedParams& p, int index
   r.step = 1;
   int before = 0, slots_before = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const PagedSeq q = paged_seq(p, b0 + lane, block);
-    const int tiles = key_tiles_of(q.kv_len);
+    const PagedSeq q = paged_seq<EXT>(p, b0 + lane, block);
+    const int tiles = key_tiles_of(EXT ? min(q.kv_len, p.most_keys) : q.kv_len);
     const int s = max(1, (tiles + per_unit - 1) / per_unit);
     const int blocks = q.blocks * p.Hkv;
     const int slots = s > 1 ? blocks * s : 0;
@@ -519,7 +675,7 @@ __device__ __forceinline__ PagedParts paged_item(const PagedParams& p, int index
       const int src = __ffs(here) - 1;
       auto get = [&](int v) { return __shfl_sync(0xffffffffu, v, src); };
       const int splits = get(s), all_tiles = get(tiles);
-      const PagedSeq seq = seq_from(q, src);
+      const PagedSeq seq = seq_from<EXT>(q, src);
       int in = at - get(sum - count);
       if (items) in *= splits;
       const int slot = slots_before + get(slot_sum - slots) + in;
@@ -535,7 +691,7 @@ __device__ __forceinline__ PagedParts paged_item(const PagedParams& p, int index
       const int rank = in / per_block;
       in -= rank * per_block;
       const int h = in / splits, split = in - h * splits;
-      r.u = paged_unit(p, seq, b0 + src, group * hg + h, block, seq.blocks - 1 - rank);
+      r.u = paged_unit<EXT>(p, seq, b0 + src, group * hg + h, block, seq.blocks - 1 - rank);
       r.u.t_begin = split * per_unit;
       r.u.t_end = min(all_tiles, r.u.t_begin + per_unit);
       if (splits > 1) r.u.slot = slot;
@@ -596,7 +752,7 @@ struct alignas(8) PagedShared {
 // Counters that run on over a CTA's segments: `base` K/V copies (two per key
 // tile, in order K, V), `done[sub]` tiles of a sub-tile, `loads` segments that
 // loaded Q.  A barrier's phase is taken from them.
-template <int D, bool F16, int SUBS, bool NARROW>
+template <int D, bool F16, int SUBS, bool NARROW, bool EXT = false>
 __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCtasPerSm)
     fa2_paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedParams p) {
@@ -629,7 +785,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
     if (first >= w.ntok) return 0;
     const int last = min(first + p.sub_tokens, w.ntok) - 1;
     const int kept = paged_kept(p.causal, w.kv_len, w.q_len, w.tok0 + last);
-    return max(0, min(w.t_end, key_tiles_of(kept)) - w.t_begin);
+    return max(0, min(w.t_end, key_tiles_of(kept) - (EXT ? w.skip : 0)) - w.t_begin);
   };
 
   // ---- the producers' copies; whole warps, `ok` is cleared after an abort
@@ -642,14 +798,14 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
   // key tile `tile`, which lies at or behind the cursor.  Everything is ready
   // before the wait for the slot: instructions after it delay every tile.
   int last[2] = {-1, -1};   // this warp's last copies of K and of V
-  auto copy = [&](auto C0, auto C1, const PagedUnit& w, PageCursor& pages, int tile, int index, bool& ok) {
+  auto copy = [&](auto C0, auto C1, const PagedUnit& w, PageCursor<EXT>& pages, int tile, int index, bool& ok) {
     constexpr int kFirst = decltype(C0)::value, kEnd = decltype(C1)::value;
     const int slot = index % STAGES, lap = index / STAGES;
     const int slots_log2 = min(p.page_log2, 7);   // slots of a page that the tile reads
     int count;
     const int id = pages.tile(p, tile, &count);
     const CUtensorMap* map = (index & 1) == 0 ? &tm_k : &tm_v;
-    const int row = (tile << 7) & ((1 << p.page_log2) - 1);
+    const int row = (w.tile<EXT>(tile) << 7) & ((1 << p.page_log2) - 1);
     uint8_t* dst = sKV + slot * TILE + (static_cast<uint32_t>(lane) << slots_log2) * 128;
     const uint32_t bytes = static_cast<uint32_t>(count * (kEnd - kFirst)) * (128u << slots_log2);
     if (lap > 0) warp_wait(&bars->kv_empty[slot], (lap - 1) & 1, ok);
@@ -666,8 +822,8 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
   };
   // Three producers: their chunks of K and of V.  In the order of the MMAs: K(j+1),
   // whose slot S(j) frees, then V(j), whose slot P(j-1) V frees.
-  auto copy_three = [&](auto K0, auto K1, auto V0, auto V1, const PagedUnit& w, int n, int tiles, PageCursor& k_pages,
-                        PageCursor& v_pages, int first, bool& ok) {
+  auto copy_three = [&](auto K0, auto K1, auto V0, auto V1, const PagedUnit& w, int n, int tiles, PageCursor<EXT>& k_pages,
+                        PageCursor<EXT>& v_pages, int first, bool& ok) {
     for (int j = first; j <= n && ok; ++j) {
       if (j < n) copy(K0, K1, w, k_pages, w.t_begin + j, 2 * (tiles + j), ok);
       if (j > 0 && ok) copy(V0, V1, w, v_pages, w.t_begin + j - 1, 2 * (tiles + j) - 1, ok);
@@ -715,7 +871,12 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
 
   // The grid before this one is complete from here on; behind that, the merge may
   // start (it finds its items and then waits for this grid to end).
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // EXT, a sequence's own pages: the kernel before is that of the shared prefix, whose
+  // results this one does not read, and which started behind its own wait: the two
+  // run side by side, and this one waits for the other at its end (all of whose
+  // blocks are running by then).
+  const bool beside = EXT && p.role == kPagedOwn;
+  if (!beside) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp >= kWarpProducer) {
@@ -726,16 +887,16 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
       PagedWalk walk;
       bool begun = false;
       auto next_unit = [&]() {
-        if (NARROW || p.even) return walk.next<SUBS>(p);   // (narrow blocks always have equal ranges)
+        if (NARROW || p.even) return walk.next<SUBS, EXT>(p);   // (narrow blocks always have equal ranges)
         int index = blockIdx.x;   // the first unit by number, the others as CTAs become free
         if (begun) {
           if (lane == 0) index = gridDim.x + atomicAdd(p.counter, 1);
           index = __shfl_sync(0xffffffffu, index, 0);
         }
         begun = true;
-        return paged_item<SUBS>(p, index, false, D).u;
+        return paged_item<SUBS, EXT>(p, index, false, D).u;
       };
-      if (NARROW || p.even) walk = paged_walk<SUBS>(p, static_cast<int>(blockIdx.x));
+      if (NARROW || p.even) walk = paged_walk<SUBS, EXT>(p, static_cast<int>(blockIdx.x));
       PagedUnit w = next_unit();
       int tiles = 0, loads = 0;   // tiles of the segments before; Q loads
       bool ok = true;
@@ -748,7 +909,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
           n = tiles_for(w, 0);
           if (SUBS == 2) n = max(n, tiles_for(w, 1));
         }
-        PageCursor pages(p, w, n);
+        PageCursor<EXT> pages(p, w, n);
         // Ahead of the hand-over: the first copies, which do not wait for the
         // last V of the segment before (its slot comes STAGES - 1 copies
         // later), and Q, once the last S of the segment before is complete.
@@ -783,7 +944,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
         named_sync(kBarSegment, Cfg::kSegmentThreads);
         if (!w.valid) break;
         if constexpr (Cfg::kThree) {
-          PageCursor v_pages(p, w, n);
+          PageCursor<EXT> v_pages(p, w, n);
           copy_three(Int<0>{}, Int<2>{}, Int<0>{}, Int<1>{}, w, n, tiles, pages, v_pages, 1, ok);
         } else {
           for (int i = early; i < 2 * n && ok; ++i)
@@ -808,9 +969,9 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
         if (!w.valid) break;
         int n = tiles_for(w, 0);
         if (SUBS == 2) n = max(n, tiles_for(w, 1));
-        PageCursor pages(p, w, n);
+        PageCursor<EXT> pages(p, w, n);
         if constexpr (Cfg::kThree) {
-          PageCursor v_pages(p, w, n);
+          PageCursor<EXT> v_pages(p, w, n);
           if (warp == kWarpMma + 1)
             copy_three(Int<2>{}, Int<3>{}, Int<1>{}, Int<3>{}, w, n, tiles, pages, v_pages, 0, ok);
           else
@@ -1006,6 +1167,9 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
       const int lim = live ? paged_kept(p.causal, kv_len, w.q_len, w.tok0 + sub_tok0 + tok) : 0;
       // every live row keeps at least the first token's keys
       const int lim_min = paged_kept(p.causal, kv_len, w.q_len, w.tok0 + sub_tok0);
+      // EXT: keys below this one may lie outside some live row's window
+      const int low_max =
+          EXT ? paged_kept(p.causal, kv_len, w.q_len, w.tok0 + min(sub_tok0 + p.sub_tokens, w.ntok) - 1) - p.window : 0;
 
       // One thread of the sub-tile that visits every key tile releases the ring slots.
       const bool releaser = (threadIdx.x & (kRowsPerSub - 1)) == 0 && n_tiles == nmax && n_tiles > 0 &&
@@ -1027,7 +1191,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
           if (j > 0) bar_arrive(&bars->kv_empty[(base + 2 * j - 1) % STAGES]);
           bar_arrive(&bars->kv_empty[(base + 2 * j) % STAGES]);
         }
-        const int key0 = (t_begin + j) * kKeysPerTile;
+        const int key0 = w.tile<EXT>(t_begin + j) * kKeysPerTile;
         // V rows behind the last key: zeros, written by the first sub-tile that reads them
         if (key0 + kKeysPerTile > kv_len && (sub == 0 || j >= n0)) {
           const int tid = wq * 32 + lane;
@@ -1058,7 +1222,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
           const int first = key0 + (NARROW ? wq * 32 : 0);
           const uint32_t tMine = tS + (NARROW ? wq * 32 : 0);
           uint32_t s[kChunks][32];
-          const bool masked = key0 + kKeysPerTile > lim_min;
+          const bool masked = key0 + kKeysPerTile > lim_min || (EXT && key0 < low_max && key0 + kKeysPerTile > p.sinks);
           auto load_s = [&]() {
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) tmem_ld32(tMine + c * 32, s[c]);
@@ -1067,10 +1231,19 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
             for (int c = 1; c < kChunks; ++c) regs_after_wait(s[c]);
             if (masked) {
 #pragma unroll
-              for (int c = 0; c < kChunks; ++c)
+              for (int c = 0; c < kChunks; ++c) {
+                if constexpr (EXT) {
+                  const int at = first + c * 32;
+                  const uint32_t keep = low_bits(lim - at) & (~low_bits(lim - p.window - at) | low_bits(p.sinks - at));
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (first + c * 32 + e >= lim) s[c][e] = __float_as_uint(-INFINITY);
+                  for (int e = 0; e < 32; ++e)
+                    if (!(keep >> e & 1u)) s[c][e] = __float_as_uint(-INFINITY);
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    if (first + c * 32 + e >= lim) s[c][e] = __float_as_uint(-INFINITY);
+                }
+              }
             }
           };
           // the row max, and the offset moved to it when it exceeds it by more than kRescaleLog2
@@ -1365,6 +1538,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
   }
 
   // ------------------------------------------------------------ teardown
+  if (beside) asm volatile("griddepcontrol.wait;" ::: "memory");
   tc_fence_before_sync();
   __syncthreads();
   if (warp == kWarpMma) {
@@ -1384,12 +1558,12 @@ constexpr int kPagedMergeMany = 6;    // parts from which the warps of a block s
 // parts with L_s = -inf have w_s = 0 and their O is not used.  An item of many
 // parts has few rows (it was cut because there were few items): its block's
 // warps take every fourth part each and add up through shared memory.
-template <int D, bool F16, int SUBS>
+template <int D, bool F16, int SUBS, bool EXT = false>
 __global__ void __launch_bounds__(kPagedMergeWarps * 32) fa2_paged_merge_kernel(const __grid_constant__ PagedParams p) {
   __shared__ float4 sums[kPagedMergeWarps - 1][D / 16][32];
   __shared__ float2 weights[kPagedMergeWarps - 1][32];
   const int index = static_cast<int>(blockIdx.x);
-  const PagedParts w = p.even ? paged_parts_even<SUBS>(p, index) : paged_item<SUBS>(p, index, true, D);
+  const PagedParts w = p.even ? paged_parts_even<SUBS, EXT>(p, index) : paged_item<SUBS, EXT>(p, index, true, D);
   // launched while the partial results are computed: they are complete from here on
   // (what was read above the kernel before this one does not write, and that one lets
   // this one start behind its own wait for what came before it)

@@ -59,7 +59,9 @@ def _load():
             "fa2_forward_paged", "fa2_forward_paged_workspace_bytes", "fa2_rope", "fa2_append_paged",
             "fa2_pages_workspace_bytes", "fa2_pages_reserve", "fa2_pages_fork", "fa2_pages_free", "fa2_pages_compact",
             "fa2_pages_copy", "fa2_append_paged_norm", "fa2_norm_rope", "fa2_norm_rope_backward",
-            "fa2_norm_rope_backward_workspace_bytes")))
+            "fa2_norm_rope_backward_workspace_bytes", "fa2_forward_paged_window", "fa2_forward_paged_prefix",
+            "fa2_forward_paged_prefix_workspace_bytes", "fa2_forward_window", "fa2_backward_window",
+            "fa2_backward_window_workspace_bytes")))
         _fast = _binding
     _codes = fa2._dtype_codes()
     _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None) or (lambda i: t.cuda.current_stream(i).cuda_stream)
@@ -198,6 +200,14 @@ def forward_paged(q, k_pages, v_pages, page_table, kv_lens, cu_q=None, causal: b
         r = _fast.forward_paged(q, k_pages, v_pages, page_table, kv_lens, cu_q, causal, scale)
         if r is not None:
             return _answer(r, "fa2_forward_paged")
+    return _attend("fa2_forward_paged", (1 if causal else 0,), _paged_workspace_bytes, (), q, k_pages, v_pages, page_table,
+                   kv_lens, cu_q, scale, out, lse, out_dtype, workspace, stream)
+
+
+def _attend(name, own, workspace_bytes, workspace_sizes, q, k_pages, v_pages, page_table, kv_lens, cu_q, scale, out, lse,
+            out_dtype, workspace, stream):
+    """One of the attention calls over a cache: ``own`` are its arguments between Hq and scale, ``workspace_sizes``
+    those of its workspace behind B."""
     dtype, device = k_pages.dtype, k_pages.device
     args = _cache_args(k_pages, v_pages, page_table, kv_lens, device, dtype)
     shape = q.shape
@@ -225,16 +235,78 @@ def forward_paged(q, k_pages, v_pages, page_table, kv_lens, cu_q=None, causal: b
               or lse.device != device):
             raise ValueError(f"lse must be a contiguous fp32 tensor of shape {(T, Hq)} on {device}")
         if workspace is None:
-            size = _paged_workspace_bytes(device.index, args.B, T, Hq, args.kv_heads, d, offsets is not None)
+            size = workspace_bytes(device.index, args.B, *workspace_sizes, T, Hq, args.kv_heads, d, offsets is not None)
             workspace = torch.empty(max(size, 1), dtype=torch.uint8, device=device)
         else:
             size = _workspace_size(workspace, device)
-        rc = _lib.fa2_forward_paged(ctypes.byref(args), q.data_ptr(), strides[0], strides[1], out.data_ptr(),
-                                    lse.data_ptr(), offsets, T, Hq, 1 if causal else 0, scale, _codes[out_dtype],
-                                    workspace.data_ptr(), size, handle)
+        rc = getattr(_lib, name)(ctypes.byref(args), q.data_ptr(), strides[0], strides[1], out.data_ptr(),
+                                 lse.data_ptr(), offsets, T, Hq, *own, scale, _codes[out_dtype], workspace.data_ptr(),
+                                 size, handle)
     if rc:
-        _fail(rc, "fa2_forward_paged")
+        _fail(rc, name)
     return out, lse
+
+
+def forward_paged_window(q, k_pages, v_pages, page_table, kv_lens, window: int, sinks: int = 0, cu_q=None,
+                         scale: float | None = None, out=None, lse=None, out_dtype=None, workspace=None, stream=None):
+    """``forward_paged`` (causal) with a window (fa2_forward_paged_window).
+
+    A token at position p sees the keys j <= p with p - j < window (its own among
+    them) or j < sinks.  Pages that no new token sees are not read, nor their
+    table entries: they may have been freed.  The other arguments and the
+    workspace are ``forward_paged``'s.
+    """
+    if torch is None:
+        _load()
+    # a window or sinks beyond every length are all of them
+    window, sinks = min(int(window), (1 << 31) - 1), min(int(sinks), (1 << 31) - 1)
+    if window < 1 or sinks < 0:
+        raise ValueError("window must be at least 1, sinks not negative")
+    if (_fast is not None and out is None and lse is None and out_dtype is None and workspace is None
+            and stream is None):
+        r = _fast.forward_paged_window(q, k_pages, v_pages, page_table, kv_lens, cu_q, window, sinks, scale)
+        if r is not None:
+            return _answer(r, "fa2_forward_paged_window")
+    return _attend("fa2_forward_paged_window", (window, sinks), _paged_workspace_bytes, (), q, k_pages, v_pages,
+                   page_table, kv_lens, cu_q, scale, out, lse, out_dtype, workspace, stream)
+
+
+@functools.lru_cache(maxsize=1024)
+def _prefix_workspace_bytes(device_index, *sizes):
+    with torch.cuda.device(device_index):
+        return _lib.fa2_forward_paged_prefix_workspace_bytes(*sizes)
+
+
+def forward_paged_prefix(q, k_pages, v_pages, page_table, kv_lens, cu_groups, prefix_lens, cu_q=None,
+                         causal: bool = True, scale: float | None = None, out=None, lse=None, out_dtype=None,
+                         workspace=None, stream=None):
+    """``forward_paged`` for sequences that share prefixes (fa2_forward_paged_prefix).
+
+    Group g is the sequences ``cu_groups[g]`` .. ``cu_groups[g + 1]`` - 1 (int32
+    [groups + 1]); their first ``prefix_lens[g]`` tokens (int32 [groups]) lie in
+    the same pages, as ``pages_fork`` leaves them, before all new tokens.  Their keys
+    are read once for the group.  The part of a prefix behind its last whole
+    page is read from each sequence's own pages.  The other arguments are
+    ``forward_paged``'s; so are the results, but for the order of the sums.
+    """
+    if torch is None:
+        _load()
+    if (_fast is not None and out is None and lse is None and out_dtype is None and workspace is None
+            and stream is None):
+        r = _fast.forward_paged_prefix(q, k_pages, v_pages, page_table, kv_lens, cu_q, cu_groups, prefix_lens, causal,
+                                       scale)
+        if r is not None:
+            return _answer(r, "fa2_forward_paged_prefix")
+    device = k_pages.device
+    if prefix_lens.dim() != 1:
+        raise ValueError("prefix_lens must be 1-D")
+    groups = prefix_lens.shape[0]
+    _ints("prefix_lens", prefix_lens, (groups,), device)
+    _ints("cu_groups", cu_groups, (groups + 1,), device)
+    own = (cu_groups.data_ptr(), prefix_lens.data_ptr(), groups, 1 if causal else 0)
+    return _attend("fa2_forward_paged_prefix", own, _prefix_workspace_bytes if groups else _paged_workspace_bytes,
+                   (groups,) if groups else (), q, k_pages, v_pages, page_table, kv_lens, cu_q, scale, out, lse, out_dtype,
+                   workspace, stream)
 
 
 def _workspace_size(workspace, device):

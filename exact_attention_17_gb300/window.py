@@ -8,7 +8,7 @@ does.
 from __future__ import annotations
 
 from . import paged
-from .paged import _Call, _default_scale, _fail, _sizes, _workspace_size
+from .paged import _answer, _Call, _default_scale, _fail, _sizes, _workspace_size
 
 
 def _dense(name, t, shape, dtype, device):
@@ -19,6 +19,14 @@ def _dense(name, t, shape, dtype, device):
 
 def _output(name, t, shape, dtype, device):
     return paged.torch.empty(shape, dtype=dtype, device=device) if t is None else _dense(name, t, shape, dtype, device)
+
+
+def _reach(window, sinks):
+    """As C ints: a window or sinks beyond every length are all of them."""
+    window, sinks = min(int(window), (1 << 31) - 1), min(int(sinks), (1 << 31) - 1)
+    if window < 1 or sinks < 0:
+        raise ValueError("window must be at least 1, sinks not negative")
+    return window, sinks
 
 
 def _arguments(q, k, v, window, sinks, scale):
@@ -35,10 +43,6 @@ def _arguments(q, k, v, window, sinks, scale):
         _dense(name, t, (B, Hkv, Nk, d), q.dtype, q.device)
     if (H % Hkv if Hkv else H) != 0:
         raise ValueError(f"{H} query heads are no multiple of {Hkv} key/value heads")
-    # a window or sinks beyond every length are all of them
-    window, sinks = min(int(window), (1 << 31) - 1), min(int(sinks), (1 << 31) - 1)
-    if window < 1 or sinks < 0:
-        raise ValueError("window must be at least 1, sinks not negative")
     _sizes(B, H, Hkv, Nq, Nk, d)
     return (B, H, Hkv, Nq, Nk, d, window, sinks), _default_scale(d) if scale is None else scale
 
@@ -55,6 +59,13 @@ def forward_window(q, k, v, window: int, sinks: int = 0, scale: float | None = N
     """
     if paged.torch is None:
         paged._load()
+    window, sinks = _reach(window, sinks)
+    if paged._fast is not None and out is None and lse is None and stream is None:
+        half = out_dtype is not None and out_dtype is not paged.torch.float32
+        if not half or out_dtype is q.dtype:
+            r = paged._fast.forward_window(q, k, v, window, sinks, scale, half)
+            if r is not None:
+                return _answer(r, "fa2_forward_window")
     sizes, scale = _arguments(q, k, v, window, sinks, scale)
     torch, device = paged.torch, q.device
     out_dtype = torch.float32 if out_dtype is None else out_dtype
@@ -82,6 +93,13 @@ def backward_window(q, k, v, o, lse, do, window: int, sinks: int = 0, scale: flo
     """
     if paged.torch is None:
         paged._load()
+    window, sinks = _reach(window, sinks)
+    if paged._fast is not None and dq is None and dk is None and dv is None and workspace is None and stream is None:
+        half = grad_dtype is not None and grad_dtype is not paged.torch.float32
+        if not half or grad_dtype is q.dtype:
+            r = paged._fast.backward_window(q, k, v, o, lse, do, window, sinks, scale, half)
+            if r is not None:
+                return _answer(r, "fa2_backward_window")
     sizes, scale = _arguments(q, k, v, window, sinks, scale)
     torch, device = paged.torch, q.device
     grad_dtype = torch.float32 if grad_dtype is None else grad_dtype

@@ -410,6 +410,45 @@ int fa2_forward_paged(const fa2_paged_cache *cache, const void *Q, long long q_t
 size_t fa2_forward_paged_workspace_bytes(int B, int T, int Hq, int kv_heads, int d, int has_cu_q);
 
 /*
+ * fa2_forward_paged (causal) with a window: a token at position p sees the keys j <=
+ * p with p - j < window or j < sinks.  Pages without a key that some row of a block of
+ * queries sees are not read, and their table entries are not looked at: pages
+ * that every new token's window has left behind (and that hold no sinks) may have been
+ * given to others.  window >= 1, sinks >= 0; the workspace is fa2_forward_paged's.
+ */
+int fa2_forward_paged_window(const fa2_paged_cache *cache, const void *Q, long long q_token_stride,
+                             long long q_head_stride, void *O, float *LSE, const int *cu_q, int T,
+                             int Hq, int window, int sinks, float scale, int o_dtype,
+                             void *workspace, size_t workspace_size, fa2_stream_t stream);
+
+/*
+ * fa2_forward_paged for sequences that share prefixes (as fa2_pages_fork makes them):
+ * the shared pages are read once for a group instead of once for each sequence.
+ * Group g is the sequences cu_groups[g] .. cu_groups[g+1]-1, whose first prefix_lens[g]
+ * tokens lie in the same pages (those of the group's first sequence are read) and come
+ * before the new ones: prefix_lens[g] <= kv_lens[b] - c_b.  Of a prefix the whole pages count,
+ * the rest is read from each sequence's own; a group of one sequence shares nothing,
+ * and neither do sequences outside all groups.  The results are those of fa2_forward_paged but
+ * for the rounding order of the sums: a row's prefix and own part are computed apart (P rounded
+ * in each), kept in fp32 and joined as fa2_merge does.
+ *   cu_groups    device int32 [groups + 1], ascending, within 0 .. B
+ *   prefix_lens  device int32 [groups]
+ *   groups       0 .. B (0: fa2_forward_paged)
+ *   workspace    at least fa2_forward_paged_prefix_workspace_bytes
+ * Groups out of order, lengths outside the table and prefixes that reach into a
+ * sequence's new tokens are reported (FA2_ERR_PAGE); the rows concerned are undefined.
+ */
+int fa2_forward_paged_prefix(const fa2_paged_cache *cache, const void *Q, long long q_token_stride,
+                             long long q_head_stride, void *O, float *LSE, const int *cu_q, int T,
+                             int Hq, const int *cu_groups, const int *prefix_lens, int groups,
+                             int causal, float scale, int o_dtype, void *workspace,
+                             size_t workspace_size, fa2_stream_t stream);
+
+/* Workspace of fa2_forward_paged_prefix on the current device; 0 for invalid arguments or an empty problem. */
+size_t fa2_forward_paged_prefix_workspace_bytes(int B, int groups, int T, int Hq, int kv_heads, int d,
+                                                int has_cu_q);
+
+/*
  * Rotary positions.  Pair i of the first rotary_dim columns of the row at
  * position t -- columns (i, i + rotary_dim / 2), or (2i, 2i + 1) when
  * interleaved -- becomes

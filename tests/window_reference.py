@@ -75,3 +75,25 @@ def backward(q, k, v, do, mask, scale, o_eps, grad_eps):
     grads = scale * (ds @ kk), scale * group(t(ds) @ x), group(t(p) @ g)
     bounds = scale * (err_ds @ kk.abs()), scale * group(t(err_ds) @ x.abs()), group(t(err_p) @ g.abs())
     return grads, [b * (1 + 2 * grad_eps) + grad_eps * a.abs() + 2.0 ** -25 for a, b in zip(grads, bounds)]
+
+
+def paged(q, keys, values, q_lens, masks, scale, out_eps, parts=1):
+    """Packed queries [T, Hq, d] over each sequence's keys [n, Hkv, d] under its mask [new tokens, n]: (O, LSE, bounds).
+
+    With `parts` > 1 a row's result is joined from parts whose sums carry `rel` each, as do their weights.
+    """
+    out, at = [], 0
+    for n, k, v, mask in zip(q_lens, keys, values, masks):
+        heads = lambda t: t.transpose(0, 1)[None]  # noqa: E731
+        if k.shape[0] == 0:   # one key that nobody sees
+            k, v, mask = k.new_zeros(1, *k.shape[1:]), v.new_zeros(1, *v.shape[1:]), mask.new_zeros(n, 1)
+        if n:
+            o, lse, bO, bL, _, rel = forward(heads(q[at:at + n]), heads(k), heads(v), mask, scale, out_eps)
+            A = (bO - out_eps * o.abs()) / (EPS[q.dtype] + rel[..., None])   # (at least sum p |v|)
+            bO = bO + 2 * (parts - 1) * rel[..., None] * A
+            out.append([t[0].transpose(0, 1) for t in (o, lse, bO, bL * parts)])
+        at += n
+    d, H = q.shape[2], q.shape[1]
+    if not out:
+        return [torch.zeros(s, dtype=torch.float64, device=q.device) for s in ((0, H, d), (0, H), (0, H, d), (0, H))]
+    return [torch.cat(t) for t in zip(*out)]
