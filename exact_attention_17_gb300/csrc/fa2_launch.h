@@ -120,20 +120,16 @@ cudaError_t launch_paged_bf16(int d, int subs, const CUtensorMap& mq, const CUte
 cudaError_t launch_paged_f16(int d, int subs, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                              const fa2dev::PagedParams& p, unsigned grid, dim3 merge_grid, cudaStream_t s);
 
-// The same with windows or shared prefixes (fa2_paged_ext_bf16.cu, fa2_paged_ext_f16.cu).  The merge alone
-// (grid 0), or the partial results alone (merge_grid.x 0).
+// The same with windows or shared prefixes (fa2_paged_ext_bf16.cu, fa2_paged_ext_f16.cu).
 cudaError_t prepare_paged_ext_bf16();
 cudaError_t prepare_paged_ext_f16();
 cudaError_t launch_paged_ext_bf16(int d, int subs, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                                   const fa2dev::PagedParams& p, unsigned grid, dim3 merge_grid, cudaStream_t s);
 cudaError_t launch_paged_ext_f16(int d, int subs, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                                  const fa2dev::PagedParams& p, unsigned grid, dim3 merge_grid, cudaStream_t s);
-// Shared prefixes: the groups' launch (0) and the sequences' own (1), side by side, their merges, and the kernel that
-// joins their results into O (half_out: in the input type) and LSE (fa2_paged_prefix.cu).
-cudaError_t launch_paged_prefix(int d, bool f16, int subs0, const CUtensorMap& mq0, const CUtensorMap& mk0,
-                                const CUtensorMap& mv0, const fa2dev::PagedParams& p0, dim3 merge0, int subs1,
-                                const CUtensorMap& mq1, const CUtensorMap& mk1, const CUtensorMap& mv1,
-                                const fa2dev::PagedParams& p1, dim3 merge1, void* O, float* LSE, bool half_out,
-                                cudaStream_t s);
+// Shared prefixes: behind the groups' launch (p0) and the sequences' own (p1), what joins their results into O
+// (half_out: in the input type) and LSE (fa2_paged_prefix.cu).
+cudaError_t launch_paged_join(int d, bool f16, const fa2dev::PagedParams& p0, int subs0, const fa2dev::PagedParams& p1,
+                              int subs1, void* O, float* LSE, bool half_out, cudaStream_t s);
 
 }  // namespace fa2host

@@ -223,9 +223,12 @@ int forward_paged(const PagedCall& a, int window, int sinks, cudaStream_t s) {
     // what lies beyond the longest sequence means the same as it
     p.window = window < p.max_len ? window : p.max_len;
     p.sinks = sinks < p.max_len ? sinks : p.max_len;
-    // tiles that hold sinks, and most that a block's windows reach over (n keys lie in at most (n + 126) / 128 + 1)
-    const long long tiles = (p.sinks + 127) / 128 + (static_cast<long long>(plan.sub_tokens) * plan.subs - 1 + p.window + 126) / 128 + 1;
-    if (tiles * 128 < p.most_keys) p.most_keys = static_cast<int>(tiles * 128);
+    // pages (tiles, where those are smaller) that hold sinks, and most that a block's windows reach over: n keys lie in
+    // at most (n + 2 unit - 2) / unit of them
+    const long long unit = c.page_size < 128 ? c.page_size : 128;
+    const long long reach = static_cast<long long>(plan.sub_tokens) * plan.subs - 1 + p.window;
+    const long long most = ((p.sinks + unit - 1) / unit + (reach + 2 * unit - 2) / unit) * unit;
+    if (most < p.most_keys) p.most_keys = static_cast<int>(most);
   }
   return launch(c.d, plan.subs, maps.q, maps.k, maps.v, p, static_cast<unsigned>(plan.ctas), merge_grid(plan), s) ==
                  cudaSuccess
@@ -263,11 +266,11 @@ extern "C" int fa2_forward_paged_window(const fa2_paged_cache* cache, const void
 
 namespace {
 
-// A call with shared prefixes: the groups' launch, the sequences' own, and what
-// joins their results.
+// A call with shared prefixes: the groups' launch, the sequences' own beside it, and
+// the kernel that joins their results.
 struct PrefixPlan {
   PagedPlan prefix, own;
-  size_t own_at, o_at[2], lse_at[2], bytes;   // workspace; O and LSE of the two launches in fp32
+  size_t own_at, o_at[2], lse_at[2], parts_at[2], bytes;   // workspace; O and LSE of the two launches in fp32
 };
 
 PrefixPlan plan_prefix(int B, int groups, int T, int Hq, int Hkv, int d, bool has_cu, int sms) {
@@ -283,6 +286,9 @@ PrefixPlan plan_prefix(int B, int groups, int T, int Hq, int Hkv, int d, bool ha
     at += align256(rows * d * 4);
     q.lse_at[i] = at;
     at += align256(rows * 4);
+    const PagedPlan& plan = i == 0 ? q.prefix : q.own;
+    q.parts_at[i] = at;
+    at += align256((static_cast<size_t>(T) / (plan.sub_tokens * plan.subs) + (i == 0 ? groups : B) + 1) * Hkv * sizeof(int4));
   }
   q.bytes = at;
   return q;
@@ -342,11 +348,19 @@ extern "C" int fa2_forward_paged_prefix(const fa2_paged_cache* cache, const void
     p[i].groups = groups;
     p[i].cu_groups = cu_groups;
     p[i].prefix_lens = prefix_lens;
+    p[i].parts = reinterpret_cast<int4*>(ws + plan.parts_at[i]);
   }
+  const long long join_blocks = (static_cast<long long>(T) * plan.own.G + 7) / 8;
+  if (join_blocks > 0x7fffffffll || c.kv_heads > 65535) return FA2_ERR_SHAPE;
   const bool f16 = c.dtype == FA2_DTYPE_FP16;
-  return fa2host::launch_paged_prefix(c.d, f16, plan.prefix.subs, maps[0].q, maps[0].k, maps[0].v, p[0],
-                                      merge_grid(plan.prefix), plan.own.subs, maps[1].q, maps[1].k, maps[1].v, p[1],
-                                      merge_grid(plan.own), O, LSE, o_dtype != FA2_DTYPE_FP32, s) == cudaSuccess
+  const auto launch = f16 ? fa2host::launch_paged_ext_f16 : fa2host::launch_paged_ext_bf16;
+  const dim3 no_merge(0);
+  return launch(c.d, plan.prefix.subs, maps[0].q, maps[0].k, maps[0].v, p[0], static_cast<unsigned>(p[0].ctas), no_merge,
+                s) == cudaSuccess &&
+                 launch(c.d, plan.own.subs, maps[1].q, maps[1].k, maps[1].v, p[1], static_cast<unsigned>(p[1].ctas),
+                        no_merge, s) == cudaSuccess &&
+                 fa2host::launch_paged_join(c.d, f16, p[0], plan.prefix.subs, p[1], plan.own.subs, O, LSE,
+                                            o_dtype != FA2_DTYPE_FP32, s) == cudaSuccess
              ? FA2_OK
              : FA2_ERR_LAUNCH;
 }

@@ -19,9 +19,8 @@ cudaError_t run(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap&
   const auto kernel = fa2dev::fa2_paged_tc_kernel<D, kF16, SUBS, NARROW, true>;
   constexpr int kThreads = fa2dev::FwdShape<SUBS>::kThreads;
   constexpr unsigned kSmem = fa2dev::PagedConfig<D, SUBS>::kSmemBytes;
-  cudaError_t e = cudaSuccess;
-  if (grid == 0) {   // the merge alone
-  } else if (p.even) {
+  cudaError_t e;
+  if (p.even) {
     e = launch_behind(kernel, dim3(grid), kThreads, kSmem, s, mq, mk, mv, p);
   } else {   // (behind the counter's memset)
     kernel<<<grid, kThreads, kSmem, s>>>(mq, mk, mv, p);

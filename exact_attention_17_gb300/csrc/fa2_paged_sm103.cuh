@@ -62,13 +62,14 @@
 //
 //  * Windows, shared prefixes (EXT; the other kernels do not have their code).  With
 //    a window a token at position t sees the keys j <= t with t - j < window or j <
-//    sinks.  The tiles of a block are those with sinks and those from its first
-//    token's window on: a list with one gap, whose numbers the schedule and the
-//    pipeline count in; only the copies and the masks look up which tile of the keys it
-//    is.  A page without a key that some row of the block sees is not read (its number
-//    may be anything: zeros are copied from outside the pool).  The cost of a block is
-//    that of its keys, at most the longest list there can be, so that sums of
-//    costs stay closed forms.
+//    sinks.  The keys of a block are the pages with sinks and those from its first
+//    token's window on (tiles, where pages are larger), one after the other: a list
+//    with one gap, whose tiles the schedule and the pipeline count in; only the
+//    copies and the masks look up which key it is.  Pages without a key that some row of
+//    the block sees are not in it.  (Whole tiles on both sides of the gap: 64 single
+//    tokens, window 2048 and 4 sinks in pages of 16, 101 us, see below.)  The cost of
+//    a block is that of its keys, at most the longest list there can be, so that
+//    sums of costs stay closed forms.
 //    With a shared prefix one launch has the groups of sequences as its sequences (all
 //    their new tokens over the shared pages, without a mask) and the next the sequences
 //    over their own pages; see fa2_paged_api.cu.
@@ -132,13 +133,16 @@ struct PagedParams {
   int groups;
   const int* cu_groups;    // [groups + 1]: first sequence of each group
   const int* prefix_lens;  // [groups]: tokens that a group's sequences share
+  // Where an item's parts are (kPagedPrefix, kPagedOwn): {slot of the first or -1 (whole, in O and LSE), of the second
+  // (then every other slot), parts, 0}, by paged_entry
+  int4* parts;
 };
 
 constexpr int kPagedPlain = 0;
 constexpr int kPagedPrefix = 1;   // the new tokens of groups of sequences over the groups' shared pages
 constexpr int kPagedOwn = 2;      // the new tokens of each sequence over its pages behind the shared ones
 
-// Key tiles [t_begin, t_end) of an item; EXT: numbers of its list (see tile).
+// Key tiles [t_begin, t_end) of an item; EXT: of its list.
 struct PagedUnit {
   int valid;
   int head;
@@ -149,11 +153,7 @@ struct PagedUnit {
   int t_begin, t_end;
   int slot;       // workspace slot of this part, -1: the whole item
   long long table;   // offset of the sequence's row in the page table
-  int sink_tiles, skip;   // EXT: list entry v is tile v (v < sink_tiles) or v + skip
-  template <bool EXT>
-  __device__ __forceinline__ int tile(int v) const {
-    return !EXT || v < sink_tiles ? v : v + skip;
-  }
+  int sink_keys, skip;   // EXT: key x of the list is key x (x < sink_keys) or x + skip
 };
 
 // Keys that the token `tok` of a sequence keeps: [0, kept).
@@ -252,12 +252,20 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b, int b
   return s;
 }
 
-// EXT: a block's list, whose first token is token tok0 of the sequence.
-__device__ __forceinline__ void paged_list(const PagedParams& p, const PagedSeq& s, int tok0, int* sink_tiles,
+// EXT: the list of a block whose first token is token tok0 of the sequence, in whole
+// pages, or tiles where those are smaller.
+__device__ __forceinline__ void paged_list(const PagedParams& p, const PagedSeq& s, int tok0, int* sink_keys,
                                            int* skip) {
-  const int lo = max(0, s.kv_len - s.q_len + tok0 - p.window + 1) / kKeysPerTile;
-  *sink_tiles = min(key_tiles_of(p.sinks), lo);
-  *skip = lo - *sink_tiles;
+  const int log2 = min(p.page_log2, 7), unit = 1 << log2;
+  const int lo = max(0, s.kv_len - s.q_len + tok0 - p.window + 1) >> log2 << log2;
+  *sink_keys = min((p.sinks + unit - 1) >> log2 << log2, lo);
+  *skip = lo - *sink_keys;
+}
+
+// The entry of block i of sequence b in PagedParams::parts.  No two blocks have the same: q0 / block grows by a
+// sequence's blocks but one at least.
+__device__ __forceinline__ long long paged_entry(const PagedParams& p, int q0, int block, int i, int b, int head) {
+  return (static_cast<long long>(q0) / block + i + b) * p.Hkv + head;
 }
 
 // Cost of an item: item_keys for its start and end, then its keys, at least one (a
@@ -349,9 +357,9 @@ struct PagedPlace {
     tiles = key_tiles_of(keys);
     cost = p.item_keys + keys;
     if constexpr (EXT) {
-      int sink_tiles, skip;
-      paged_list(p, s, i * p.sub_tokens * SUBS, &sink_tiles, &skip);
-      tiles -= skip;
+      int sink_keys, skip;
+      paged_list(p, s, i * p.sub_tokens * SUBS, &sink_keys, &skip);
+      tiles = key_tiles_of(keys - skip);
       cost = p.item_keys + min(keys, p.most_keys);
     }
   }
@@ -471,7 +479,7 @@ __device__ __forceinline__ PagedUnit paged_unit(const PagedParams& p, const Page
   u.table = b * p.table_stride;
   if constexpr (EXT) {
     u.table = s.row * p.table_stride + s.page0;
-    paged_list(p, s, u.tok0, &u.sink_tiles, &u.skip);
+    paged_list(p, s, u.tok0, &u.sink_keys, &u.skip);
   }
   u.t_begin = u.t_end = 0;
   u.slot = -1;
@@ -485,6 +493,7 @@ struct PagedWalk {
   PagedPlace at;
   long long lo, hi;   // the range
   int cta;
+  long long share, total;   // EXT: of a range, of the list
 
   template <int SUBS, bool EXT>
   __device__ __forceinline__ PagedUnit next(const PagedParams& p) {
@@ -501,6 +510,15 @@ struct PagedWalk {
           u.slot = 2 * cta;
         else if (to < at.tiles)
           u.slot = 2 * cta + 1;
+        if constexpr (EXT) {
+          if (p.parts != nullptr && from == 0) {   // the ranges that follow hold the item's other parts
+            int parts = 1;
+            for (long long next = hi; next < total && at.tile(p, next) < at.tiles; next += share) ++parts;
+            if (lane == 0)
+              p.parts[paged_entry(p, at.s.q0, p.sub_tokens * SUBS, at.i, at.b, at.head)] =
+                  make_int4(u.slot, 2 * (cta + 1), parts, 0);
+          }
+        }
       }
       at.start += at.cost;
       lo = max(lo, at.start);
@@ -540,6 +558,8 @@ __device__ __forceinline__ PagedWalk paged_walk(const PagedParams& p, int cta) {
   const PagedStrips f = paged_strips<SUBS, EXT>(p);
   const long long share = paged_share<SUBS, EXT>(p, f, &total);
   w.cta = cta;
+  w.share = share;
+  w.total = total;
   w.lo = cta * share;
   w.hi = cta < p.ctas ? min(w.lo + share, total) : w.lo;
   if (w.lo < w.hi) w.at = paged_find<SUBS, EXT>(p, f, w.lo);
@@ -578,7 +598,7 @@ __device__ __forceinline__ PagedParts paged_parts_even(const PagedParams& p, int
 
 // Whole warp: the page numbers of a sequence's tiles, in ascending order of the
 // tiles, 32 table entries at a time (one per lane) and the next 32 on their way.
-// EXT: entries are numbered in the list of tiles, one for a page of a tile, or for a tile within a page.
+// EXT: entries are those of the list, a page each, or a tile of a page where those are larger.
 template <bool EXT>
 struct PageCursor {
   const int* table;
@@ -586,18 +606,17 @@ struct PageCursor {
   int chunk0;      // first entry in `pages`
   int pages, pages_next;
   int log2_tile;   // EXT: log2 of a tile's entries
-  int entries;     // EXT: entries of the unit
-  int lo;          // EXT: first key of the block's windows
-  const PagedUnit* unit;
+  int sinks, skip; // EXT: the list's gap, in entries
 
   __device__ __forceinline__ PageCursor(const PagedParams& p, const PagedUnit& w, int tiles) {
     table = p.page_table + (tiles > 0 ? w.table : 0);
     live = tiles > 0 ? (w.kv_len + (1 << p.page_log2) - 1) >> p.page_log2 : 0;
     if constexpr (EXT) {
-      unit = &w;
-      log2_tile = max(0, 7 - p.page_log2);
-      entries = tiles > 0 ? (w.t_begin + tiles) << log2_tile : 0;
-      lo = w.kv_len - w.q_len + w.tok0 - p.window + 1;
+      const int log2 = min(p.page_log2, 7);   // of an entry's keys
+      log2_tile = 7 - log2;
+      sinks = w.sink_keys >> log2;
+      skip = w.skip >> log2;
+      live = tiles > 0 ? ((w.kv_len + (1 << log2) - 1) >> log2) - skip : 0;
       chunk0 = tiles > 0 ? w.t_begin << log2_tile : 0;
     } else {
       chunk0 = tiles > 0 ? (w.t_begin << 7) >> p.page_log2 : 0;
@@ -605,25 +624,16 @@ struct PageCursor {
     pages = fetch(p, chunk0);
     pages_next = fetch(p, chunk0 + 32);
   }
+  // EXT: number in the sequence's keys of an entry of the list
+  __device__ __forceinline__ int place(int entry) const { return entry < sinks ? entry : entry + skip; }
   __device__ __forceinline__ int fetch(const PagedParams& p, int first) const {
-    int i = first + (threadIdx.x & 31);
+    const int i = first + (threadIdx.x & 31);
     int id = 0;
-    if constexpr (EXT) {
-      if (i >= entries) return id;
-      i = page(p, i);
-      const int begin = i << p.page_log2;
-      if (begin + (1 << p.page_log2) <= lo && begin >= p.sinks) return p.num_pages;   // nobody sees it: zeros
-    }
     if (i < live) {
-      id = table[i];
+      id = table[EXT ? place(i) >> max(0, p.page_log2 - 7) : i];
       if (id < 0 || id >= p.num_pages) atomicOr(p.status, kDevErrPage);
     }
     return id;
-  }
-  // EXT: the page (number in the sequence) of an entry
-  __device__ __forceinline__ int page(const PagedParams& p, int entry) const {
-    const int t = unit->template tile<true>(entry >> log2_tile);
-    return p.page_log2 <= 7 ? (t << log2_tile) + (entry & ((1 << log2_tile) - 1)) : t >> (p.page_log2 - 7);
   }
   // lane x: the tile's x-th page; *count: how many there are
   __device__ __forceinline__ int tile(const PagedParams& p, int t, int* count) {
@@ -633,8 +643,12 @@ struct PageCursor {
       pages = pages_next;
       pages_next = fetch(p, chunk0 + 32);
     }
-    *count = min(kKeysPerTile >> min(p.page_log2, 7), live - (EXT ? page(p, first) : first));
+    *count = min(kKeysPerTile >> min(p.page_log2, 7), live - first);
     return __shfl_sync(0xffffffffu, pages, (first - chunk0 + (threadIdx.x & 31)) & 31);
+  }
+  // slot within its page of tile t's first key
+  __device__ __forceinline__ int row(const PagedParams& p, int t) const {
+    return ((EXT && p.page_log2 > 7 ? place(t) : t) << 7) & ((1 << p.page_log2) - 1);
   }
 };
 
@@ -785,7 +799,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
     if (first >= w.ntok) return 0;
     const int last = min(first + p.sub_tokens, w.ntok) - 1;
     const int kept = paged_kept(p.causal, w.kv_len, w.q_len, w.tok0 + last);
-    return max(0, min(w.t_end, key_tiles_of(kept) - (EXT ? w.skip : 0)) - w.t_begin);
+    return max(0, min(w.t_end, key_tiles_of(EXT ? max(0, kept - w.skip) : kept)) - w.t_begin);
   };
 
   // ---- the producers' copies; whole warps, `ok` is cleared after an abort
@@ -805,7 +819,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
     int count;
     const int id = pages.tile(p, tile, &count);
     const CUtensorMap* map = (index & 1) == 0 ? &tm_k : &tm_v;
-    const int row = (w.tile<EXT>(tile) << 7) & ((1 << p.page_log2) - 1);
+    const int row = pages.row(p, tile);
     uint8_t* dst = sKV + slot * TILE + (static_cast<uint32_t>(lane) << slots_log2) * 128;
     const uint32_t bytes = static_cast<uint32_t>(count * (kEnd - kFirst)) * (128u << slots_log2);
     if (lap > 0) warp_wait(&bars->kv_empty[slot], (lap - 1) & 1, ok);
@@ -1163,13 +1177,18 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
       const int rows = max(0, min(p.sub_tokens, w.ntok - sub_tok0)) * p.G;   // live rows
       const bool live = row < rows;
       const bool warp_live = NARROW || wq * 32 < rows;
-      const int kv_len = w.kv_len, t_begin = w.t_begin;
-      const int lim = live ? paged_kept(p.causal, kv_len, w.q_len, w.tok0 + sub_tok0 + tok) : 0;
+      const int t_begin = w.t_begin;
+      const int lim = live ? paged_kept(p.causal, w.kv_len, w.q_len, w.tok0 + sub_tok0 + tok) : 0;
       // every live row keeps at least the first token's keys
-      const int lim_min = paged_kept(p.causal, kv_len, w.q_len, w.tok0 + sub_tok0);
-      // EXT: keys below this one may lie outside some live row's window
-      const int low_max =
-          EXT ? paged_kept(p.causal, kv_len, w.q_len, w.tok0 + min(sub_tok0 + p.sub_tokens, w.ntok) - 1) - p.window : 0;
+      int lim_min = paged_kept(p.causal, w.kv_len, w.q_len, w.tok0 + sub_tok0);
+      int kv_len = w.kv_len, low_max = 0;
+      if constexpr (EXT) {   // numbers of the list from here on
+        // keys below this one may lie outside some live row's window
+        low_max = paged_kept(p.causal, kv_len, w.q_len, w.tok0 + min(sub_tok0 + p.sub_tokens, w.ntok) - 1) - p.window -
+                  w.skip;
+        lim_min -= w.skip;
+        kv_len -= w.skip;
+      }
 
       // One thread of the sub-tile that visits every key tile releases the ring slots.
       const bool releaser = (threadIdx.x & (kRowsPerSub - 1)) == 0 && n_tiles == nmax && n_tiles > 0 &&
@@ -1191,7 +1210,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
           if (j > 0) bar_arrive(&bars->kv_empty[(base + 2 * j - 1) % STAGES]);
           bar_arrive(&bars->kv_empty[(base + 2 * j) % STAGES]);
         }
-        const int key0 = w.tile<EXT>(t_begin + j) * kKeysPerTile;
+        const int key0 = (t_begin + j) * kKeysPerTile;
         // V rows behind the last key: zeros, written by the first sub-tile that reads them
         if (key0 + kKeysPerTile > kv_len && (sub == 0 || j >= n0)) {
           const int tid = wq * 32 + lane;
@@ -1222,7 +1241,8 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
           const int first = key0 + (NARROW ? wq * 32 : 0);
           const uint32_t tMine = tS + (NARROW ? wq * 32 : 0);
           uint32_t s[kChunks][32];
-          const bool masked = key0 + kKeysPerTile > lim_min || (EXT && key0 < low_max && key0 + kKeysPerTile > p.sinks);
+          const bool masked = key0 + kKeysPerTile > lim_min ||
+                              (EXT && key0 < max(low_max, w.sink_keys) && key0 + kKeysPerTile > p.sinks);
           auto load_s = [&]() {
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) tmem_ld32(tMine + c * 32, s[c]);
@@ -1234,7 +1254,11 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
               for (int c = 0; c < kChunks; ++c) {
                 if constexpr (EXT) {
                   const int at = first + c * 32;
-                  const uint32_t keep = low_bits(lim - at) & (~low_bits(lim - p.window - at) | low_bits(p.sinks - at));
+                  // before the gap, and behind it
+                  const uint32_t a = low_bits(lim - at) & (~low_bits(lim - p.window - at) | low_bits(p.sinks - at));
+                  const int to = at + w.skip;
+                  const uint32_t b = low_bits(lim - to) & (~low_bits(lim - p.window - to) | low_bits(p.sinks - to));
+                  const uint32_t before = low_bits(w.sink_keys - at), keep = (a & before) | (b & ~before);
 #pragma unroll
                   for (int e = 0; e < 32; ++e)
                     if (!(keep >> e & 1u)) s[c][e] = __float_as_uint(-INFINITY);

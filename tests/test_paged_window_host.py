@@ -94,37 +94,37 @@ def tiles_of(keys):
 
 
 def test_lists_and_costs():
-    """The kernel's list of a block (tiles with sinks, then those of its windows) holds every tile that a row sees; the
-    closed form of the blocks' costs is the sum of theirs, and a block's cost reaches its last tile."""
+    """The kernel's list of a block (pages, or tiles of larger pages, with sinks, then those of its windows) holds every
+    key that a row sees; the closed form of the blocks' costs is the sum of theirs, and a block's cost reaches its last
+    tile."""
     rng = random.Random(5)
     for _ in range(3000):
-        block = rng.choice([1, 4, 18, 32, 128, 256])
+        block, unit = rng.choice([1, 4, 18, 32, 128, 256]), rng.choice([16, 32, 64, 128])
         window = rng.choice([1, 5, 127, 128, 129, rng.randint(1, 3000)])
         sinks = rng.choice([0, 1, 128, 130, rng.randint(0, 600)])
         kv, q = rng.randint(0, 4000), rng.randint(1, 1200)
         fixed = rng.choice([256, 512])
         blocks = -(-q // block)
-        most = TILE * (tiles_of(sinks) + (block - 1 + window + 126) // TILE + 1)
+        most = (-(-sinks // unit) + (block - 1 + window + 2 * unit - 2) // unit) * unit
 
         def keys(i):
             return max(1, max(0, min(kv, kv - q + min((i + 1) * block, q))))
 
         for i in rng.sample(range(blocks), min(blocks, 4)):
             first, last = kv - q + i * block, kv - q + min((i + 1) * block, q) - 1
-            lo = int(max(0, first - window + 1) / TILE)
-            sink_tiles = min(tiles_of(sinks), lo)
-            skip = lo - sink_tiles
+            lo = max(0, first - window + 1) // unit * unit
+            sink_keys = min(-(-sinks // unit) * unit, lo)
+            skip = lo - sink_keys
             kept = max(0, min(kv, last + 1))
-            listed = [v if v < sink_tiles else v + skip for v in range(max(0, tiles_of(kept) - skip))]
-            assert listed == sorted(set(listed))
+            listed = [x if x < sink_keys else x + skip for x in range(max(0, kept - skip))]
+            assert listed == sorted(set(listed)) and len(listed) <= most
+            every = set(listed)
             for row in {first, last, rng.randint(first, last)}:
-                if row < 0:
-                    continue
-                assert set(range(max(0, row - window + 1) // TILE, row // TILE + 1)) <= set(listed)
-                if sinks:
-                    assert set(range(0, (min(sinks, row + 1) - 1) // TILE + 1)) <= set(listed)
-            tiles = tiles_of(keys(i)) - skip
-            assert tiles >= 1 and tiles <= tiles_of(min(keys(i), most)) and (kept == 0 or tiles == len(listed))
+                if row >= 0:
+                    assert set(range(max(0, row - window + 1), row + 1)) <= every
+                    assert set(range(min(sinks, row + 1))) <= every
+            tiles = tiles_of(keys(i) - skip)
+            assert 1 <= tiles <= tiles_of(min(keys(i), most)) and (kept == 0 or tiles == tiles_of(len(listed)))
 
         # cost_before
         for i in rng.sample(range(blocks + 1), min(blocks + 1, 4)):
@@ -145,3 +145,16 @@ def test_lists_and_costs():
                 if i == blocks:
                     got += max(1, min(kv, most))
             assert got == want, (block, window, sinks, kv, q, i)
+
+
+def test_entries_of_blocks():
+    """Blocks of all sequences have entries of their own (the parts that the joining kernel looks up)."""
+    rng = random.Random(6)
+    for _ in range(500):
+        block, B = rng.choice([1, 2, 5, 32, 128]), rng.randint(1, 30)
+        lens = [rng.choice([0, 1, rng.randint(0, 300)]) for _ in range(B)]
+        T, q0, seen = sum(lens) + rng.randint(0, 5), 0, []
+        for b, n in enumerate(lens):
+            seen += [q0 // block + i + b for i in range(-(-n // block))]
+            q0 += n
+        assert len(seen) == len(set(seen)) and all(0 <= x < T // block + B + 1 for x in seen)
