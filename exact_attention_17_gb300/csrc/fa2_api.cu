@@ -13,6 +13,7 @@
 #include "fa2.h"
 #include "fa2_host.h"
 #include "fa2_launch.h"
+#include "fa2_norm.h"
 
 namespace {
 
@@ -74,7 +75,7 @@ int device_ready() {
         fa2host::prepare_tc_pair_d128() != cudaSuccess || fa2host::prepare_simt() != cudaSuccess ||
         fa2host::prepare_bwd() != cudaSuccess || fa2host::prepare_bwd2() != cudaSuccess ||
         fa2host::prepare_window_bf16() != cudaSuccess || fa2host::prepare_window_f16() != cudaSuccess ||
-        fa2host::prepare_bwd_window() != cudaSuccess ||
+        fa2host::prepare_bwd_window() != cudaSuccess || fa2host::prepare_norm() != cudaSuccess ||
         fa2host::prepare_paged_ext_bf16() != cudaSuccess || fa2host::prepare_paged_ext_f16() != cudaSuccess ||
         fa2host::prepare_paged_bf16() != cudaSuccess || fa2host::prepare_paged_f16() != cudaSuccess)
       return;

@@ -38,11 +38,11 @@ void run_bwd(bool causal, const CUtensorMap& mq, const CUtensorMap& mk, const CU
 }
 
 template <int D, bool F16>
-void run_bwd_pre(const void* O, const uint16_t* g, const float* LSE, float* dQ, float* L2, float* Dr,
-                 long long rows, int Nq, int Nq_pad, cudaStream_t s, bool o_half = false) {
+void run_bwd_pre(const float* O, const uint16_t* g, const float* LSE, float* dQ, float* L2, float* Dr,
+                 long long rows, int Nq, int Nq_pad, cudaStream_t s) {
   const long long blocks = (rows * 32 + 255) / 256;
-  const auto kernel = o_half ? fa2dev::fa2_bwd_pre_kernel<D, F16, true> : fa2dev::fa2_bwd_pre_kernel<D, F16, false>;
-  kernel<<<static_cast<unsigned>(blocks), 256, 0, s>>>(O, g, LSE, dQ, L2, Dr, rows, Nq, Nq_pad);
+  fa2dev::fa2_bwd_pre_kernel<D, F16><<<static_cast<unsigned>(blocks), 256, 0, s>>>(O, g, LSE, dQ, L2, Dr, rows,
+                                                                                 Nq, Nq_pad);
 }
 }  // namespace
 
@@ -66,15 +66,15 @@ cudaError_t launch_bwd(int d, bool causal, bool f16, const CUtensorMap& mq, cons
   return cudaGetLastError();
 }
 
-cudaError_t launch_bwd_pre(int d, bool f16, const void* O, const void* dO, const float* LSE, float* dQ,
-                           float* L2, float* Dr, long long rows, int Nq, int Nq_pad, cudaStream_t s, bool o_half) {
+cudaError_t launch_bwd_pre(int d, bool f16, const float* O, const void* dO, const float* LSE, float* dQ,
+                           float* L2, float* Dr, long long rows, int Nq, int Nq_pad, cudaStream_t s) {
   const uint16_t* g = static_cast<const uint16_t*>(dO);
   if (d == 64)
-    f16 ? run_bwd_pre<64, true>(O, g, LSE, dQ, L2, Dr, rows, Nq, Nq_pad, s, o_half)
-        : run_bwd_pre<64, false>(O, g, LSE, dQ, L2, Dr, rows, Nq, Nq_pad, s, o_half);
+    f16 ? run_bwd_pre<64, true>(O, g, LSE, dQ, L2, Dr, rows, Nq, Nq_pad, s)
+        : run_bwd_pre<64, false>(O, g, LSE, dQ, L2, Dr, rows, Nq, Nq_pad, s);
   else
-    f16 ? run_bwd_pre<128, true>(O, g, LSE, dQ, L2, Dr, rows, Nq, Nq_pad, s, o_half)
-        : run_bwd_pre<128, false>(O, g, LSE, dQ, L2, Dr, rows, Nq, Nq_pad, s, o_half);
+    f16 ? run_bwd_pre<128, true>(O, g, LSE, dQ, L2, Dr, rows, Nq, Nq_pad, s)
+        : run_bwd_pre<128, false>(O, g, LSE, dQ, L2, Dr, rows, Nq, Nq_pad, s);
   return cudaGetLastError();
 }
 

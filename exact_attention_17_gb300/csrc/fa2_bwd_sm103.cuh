@@ -103,9 +103,8 @@ struct alignas(8) BwdBarriers {
 // Pre-pass: one warp per query row.  D_i = dO_i . O_i, L2_i = LSE_i log2(e),
 // and the row of dQ set to zero.  Entries past Nq in each head's padded
 // arrays are set to zero.
-// O_HALF: O has the input type instead of fp32.
-template <int D, bool F16, bool O_HALF = false>
-__global__ void __launch_bounds__(256) fa2_bwd_pre_kernel(const void* __restrict__ O_any,
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) fa2_bwd_pre_kernel(const float* __restrict__ O,
                                                           const uint16_t* __restrict__ dO,
                                                           const float* __restrict__ LSE,
                                                           float* __restrict__ dQ,
@@ -116,16 +115,15 @@ __global__ void __launch_bounds__(256) fa2_bwd_pre_kernel(const void* __restrict
   const long long r = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   if (r >= rows) return;
+  const float* o = O + r * D + lane * E;
   const uint16_t* g = dO + r * D + lane * E;
-  auto wide = [](uint32_t bits) {
-    return F16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(bits))) : __uint_as_float(bits << 16);
-  };
   float acc = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const float ov = O_HALF ? wide(static_cast<const uint16_t*>(O_any)[r * D + lane * E + e])
-                            : static_cast<const float*>(O_any)[r * D + lane * E + e];
-    acc = fmaf(wide(g[e]), ov, acc);
+    const uint32_t bits = g[e];
+    const float gv = F16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(bits)))
+                         : __uint_as_float(bits << 16);
+    acc = fmaf(gv, o[e], acc);
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
@@ -265,6 +263,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = bars->tmem_base;
+  if constexpr (WINDOW) {   // (launched behind the pre-pass, see launch_behind)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  }
 
   if (warp >= kWarpProducer) {
     regs_decrease<kBwdAuxRegs>();

@@ -4,12 +4,69 @@
 
 namespace fa2dev {
 
+// Pre-pass: D_i = dO_i . O_i, LSE_i log2(e), and the row of dQ set to zero, D / 8
+// lanes a query row.  Entries past Nq in each head's padded arrays are set to zero.
+// Bound: bytes (O and dO read, fp32 dQ written).
+template <int D, bool F16, bool O_HALF>
+__global__ void __launch_bounds__(256) fa2_bwd_window_pre_kernel(const void* __restrict__ O,
+                                                                 const uint16_t* __restrict__ dO,
+                                                                 const float* __restrict__ LSE,
+                                                                 float* __restrict__ dQ, float* __restrict__ L2,
+                                                                 float* __restrict__ Dr, long long rows, int Nq,
+                                                                 int Nq_pad) {
+  constexpr int kLanes = D / 8;
+  const long long r = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / kLanes;
+  const int lane = threadIdx.x % kLanes;
+  const bool live = r < rows;   // (every lane takes part in the shuffles)
+  const long long at = (live ? r : 0) * D + lane * 8;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  auto wide = [](uint32_t bits) {
+    return F16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(bits))) : __uint_as_float(bits << 16);
+  };
+  const uint4 g = *reinterpret_cast<const uint4*>(dO + at);
+  const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
+  float o[8];
+  if constexpr (O_HALF) {
+    const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(O) + at);
+    const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = wide(e & 1 ? xw[e / 2] >> 16 : xw[e / 2] & 0xffffu);
+  } else {
+    const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(O) + at);
+    const float4 y = *reinterpret_cast<const float4*>(static_cast<const float*>(O) + at + 4);
+    o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
+    o[4] = y.x; o[5] = y.y; o[6] = y.z; o[7] = y.w;
+  }
+  float acc = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) acc = fmaf(wide(e & 1 ? gw[e / 2] >> 16 : gw[e / 2] & 0xffffu), o[e], acc);
+#pragma unroll
+  for (int off = kLanes / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+  if (!live) return;
+  *reinterpret_cast<float4*>(dQ + at) = make_float4(0.f, 0.f, 0.f, 0.f);
+  *reinterpret_cast<float4*>(dQ + at + 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+  const long long bh = r / Nq, q = r - bh * Nq;
+  if (lane == 0) {
+    Dr[bh * Nq_pad + q] = acc;
+    L2[bh * Nq_pad + q] = LSE[r] * 1.4426950408889634f;
+  }
+  if (q == Nq - 1) {
+    for (long long pq = Nq + lane; pq < Nq_pad; pq += kLanes) {
+      Dr[bh * Nq_pad + pq] = 0.f;
+      L2[bh * Nq_pad + pq] = 0.f;
+    }
+  }
+}
+
 // dQ from fp32 to the input type (blocks from `key_blocks_from` on: see the launch), and
 // sums of the items of the key blocks that were cut: key row, four columns a thread.
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) fa2_bwd_window_end_kernel(const __grid_constant__ BwdParams p,
                                                                  uint2* __restrict__ dq_out, long long q_quads,
                                                                  int dq_blocks, long long sum_quads) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (static_cast<int>(blockIdx.x) < dq_blocks) {
     const float4* in = reinterpret_cast<const float4*>(p.dQ);
     for (long long i = blockIdx.x * 256ll + threadIdx.x; i < q_quads; i += dq_blocks * 256ll) {
@@ -65,9 +122,16 @@ cudaError_t set_limits() {
 template <int D, bool F16>
 cudaError_t run(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo,
                 const CUtensorMap& mdq, const fa2dev::BwdParams& p, unsigned grid, cudaStream_t s) {
-  fa2dev::fa2_bwd_tc_kernel<D, true, F16, true>
-      <<<grid, fa2dev::kBwdThreads, fa2dev::BwdConfig<D>::kSmemBytes, s>>>(mq, mk, mv, mdo, mdq, p);
-  return cudaGetLastError();
+  return launch_behind(fa2dev::fa2_bwd_tc_kernel<D, true, F16, true>, dim3(grid), fa2dev::kBwdThreads,
+                       fa2dev::BwdConfig<D>::kSmemBytes, s, mq, mk, mv, mdo, mdq, p);
+}
+
+template <int D, bool F16, bool O_HALF>
+cudaError_t run_pre(const void* O, const void* dO, const float* LSE, float* dQ, float* L2, float* Dr, long long rows,
+                    int Nq, int Nq_pad, cudaStream_t s) {
+  const long long blocks = (rows * (D / 8) + 255) / 256;
+  return launch_behind(fa2dev::fa2_bwd_window_pre_kernel<D, F16, O_HALF>, dim3(static_cast<unsigned>(blocks)), 256, 0, s,
+                       O, static_cast<const uint16_t*>(dO), LSE, dQ, L2, Dr, rows, Nq, Nq_pad);
 }
 
 template <int D, bool F16>
@@ -79,9 +143,8 @@ cudaError_t run_end(const fa2dev::BwdParams& p, void* dq_out, long long q_elems,
   const long long sum_blocks = (sum_quads + 255) / 256;
   if (dq_blocks + sum_blocks == 0) return cudaSuccess;
   if (dq_blocks + sum_blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  fa2dev::fa2_bwd_window_end_kernel<D, F16><<<static_cast<unsigned>(dq_blocks + sum_blocks), 256, 0, s>>>(
-      p, static_cast<uint2*>(dq_out), quads, dq_blocks, sum_quads);
-  return cudaGetLastError();
+  return launch_behind(fa2dev::fa2_bwd_window_end_kernel<D, F16>, dim3(static_cast<unsigned>(dq_blocks + sum_blocks)),
+                       256, 0, s, p, static_cast<uint2*>(dq_out), quads, dq_blocks, sum_quads);
 }
 }  // namespace
 
@@ -91,6 +154,17 @@ cudaError_t prepare_bwd_window() {
       (e = set_limits<128, false>()) != cudaSuccess)
     return e;
   return set_limits<128, true>();
+}
+
+cudaError_t launch_bwd_window_pre(int d, bool f16, bool o_half, const void* O, const void* dO, const float* LSE,
+                                  float* dQ, float* L2, float* Dr, long long rows, int Nq, int Nq_pad, cudaStream_t s) {
+  const auto pick = [&](auto dim) {
+    constexpr int D = decltype(dim)::value;
+    return f16 ? (o_half ? run_pre<D, true, true> : run_pre<D, true, false>)
+               : (o_half ? run_pre<D, false, true> : run_pre<D, false, false>);
+  };
+  const auto f = d == 64 ? pick(fa2dev::Int<64>{}) : pick(fa2dev::Int<128>{});
+  return f(O, dO, LSE, dQ, L2, Dr, rows, Nq, Nq_pad, s);
 }
 
 cudaError_t launch_bwd_window(int d, bool f16, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,

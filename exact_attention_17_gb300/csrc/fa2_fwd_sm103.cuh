@@ -375,6 +375,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
     prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
+    if constexpr (WINDOW) asm volatile("griddepcontrol.wait;" ::: "memory");   // (see launch_behind)
     if (qbytes) {
       bar_arrive_expect_tx(&bars->q_full, qbytes);
       for (int s = 0; s < SUBS; ++s) {
@@ -417,6 +418,10 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = bars->tmem_base;
+  if constexpr (WINDOW) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  }
 
   // Each role branch starts with its register budget change, so that the
   // compiler can allocate each branch for its own budget.
@@ -754,7 +759,13 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
       // Offset decision: the row max (eight independent 3-input max chains
       // over the 128 scores, then a small tree); the offset moves to it when
       // it exceeds the current one by more than kRescaleLog2.
-      float m_new = m;
+      // WINDOW: a row that sees few keys of the sinks' tile and of the first of its window has an offset that is low for
+      // the tiles behind them: its sums exceed the bound while no score is kRescaleLog2 above the offset, and it would
+      // send its warp the long way at every tile.  So the max comes first, and the offset moves to it however little it
+      // exceeds it, at those tiles and the one behind them, and wherever a sum exceeds the bound later on.  (16384
+      // positions, 32 heads, window 4096: 780 us, with 4 sinks 881.)
+      bool settle = WINDOW && j <= wt.sink_tiles + 1;
+      float m_new = m, rs = 0.f;
       float alpha = 1.f;   // correction factor 2^(m - m'): 0 on the first tile, 1 when the offset stays
       auto decide = [&]() {
 #define FA2_S(f) __uint_as_float(s[(f) >> 5][(f) & 31])
@@ -771,14 +782,13 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
         const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
                                fmaxf(mx8[6], mx8[7]));
         const float m_cand = fmaxf(m, mx * sl2);
-        const bool move = (j == 0) || (m_cand > m + kRescaleLog2);
+        const bool move = (j == 0) || (m_cand > m + kRescaleLog2) || (WINDOW && settle && m_cand > m);
         m_new = move ? m_cand : m;
         alpha = !move ? 1.f : (m == -INFINITY ? 0.f : ex2_approx(m - m_new));
       };
 
       // P = 2^(s * scale*log2e - offset), packed pairwise; row sum in four packed accumulators
       uint32_t pk[2][32];
-      float rs;
       auto exps = [&]() {
         const float off = m_new == -INFINITY ? 0.f : m_new;
         const float2 c2 = make_float2(sl2, sl2);
@@ -811,11 +821,12 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
       // those of taking the max first, but for a max within rounding of the
       // bound.
       load_s();
-      const bool max_first = __any_sync(0xffffffffu, m == -INFINITY);
+      const bool max_first = (WINDOW && settle) || __any_sync(0xffffffffu, m == -INFINITY);
       bool decided = max_first;   // (otherwise alpha is 1 on every lane)
       if (max_first) decide();
       exps();
       if (!max_first && __any_sync(0xffffffffu, rs > kRescaleBound)) {
+        settle = true;
         load_s();
         decide();
         exps();

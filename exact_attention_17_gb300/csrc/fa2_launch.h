@@ -81,10 +81,8 @@ cudaError_t launch_bwd(int d, bool causal, bool f16, const CUtensorMap& mq, cons
                        const CUtensorMap& mv, const CUtensorMap& mdo, const CUtensorMap& mdq,
                        const fa2dev::BwdParams& p, unsigned grid, cudaStream_t s);
 // D_i = dO_i . O_i and LSE_i log2(e) into [BH][Nq_pad] arrays; dQ rows zeroed.
-// o_half: O has the input type (else fp32).
-cudaError_t launch_bwd_pre(int d, bool f16, const void* O, const void* dO, const float* LSE, float* dQ,
-                           float* L2, float* Dr, long long rows, int Nq, int Nq_pad, cudaStream_t s,
-                           bool o_half = false);
+cudaError_t launch_bwd_pre(int d, bool f16, const float* O, const void* dO, const float* LSE, float* dQ,
+                           float* L2, float* Dr, long long rows, int Nq, int Nq_pad, cudaStream_t s);
 cudaError_t launch_zero(float* p, long long n, cudaStream_t s);
 
 // Two-tile backward kernel (fa2_bwd2.cu), head dimension 128.  mq64, mdo64:
@@ -102,6 +100,9 @@ cudaError_t launch_window_bf16(int d, int subs, const CUtensorMap& mq, const CUt
 cudaError_t launch_window_f16(int d, int subs, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                               const CUtensorMap& mo, const fa2dev::FwdParams& p, unsigned grid, cudaStream_t s);
 cudaError_t prepare_bwd_window();
+// The pre-pass of the gradients, as launch_bwd_pre (o_half: O has the input type, else fp32).
+cudaError_t launch_bwd_window_pre(int d, bool f16, bool o_half, const void* O, const void* dO, const float* LSE,
+                                  float* dQ, float* L2, float* Dr, long long rows, int Nq, int Nq_pad, cudaStream_t s);
 cudaError_t launch_bwd_window(int d, bool f16, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                               const CUtensorMap& mdo, const CUtensorMap& mdq, const fa2dev::BwdParams& p, unsigned grid,
                               cudaStream_t s);

@@ -49,30 +49,6 @@ struct NormShape {
   static __device__ __forceinline__ int second(int e) { return kAcross ? first(e) + W : 2 * e + 1; }
 };
 
-template <typename T, int W>
-__device__ __forceinline__ void widen_all(const Vec<T, W>& a, float* out) {
-  if constexpr (W % 2 == 0) {
-#pragma unroll
-    for (int e = 0; e < W; e += 2) {
-      const float2 x = widen(&a.v[e]);
-      out[e] = x.x;
-      out[e + 1] = x.y;
-    }
-  } else {
-    out[0] = widen1(a.v[0]);
-  }
-}
-
-template <typename T, int W>
-__device__ __forceinline__ void narrow_all(Vec<T, W>& a, const float* in) {
-  if constexpr (W % 2 == 0) {
-#pragma unroll
-    for (int e = 0; e < W; e += 2) narrow(&a.v[e], in[e], in[e + 1]);
-  } else {
-    narrow1(a.v[0], in[0]);
-  }
-}
-
 template <int LANES>
 __device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
@@ -121,82 +97,158 @@ __device__ __forceinline__ unsigned load_turns(const RopeParams& p, int lane, lo
   return turned;
 }
 
-__device__ __forceinline__ long long position_of(const RopeParams& p, long long t, long long* batch, long long* n) {
-  *batch = 0;
-  *n = t;
-  if (p.N < p.total_tokens) {
-    *batch = t < 0x7fffffff ? static_cast<long long>(fast_div(static_cast<int>(t), p.div_n)) : t / p.N;
-    *n = t - *batch * p.N;
-  }
-  const long long at = *batch * p.pos_batch + *n;
-  return p.pos64 ? static_cast<const long long*>(p.positions)[at] : static_cast<const int*>(p.positions)[at];
+// Every pair of a lane.
+template <typename S>
+__host__ __device__ constexpr unsigned all_pairs() {
+  return S::PAIRS == 32 ? 0xffffffffu : (1u << (S::PAIRS & 31)) - 1u;
 }
 
-constexpr int kNormUnroll = 2;   // heads whose rows are normed side by side (and as many on their way)
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 
-template <typename T, int D, int W, bool HALF, bool APPEND>
-__global__ void __launch_bounds__(kRopeThreads, 2) fa2_norm_rope_kernel(const __grid_constant__ NormParams np) {
+// The partner of element pair i: the same place of the other vector where a rotated pair lies across both, else the
+// pair itself the other way round.
+template <int W, bool HALF, int E2>
+__device__ __forceinline__ float2 partner(const float2 (&f)[E2], int i) {
+  return HALF && W > 1 ? f[i % W < W / 2 ? i + W / 2 : i - W / 2] : make_float2(f[i].y, f[i].x);
+}
+
+// A lane's elements two by two: neighbours of a vector, or (vectors of one element) the pair itself.  The
+// arithmetic of a row is done on both at once (packed fp32 instructions).
+template <typename T, int W, int NV>
+__device__ __forceinline__ void widen_pairs(const Vec<T, W> (&a)[2 * NV], float2 (&out)[W * NV]) {
+#pragma unroll
+  for (int i = 0; i < W * NV; ++i) {
+    if constexpr (W == 1)
+      out[i] = make_float2(widen1(a[2 * i].v[0]), widen1(a[2 * i + 1].v[0]));
+    else
+      out[i] = widen(&a[i / (W / 2)].v[2 * (i % (W / 2))]);
+  }
+}
+
+template <typename T, int W, int NV>
+__device__ __forceinline__ void narrow_pairs(Vec<T, W> (&a)[2 * NV], const float2 (&in)[W * NV]) {
+#pragma unroll
+  for (int i = 0; i < W * NV; ++i) {
+    if constexpr (W == 1) {
+      narrow1(a[2 * i].v[0], in[i].x);
+      narrow1(a[2 * i + 1].v[0], in[i].y);
+    } else {
+      narrow(&a[i / (W / 2)].v[2 * (i % (W / 2))], in[i].x, in[i].y);
+    }
+  }
+}
+
+// y = r (own x + cross x'), x' the partner: weight and rotation of a lane's columns in one.
+template <typename S, typename T, int W, bool HALF>
+struct Turn {
+  static constexpr int E = S::E, E2 = S::E / 2;
+  float2 own[E2], cross[E2];
+  unsigned turned;
+
+  __device__ __forceinline__ void set(const void* weight, int weight32, int lane, int r, const float2 (&turns)[S::PAIRS],
+                                      unsigned which) {
+    float w[E], o[E], c[E];
+    if (weight != nullptr) {
+      load_weights<S>(weight, weight32, lane, r, w);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) w[e] = 1.f;
+    }
+#pragma unroll
+    for (int e = 0; e < S::PAIRS; ++e) {
+      const int i0 = S::first(e), i1 = S::second(e);
+      o[i0] = w[i0] * turns[e].x;
+      o[i1] = w[i1] * turns[e].x;
+      c[i0] = -w[i1] * turns[e].y;
+      c[i1] = w[i0] * turns[e].y;
+    }
+#pragma unroll
+    for (int i = 0; i < E2; ++i) {
+      own[i] = make_float2(o[2 * i], o[2 * i + 1]);
+      cross[i] = make_float2(c[2 * i], c[2 * i + 1]);
+    }
+    turned = which;
+  }
+  __device__ __forceinline__ void apply(const float2 (&f)[E2], float2 r, float2 (&u)[E2]) const {
+    if (turned == all_pairs<S>()) {
+#pragma unroll
+      for (int e = 0; e < E2; ++e) u[e] = mul2(r, fma2(partner<W, HALF>(f, e), cross[e], mul2(f[e], own[e])));
+      return;
+    }
+    // element by element: a column that is not rotated takes nothing from another, whatever that holds
+    float flat[E], o[E], c[E];
+#pragma unroll
+    for (int e = 0; e < E2; ++e) {
+      flat[2 * e] = f[e].x;
+      flat[2 * e + 1] = f[e].y;
+      o[2 * e] = own[e].x;
+      o[2 * e + 1] = own[e].y;
+      c[2 * e] = cross[e].x;
+      c[2 * e + 1] = cross[e].y;
+    }
+#pragma unroll
+    for (int e = 0; e < S::PAIRS; ++e) {
+      const int i0 = S::first(e), i1 = S::second(e);
+      float u0 = flat[i0] * o[i0], u1 = flat[i1] * o[i1];
+      if (turned >> e & 1) {
+        u0 = fmaf(flat[i1], c[i0], u0);
+        u1 = fmaf(flat[i0], c[i1], u1);
+      }
+      flat[i0] = u0;
+      flat[i1] = u1;
+    }
+#pragma unroll
+    for (int e = 0; e < E2; ++e) u[e] = mul2(r, make_float2(flat[2 * e], flat[2 * e + 1]));
+  }
+};
+
+constexpr int kNormUnroll = 2;   // append: heads whose rows are normed side by side (and as many on their way)
+
+template <typename T, int D, int W, bool HALF>
+__global__ void __launch_bounds__(kRopeThreads, 2) fa2_norm_append_kernel(const __grid_constant__ NormParams np) {
   using S = NormShape<T, D, W, HALF>;
   using V = typename S::V;
   constexpr int U = kNormUnroll, NV = S::NV, E = S::E;
   constexpr int kTokens = kRopeThreads / S::kLanes;
   const RopeParams& p = np.r;
-  __shared__ RopeToken toks[APPEND ? kTokens : 1];
-  const long long tok0 = static_cast<long long>(blockIdx.x) * kTokens;
-  const int n_tok = static_cast<int>(min(static_cast<long long>(kTokens), p.total_tokens - tok0));
-  const int row0 = blockIdx.y * p.rows, row1 = min(row0 + p.rows, p.total_rows);
+  __shared__ RopeToken toks[kTokens];
   const int k = threadIdx.x / S::kLanes, lane = threadIdx.x % S::kLanes;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-
-  // Every lane runs along to the end (the sums are the warp's); one without a token neither reads nor writes.
-  bool live = k < n_tok;
-  const long long t = tok0 + (live ? k : 0);
-  long long pos, batch = 0, n = t, slot = -1;
-  if constexpr (APPEND) {
-    append_tokens(p, static_cast<int>(tok0), n_tok, toks);
-    __syncthreads();
-    const RopeToken o = toks[live ? k : 0];
-    pos = o.pos;
-    slot = o.dst;
-    live = live && o.live;
-  } else {
-    pos = position_of(p, t, &batch, &n);
-  }
-  float2 turns[S::PAIRS];
-  unsigned turned = 0;
-  bool have_turns = false;
   int at[2 * NV];
 #pragma unroll
   for (int v = 0; v < 2 * NV; ++v) at[v] = S::column(lane, v / 2, v % 2, p.r);
 
-  // the queries' heads, the keys' and the values' of a new token, or all heads of one array
+  const int row0 = blockIdx.y * p.rows, row1 = min(row0 + p.rows, p.total_rows);
+  const long long tok0 = static_cast<long long>(blockIdx.x) * kTokens;
+  const int n_tok = static_cast<int>(min(static_cast<long long>(kTokens), p.total_tokens - tok0));
+
+  // Every lane runs along to the end (the sums are the warp's); one without a token neither reads nor writes.
+  bool live = k < n_tok;
+  const long long t = tok0 + (live ? k : 0);
+  append_tokens(p, static_cast<int>(tok0), n_tok, toks);
+  __syncthreads();
+  const RopeToken token = toks[live ? k : 0];
+  const long long pos = token.pos, slot = token.dst;
+  live = live && token.live;
+  float2 turns[S::PAIRS];   // (kept from the queries' heads to the keys')
+  unsigned turned = 0;
+  bool have_turns = false;
+
+  // the queries' heads, the keys' and the values' of a new token
 #pragma unroll 1
-  for (int part = 0; part < (APPEND ? 3 : 1); ++part) {
-    const T* x;
-    T* y;
-    long long xs, ys;
-    int from = row0, to = row1;
-    bool mine = live;
-    const void* weight = np.weight;
-    if constexpr (APPEND) {
-      const int first = part == 0 ? 0 : p.Hq + (part - 1) * p.Hkv;
-      from = max(row0, first) - first;
-      to = min(row1, first + (part == 0 ? p.Hq : p.Hkv)) - first;
-      mine = live && (part == 0 || slot >= 0);
-      weight = part == 0 ? np.weight : part == 1 ? np.k_weight : nullptr;
-      xs = part == 0 ? p.q_head : part == 1 ? p.k_head : p.v_head;
-      ys = part == 0 ? p.qo_head : p.page_head;
-      x = static_cast<const T*>(part == 0 ? p.q : part == 1 ? p.k : p.v) +
-          t * (part == 0 ? p.q_token : part == 1 ? p.k_token : p.v_token);
-      y = static_cast<T*>(part == 0 ? p.q_out : part == 1 ? p.k_pages : p.v_pages) +
-          (part == 0 ? t * p.qo_token : slot);
-    } else {
-      xs = p.x_head;
-      ys = p.y_head;
-      x = static_cast<const T*>(p.x) + batch * p.x_batch + n * p.x_token;
-      y = static_cast<T*>(p.y) + batch * p.y_batch + n * p.y_token;
-    }
+  for (int part = 0; part < 3; ++part) {
+    const int first = part == 0 ? 0 : p.Hq + (part - 1) * p.Hkv;
+    const int from = max(row0, first) - first, to = min(row1, first + (part == 0 ? p.Hq : p.Hkv)) - first;
+    const bool mine = live && (part == 0 || slot >= 0);
+    const void* weight = part == 0 ? np.weight : part == 1 ? np.k_weight : nullptr;
+    const long long xs = part == 0 ? p.q_head : part == 1 ? p.k_head : p.v_head;
+    const long long ys = part == 0 ? p.qo_head : p.page_head;
+    const T* x = static_cast<const T*>(part == 0 ? p.q : part == 1 ? p.k : p.v) +
+                 t * (part == 0 ? p.q_token : part == 1 ? p.k_token : p.v_token);
+    T* y = static_cast<T*>(part == 0 ? p.q_out : part == 1 ? p.k_pages : p.v_pages) +
+           (part == 0 ? t * p.qo_token : slot);
     int left = to - from;   // the same for the whole block
     if (left <= 0) continue;
     x += from * xs;
@@ -216,190 +268,388 @@ __global__ void __launch_bounds__(kRopeThreads, 2) fa2_norm_rope_kernel(const __
       }
     };
     load(a, left);
-    const bool plain = APPEND && part == 2;   // values are copied
-    float w[E];
+    const bool plain = part == 2;   // values are copied
+    Turn<S, T, W, HALF> turn;
     if (!plain) {
-      if (weight != nullptr) {
-        load_weights<S>(weight, np.weight32, lane, p.r, w);
-      } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) w[e] = 1.f;
-      }
       if (!have_turns) turned = load_turns<S, W, HALF>(p, lane, pos, turns);
       have_turns = true;
+      turn.set(weight, np.weight32, lane, p.r, turns, turned);
     }
-    for (;;) {
-      if (left > U) load(next, left - U);
-      if (!plain) {
-        float scale[U];
+    constexpr int E2 = E / 2;
+    auto work = [&](V (&row)[U][2 * NV]) {
+      float2 f[U][E2];
+      float scale[U];
 #pragma unroll
-        for (int i = 0; i < U; ++i) scale[i] = 1.f;
-        if (weight != nullptr) {
-          float sum[U];
-#pragma unroll
-          for (int i = 0; i < U; ++i) {
-            float f[E], s0 = 0.f, s1 = 0.f;
-#pragma unroll
-            for (int v = 0; v < 2 * NV; ++v) widen_all(a[i][v], f + v * W);
-#pragma unroll
-            for (int e = 0; e < E; e += 2) {
-              s0 = fmaf(f[e], f[e], s0);
-              s1 = fmaf(f[e + 1], f[e + 1], s1);
-            }
-            sum[i] = s0 + s1;
-          }
-#pragma unroll
-          for (int o = S::kLanes / 2; o > 0; o >>= 1)
-#pragma unroll
-            for (int i = 0; i < U; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
-#pragma unroll
-          for (int i = 0; i < U; ++i) scale[i] = rsqrtf(fmaf(sum[i], 1.f / D, np.eps));
-        }
+      for (int i = 0; i < U; ++i) {
+        widen_pairs<T, W, NV>(row[i], f[i]);
+        scale[i] = 1.f;
+      }
+      if (weight != nullptr) {
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-          float f[E];
+          float2 sum = mul2(f[i][0], f[i][0]);
 #pragma unroll
-          for (int v = 0; v < 2 * NV; ++v) widen_all(a[i][v], f + v * W);
-#pragma unroll
-          for (int e = 0; e < E; ++e) f[e] *= scale[i] * w[e];
-#pragma unroll
-          for (int e = 0; e < S::PAIRS; ++e) {
-            const int i0 = S::first(e), i1 = S::second(e);
-            const float u0 = f[i0] * turns[e].x - f[i1] * turns[e].y, u1 = f[i1] * turns[e].x + f[i0] * turns[e].y;
-            if (turned >> e & 1) {   // (a column that is not rotated takes nothing from another)
-              f[i0] = u0;
-              f[i1] = u1;
-            }
-          }
-#pragma unroll
-          for (int v = 0; v < 2 * NV; ++v) narrow_all(a[i][v], f + v * W);
+          for (int e = 1; e < E2; ++e) sum = fma2(f[i][e], f[i][e], sum);
+          scale[i] = sum.x + sum.y;
         }
+#pragma unroll
+        for (int o = S::kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+          for (int i = 0; i < U; ++i) scale[i] += __shfl_xor_sync(0xffffffffu, scale[i], o);
+#pragma unroll
+        for (int i = 0; i < U; ++i) scale[i] = rsqrtf(fmaf(scale[i], 1.f / D, np.eps));
       }
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        if (mine && i < left) {
+        const float2 r = make_float2(scale[i], scale[i]);
+        float2 u[E2];
+        turn.apply(f[i], r, u);
+        narrow_pairs<T, W, NV>(row[i], u);
+      }
+    };
+    auto store = [&](const V (&row)[U][2 * NV], int count) {
 #pragma unroll
-          for (int v = 0; v < 2 * NV; ++v) *reinterpret_cast<V*>(y + at[v]) = a[i][v];
+      for (int i = 0; i < U; ++i) {
+        if (mine && i < count) {
+#pragma unroll
+          for (int v = 0; v < 2 * NV; ++v) *reinterpret_cast<V*>(y + at[v]) = row[i][v];
         }
         y += ys;
       }
+    };
+    // two sets of rows in turn
+    for (;;) {
+      if (left > U) load(next, left - U);
+      if (!plain) work(a);
+      store(a, left);
       left -= U;
       if (left <= 0) break;
-#pragma unroll
-      for (int i = 0; i < U; ++i)
-#pragma unroll
-        for (int v = 0; v < 2 * NV; ++v) a[i][v] = next[i][v];
+      if (left > U) load(a, left - U);
+      if (!plain) work(next);
+      store(next, left);
+      left -= U;
+      if (left <= 0) break;
     }
   }
 }
 
-// Blocks take (token tile, range of heads) items one after the other, tiles innermost.
+// Block b's places are norm_range(b) .. norm_range(b + 1) - 1: all (token tile, head)
+// places in equal shares, tiles outermost.  (A block for each tile with all its heads: 512 of them on 304 slots, 29
+// us instead of 27 for the 134 MB above.)
+__device__ __forceinline__ long long norm_range(long long places, long long b) { return places * b / gridDim.x; }
+
+// A block's walk over its places.
+template <int TOKENS>
+struct NormWalk {
+  long long place, end;
+  long long t, batch, n;   // this lane's token
+  int head;
+  bool live;
+
+  __device__ __forceinline__ NormWalk(const NormParams& np) {
+    place = norm_range(np.places, blockIdx.x);
+    end = norm_range(np.places, blockIdx.x + 1ll);
+    if (place < end) seek(np.r, place / np.r.total_rows);
+  }
+  __device__ __forceinline__ bool more() const { return place < end; }
+  // to a tile, at the head that `place` says
+  __device__ __forceinline__ void seek(const RopeParams& p, long long tile) {
+    head = static_cast<int>(place - tile * p.total_rows);
+    const long long tok0 = tile * TOKENS;
+    const int k = threadIdx.x / (kRopeThreads / TOKENS);
+    live = k < p.total_tokens - tok0;
+    t = tok0 + (live ? k : 0);
+    batch = 0;
+    n = t;
+    if (p.N < p.total_tokens) {
+      batch = t < 0x7fffffff ? static_cast<long long>(fast_div(static_cast<int>(t), p.div_n)) : t / p.N;
+      n = t - batch * p.N;
+    }
+    tile_ = tile;
+  }
+  // the next place; true when it is of another tile
+  __device__ __forceinline__ bool next(const RopeParams& p) {
+    ++place;
+    if (++head < p.total_rows) return false;
+    if (place < end) seek(p, tile_ + 1);
+    return true;
+  }
+
+ private:
+  long long tile_;
+};
+
+// Rows on their way to a block: each lane copies its own vectors asynchronously into
+// its own slots of a ring in shared memory, kNormStages - 1 rows ahead of the one
+// that it works on, over the ends of tiles too.  Nothing there is another thread's, so
+// that waiting for one's own copies is all the order it takes.  (Rows ahead in
+// registers: two for y in 29 us and one of x and dy in 54, at the sizes above.)
+// Rows off 16-byte boundaries (W = 1) are loaded when it is their turn.
+constexpr int kNormStages = 3;
+constexpr int kNormBlocksPerSm = 2;
+
+template <typename T, int W, int VECTORS>
+struct NormFeed {
+  static constexpr bool kAsync = sizeof(Vec<T, W>) == 16;
+  static constexpr int kBytes = kAsync ? kNormStages * kRopeThreads * VECTORS * 16 : 16;
+  uint8_t* slots;
+
+  __device__ __forceinline__ uint8_t* slot(int stage, int v) const {
+    return slots + ((stage * VECTORS + v) * kRopeThreads + threadIdx.x) * 16;
+  }
+  // vector v of a row into the stage, zeros where it is not `live`
+  __device__ __forceinline__ void copy(int stage, int v, const T* from, bool live) const {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(slot(stage, v))), "l"(from),
+                 "r"(live ? 16 : 0)
+                 : "memory");
+  }
+  static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  static __device__ __forceinline__ void wait() {   // for all rows but the last kNormStages - 2
+    asm volatile("cp.async.wait_group %0;" ::"n"(kNormStages - 2) : "memory");
+  }
+};
+
 template <typename T, int D, int W, bool HALF>
-__global__ void __launch_bounds__(kRopeThreads, 2) fa2_norm_rope_grad_kernel(const __grid_constant__ NormParams np) {
+__global__ void __launch_bounds__(kRopeThreads, kNormBlocksPerSm) fa2_norm_rope_kernel(const __grid_constant__ NormParams np) {
   using S = NormShape<T, D, W, HALF>;
   using V = typename S::V;
-  constexpr int NV = S::NV, E = S::E;
-  constexpr int kTokens = kRopeThreads / S::kLanes;
+  constexpr int NV = S::NV, E2 = S::E / 2;
+  using Feed = NormFeed<T, W, 2 * NV>;
+  extern __shared__ __align__(16) uint8_t norm_smem[];
+  const Feed feed = {norm_smem};
   const RopeParams& p = np.r;
-  __shared__ float sums[kRopeThreads / 32][D];
-  const int k = threadIdx.x / S::kLanes, lane = threadIdx.x % S::kLanes;
+  const int lane = threadIdx.x % S::kLanes;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  float w[E], dw[E];
-  load_weights<S>(np.weight, np.weight32, lane, p.r, w);
-#pragma unroll
-  for (int e = 0; e < E; ++e) dw[e] = 0.f;
   int at[2 * NV];
 #pragma unroll
   for (int v = 0; v < 2 * NV; ++v) at[v] = S::column(lane, v / 2, v % 2, p.r);
 
-#pragma unroll 1
-  for (int item = blockIdx.x; item < np.items; item += gridDim.x) {
-    const int range = fast_div(item, np.div_tiles), tile = item - range * np.tiles;
-    const long long tok0 = static_cast<long long>(tile) * kTokens;
-    const bool live = k < p.total_tokens - tok0;
-    const long long t = tok0 + (live ? k : 0);
-    long long batch, n;
-    const long long pos = position_of(p, t, &batch, &n);
-    const int row0 = range * p.rows;
-    int left = min(p.rows, p.total_rows - row0);
-    const T* x = static_cast<const T*>(p.x) + batch * p.x_batch + n * p.x_token + row0 * p.x_head;
-    const T* g = static_cast<const T*>(np.dy) + batch * np.dy_batch + n * np.dy_token + row0 * np.dy_head;
-    T* y = static_cast<T*>(p.y) + batch * p.y_batch + n * p.y_token + row0 * p.y_head;
-    V xa[2 * NV], ga[2 * NV], xn[2 * NV], gn[2 * NV];
-    auto load = [&](V (&vx)[2 * NV], V (&vg)[2 * NV]) {
+  // Every lane runs along to the end (the sums are the warp's); one without a token neither reads nor writes.
+  NormWalk<kRopeThreads / S::kLanes> work(np), ahead = work;
+  auto row_of = [&](const decltype(work)& w) {
+    return static_cast<const T*>(p.x) + w.batch * p.x_batch + w.n * p.x_token + w.head * p.x_head;
+  };
+  auto send = [&](int stage) {
+    if (ahead.more()) {
+      const T* x = row_of(ahead);
+#pragma unroll
+      for (int v = 0; v < 2 * NV; ++v) feed.copy(stage, v, x + at[v], ahead.live);
+      ahead.next(p);
+    }
+    Feed::commit();
+  };
+  if constexpr (Feed::kAsync) {
+    for (int i = 0; i < kNormStages - 1; ++i) send(i);
+  }
+  Turn<S, T, W, HALF> turn;
+  bool fresh = true;
+  int stage = 0;
+  while (work.more()) {
+    if (fresh) {
+      float2 turns[S::PAIRS];
+      const long long i = work.batch * p.pos_batch + work.n;
+      const long long pos = p.pos64 ? static_cast<const long long*>(p.positions)[i] : static_cast<const int*>(p.positions)[i];
+      const unsigned turned = load_turns<S, W, HALF>(p, lane, pos, turns);
+      turn.set(np.weight, np.weight32, lane, p.r, turns, turned);
+    }
+    V row[2 * NV];
+    if constexpr (Feed::kAsync) {
+      Feed::wait();
+#pragma unroll
+      for (int v = 0; v < 2 * NV; ++v) row[v] = *reinterpret_cast<const V*>(feed.slot(stage, v));
+      send(stage == 0 ? kNormStages - 1 : stage - 1);   // (the row before this one's slots)
+      stage = stage == kNormStages - 1 ? 0 : stage + 1;
+    } else {
+#pragma unroll
+      for (int v = 0; v < 2 * NV; ++v) row[v] = work.live ? *reinterpret_cast<const V*>(row_of(work) + at[v]) : V{};
+    }
+    float2 f[E2], u[E2];
+    widen_pairs<T, W, NV>(row, f);
+    float2 square = mul2(f[0], f[0]);
+#pragma unroll
+    for (int e = 1; e < E2; ++e) square = fma2(f[e], f[e], square);
+    const float r = rsqrtf(fmaf(row_sum<S::kLanes>(square.x + square.y), 1.f / D, np.eps));
+    turn.apply(f, make_float2(r, r), u);
+    narrow_pairs<T, W, NV>(row, u);
+    if (work.live) {
+      T* y = static_cast<T*>(p.y) + work.batch * p.y_batch + work.n * p.y_token + work.head * p.y_head;
+#pragma unroll
+      for (int v = 0; v < 2 * NV; ++v) *reinterpret_cast<V*>(y + at[v]) = row[v];
+    }
+    fresh = work.next(p);
+  }
+}
+
+// The gradients.
+template <typename T, int D, int W, bool HALF>
+__global__ void __launch_bounds__(kRopeThreads, fa2host::kNormGradBlocksPerSm)
+    fa2_norm_rope_grad_kernel(const __grid_constant__ NormParams np) {
+  using S = NormShape<T, D, W, HALF>;
+  using V = typename S::V;
+  constexpr int NV = S::NV, E = S::E, E2 = E / 2;
+  constexpr bool kOther = HALF && W > 1;   // the partner is in the other vector
+  using Feed = NormFeed<T, W, 4 * NV>;
+  extern __shared__ __align__(16) uint8_t norm_smem[];
+  const Feed feed = {norm_smem};
+  const RopeParams& p = np.r;
+  __shared__ float sums[kRopeThreads / 32][D];
+  const int lane = threadIdx.x % S::kLanes;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  int at[2 * NV];
+#pragma unroll
+  for (int v = 0; v < 2 * NV; ++v) at[v] = S::column(lane, v / 2, v % 2, p.r);
+  NormWalk<kRopeThreads / S::kLanes> work(np), ahead = work;
+  auto row_of = [&](const decltype(work)& w) {
+    return static_cast<const T*>(p.x) + w.batch * p.x_batch + w.n * p.x_token + w.head * p.x_head;
+  };
+  auto grad_of = [&](const decltype(work)& w) {
+    return static_cast<const T*>(np.dy) + w.batch * np.dy_batch + w.n * np.dy_token + w.head * np.dy_head;
+  };
+  auto send = [&](int stage) {
+    if (ahead.more()) {
+      const T *x = row_of(ahead), *g = grad_of(ahead);
 #pragma unroll
       for (int v = 0; v < 2 * NV; ++v) {
-        vx[v] = live ? *reinterpret_cast<const V*>(x + at[v]) : V{};
-        vg[v] = live ? *reinterpret_cast<const V*>(g + at[v]) : V{};
+        feed.copy(stage, v, x + at[v], ahead.live);
+        feed.copy(stage, 2 * NV + v, g + at[v], ahead.live);
       }
-      x += p.x_head;
-      g += np.dy_head;
-    };
-    load(xa, ga);
-    float2 turns[S::PAIRS];
-    const unsigned turned = load_turns<S, W, HALF>(p, lane, pos, turns);
-    for (; left > 0; --left) {
-      if (left > 1) load(xn, gn);
-      float fx[E], fg[E];
+      ahead.next(p);
+    }
+    Feed::commit();
+  };
+  if constexpr (Feed::kAsync) {
+    for (int i = 0; i < kNormStages - 1; ++i) send(i);
+  }
+  float2 w[E2], dw[E2];
+  {
+    float one[E];
+    load_weights<S>(np.weight, np.weight32, lane, p.r, one);
 #pragma unroll
-      for (int v = 0; v < 2 * NV; ++v) {
-        widen_all(xa[v], fx + v * W);
-        widen_all(ga[v], fg + v * W);
-      }
-      float square = 0.f, dot = 0.f;
+    for (int i = 0; i < E2; ++i) {
+      w[i] = make_float2(one[2 * i], one[2 * i + 1]);
+      dw[i] = make_float2(0.f, 0.f);
+    }
+  }
+  // Pairs that lie across two vectors share their coefficients but for the sign of `cross`.
+  constexpr int C = kOther ? E2 / 2 : E2;
+  float2 own[C], cross[C];
+  unsigned turned = 0;
+  bool fresh = true;
+  int stage = 0;
+  while (work.more()) {
+    if (fresh) {
+      float2 turns[S::PAIRS];
+      const long long i = work.batch * p.pos_batch + work.n;
+      const long long pos = p.pos64 ? static_cast<const long long*>(p.positions)[i] : static_cast<const int*>(p.positions)[i];
+      turned = load_turns<S, W, HALF>(p, lane, pos, turns);
 #pragma unroll
-      for (int e = 0; e < S::PAIRS; ++e) {
-        const int i0 = S::first(e), i1 = S::second(e);
-        const float u0 = fg[i0] * turns[e].x - fg[i1] * turns[e].y, u1 = fg[i1] * turns[e].x + fg[i0] * turns[e].y;
-        if (turned >> e & 1) {
-          fg[i0] = u0;
-          fg[i1] = u1;
+      for (int c = 0; c < C; ++c) {
+        if constexpr (kOther) {
+          own[c] = make_float2(turns[2 * c].x, turns[2 * c + 1].x);
+          cross[c] = make_float2(turns[2 * c].y, turns[2 * c + 1].y);
+        } else {
+          own[c] = make_float2(turns[c].x, turns[c].x);
+          cross[c] = make_float2(-turns[c].y, turns[c].y);
         }
-      }
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        square = fmaf(fx[e], fx[e], square);
-        dot = fmaf(fx[e], fg[e] * w[e], dot);
-      }
-#pragma unroll
-      for (int o = S::kLanes / 2; o > 0; o >>= 1) {
-        square += __shfl_xor_sync(0xffffffffu, square, o);
-        dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      }
-      const float r = rsqrtf(fmaf(square, 1.f / D, np.eps));
-      const float along = dot * (1.f / D) * r * r;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        dw[e] = fmaf(fg[e], fx[e] * r, dw[e]);   // (rows that are not there are zeros)
-        fg[e] = r * (fg[e] * w[e] - fx[e] * along);
-      }
-      if (live) {
-#pragma unroll
-        for (int v = 0; v < 2 * NV; ++v) {
-          V out;
-          narrow_all(out, fg + v * W);
-          *reinterpret_cast<V*>(y + at[v]) = out;
-        }
-      }
-      y += p.y_head;
-#pragma unroll
-      for (int v = 0; v < 2 * NV; ++v) {
-        xa[v] = xn[v];
-        ga[v] = gn[v];
       }
     }
+    V xa[2 * NV], ga[2 * NV];
+    if constexpr (Feed::kAsync) {
+      Feed::wait();
+#pragma unroll
+      for (int v = 0; v < 2 * NV; ++v) {
+        xa[v] = *reinterpret_cast<const V*>(feed.slot(stage, v));
+        ga[v] = *reinterpret_cast<const V*>(feed.slot(stage, 2 * NV + v));
+      }
+      send(stage == 0 ? kNormStages - 1 : stage - 1);   // (the row before this one's slots)
+      stage = stage == kNormStages - 1 ? 0 : stage + 1;
+    } else {
+#pragma unroll
+      for (int v = 0; v < 2 * NV; ++v) {
+        xa[v] = work.live ? *reinterpret_cast<const V*>(row_of(work) + at[v]) : V{};
+        ga[v] = work.live ? *reinterpret_cast<const V*>(grad_of(work) + at[v]) : V{};
+      }
+    }
+    float2 fx[E2], fg[E2];
+    widen_pairs<T, W, NV>(xa, fx);
+    widen_pairs<T, W, NV>(ga, fg);
+    if (turned == all_pairs<S>()) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        if constexpr (kOther) {   // vector pairs i / (W / 2): first vector at a0, second W / 2 behind it
+          const int a0 = i / (W / 2) * W + i % (W / 2), a1 = a0 + W / 2;
+          const float2 less = make_float2(-cross[i].x, -cross[i].y);
+          const float2 u0 = fma2(fg[a1], less, mul2(fg[a0], own[i])), u1 = fma2(fg[a0], cross[i], mul2(fg[a1], own[i]));
+          fg[a0] = u0;
+          fg[a1] = u1;
+        } else {
+          fg[i] = fma2(make_float2(fg[i].y, fg[i].x), cross[i], mul2(fg[i], own[i]));
+        }
+      }
+    } else {   // (a column that is not rotated takes nothing from another)
+#pragma unroll
+      for (int e = 0; e < S::PAIRS; ++e) {
+        if (!(turned >> e & 1)) continue;
+        if constexpr (kOther) {
+          const int i = e / 2, a0 = i / (W / 2) * W + i % (W / 2), a1 = a0 + W / 2;
+          float &g0 = e % 2 ? fg[a0].y : fg[a0].x, &g1 = e % 2 ? fg[a1].y : fg[a1].x;
+          const float c = e % 2 ? own[i].y : own[i].x, s = e % 2 ? cross[i].y : cross[i].x;
+          const float u0 = g0 * c - g1 * s, u1 = g1 * c + g0 * s;
+          g0 = u0;
+          g1 = u1;
+        } else {
+          fg[e] = fma2(make_float2(fg[e].y, fg[e].x), cross[e], mul2(fg[e], own[e]));
+        }
+      }
+    }
+    float2 square2 = make_float2(0.f, 0.f), dot2 = square2, h[E2];
+#pragma unroll
+    for (int i = 0; i < E2; ++i) {
+      h[i] = mul2(fg[i], w[i]);
+      square2 = fma2(fx[i], fx[i], square2);
+      dot2 = fma2(fx[i], h[i], dot2);
+    }
+    float square = square2.x + square2.y, dot = dot2.x + dot2.y;
+#pragma unroll
+    for (int o = S::kLanes / 2; o > 0; o >>= 1) {
+      square += __shfl_xor_sync(0xffffffffu, square, o);
+      dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    }
+    const float r = rsqrtf(fmaf(square, 1.f / D, np.eps));
+    const float along = -dot * (1.f / D) * r * r * r;
+    const float2 r2 = make_float2(r, r), along2 = make_float2(along, along);
+#pragma unroll
+    for (int i = 0; i < E2; ++i) {
+      dw[i] = fma2(fg[i], mul2(fx[i], r2), dw[i]);   // (rows that are not there are zeros)
+      h[i] = fma2(h[i], r2, mul2(fx[i], along2));
+    }
+    if (work.live) {
+      V out[2 * NV];
+      narrow_pairs<T, W, NV>(out, h);
+      T* y = static_cast<T*>(p.y) + work.batch * p.y_batch + work.n * p.y_token + work.head * p.y_head;
+#pragma unroll
+      for (int v = 0; v < 2 * NV; ++v) *reinterpret_cast<V*>(y + at[v]) = out[v];
+    }
+    fresh = work.next(p);
   }
   // the warp's rows, then the block's warps
 #pragma unroll
-  for (int e = 0; e < E; ++e)
+  for (int i = 0; i < E2; ++i)
 #pragma unroll
-    for (int o = S::kLanes; o < 32; o <<= 1) dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], o);
+    for (int o = S::kLanes; o < 32; o <<= 1) {
+      dw[i].x += __shfl_xor_sync(0xffffffffu, dw[i].x, o);
+      dw[i].y += __shfl_xor_sync(0xffffffffu, dw[i].y, o);
+    }
   if ((threadIdx.x & 31) < S::kLanes) {
 #pragma unroll
     for (int v = 0; v < 2 * NV; ++v)
 #pragma unroll
-      for (int e = 0; e < W; ++e) sums[threadIdx.x >> 5][at[v] + e] = dw[v * W + e];
+      for (int e = 0; e < W; ++e) {
+        const float2 d = dw[(v * W + e) / 2];
+        sums[threadIdx.x >> 5][at[v] + e] = (v * W + e) % 2 ? d.y : d.x;
+      }
   }
   __syncthreads();
   if (threadIdx.x < D) {
@@ -444,8 +694,8 @@ constexpr int kWide = 16 / sizeof(T);
 template <typename T, int D, int W, bool HALF>
 constexpr int kBlockTokens = fa2dev::kRopeThreads / fa2dev::NormShape<T, D, W, HALF>::kLanes;
 
-template <typename T, int D, int W, bool HALF, bool APPEND>
-cudaError_t run(NormParams p, int sms, cudaStream_t s) {
+template <typename T, int D, int W, bool HALF>
+cudaError_t run_append(NormParams p, int sms, cudaStream_t s) {
   constexpr int tokens = kBlockTokens<T, D, W, HALF>;
   const long long tiles = (p.r.total_tokens + tokens - 1) / tokens;
   if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
@@ -456,29 +706,38 @@ cudaError_t run(NormParams p, int sms, cudaStream_t s) {
   if (chunks > 65535) chunks = 65535;
   p.r.rows = static_cast<int>((p.r.total_rows + chunks - 1) / chunks);
   chunks = (p.r.total_rows + p.r.rows - 1) / p.r.rows;
-  p.r.div_n = make_fast_div(static_cast<int>(p.r.N > 0 ? p.r.N : 1));
-  return launch_behind(fa2dev::fa2_norm_rope_kernel<T, D, W, HALF, APPEND>,
+  return launch_behind(fa2dev::fa2_norm_append_kernel<T, D, W, HALF>,
                        dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(chunks)), fa2dev::kRopeThreads, 0, s, p);
+}
+
+// Blocks for the call's places, as many as run at once; at least two places each.
+template <typename T, int D, int W, bool HALF>
+int norm_blocks(NormParams* p, int sms, int blocks_per_sm) {
+  constexpr int tokens = kBlockTokens<T, D, W, HALF>;
+  p->places = (p->r.total_tokens + tokens - 1) / tokens * p->r.total_rows;
+  p->r.div_n = make_fast_div(static_cast<int>(p->r.N > 0 ? p->r.N : 1));
+  const long long most = (p->places + 1) / 2, slots = static_cast<long long>(sms) * blocks_per_sm;
+  return static_cast<int>(most < slots ? most : slots);
+}
+
+template <typename T, int D, int W, int VECTORS>
+constexpr unsigned kFeedBytes = fa2dev::NormFeed<T, W, VECTORS>::kBytes;
+
+template <typename T, int D, int W, bool HALF>
+cudaError_t run(NormParams p, int sms, cudaStream_t s) {
+  constexpr unsigned smem = kFeedBytes<T, D, W, 2 * fa2dev::NormShape<T, D, W, HALF>::NV>;
+  const int grid = norm_blocks<T, D, W, HALF>(&p, sms, fa2dev::kNormBlocksPerSm);
+  static_assert(smem <= 49152, "more takes an attribute of the kernel");
+  return launch_behind(fa2dev::fa2_norm_rope_kernel<T, D, W, HALF>, dim3(static_cast<unsigned>(grid)),
+                       fa2dev::kRopeThreads, smem, s, p);
 }
 
 template <typename T, int D, int W, bool HALF>
 cudaError_t run_grad(NormParams p, float* dweight, int sms, cudaStream_t s) {
-  constexpr int tokens = kBlockTokens<T, D, W, HALF>;
-  const long long tiles = (p.r.total_tokens + tokens - 1) / tokens;
-  const long long most = static_cast<long long>(sms) * kNormGradBlocksPerSm;
-  // heads of an item: at least four, and items for eight rounds of the blocks
-  long long chunks = (8 * most + tiles - 1) / tiles;
-  if (chunks > (p.r.total_rows + 3) / 4) chunks = (p.r.total_rows + 3) / 4;
-  p.r.rows = static_cast<int>((p.r.total_rows + chunks - 1) / chunks);
-  chunks = (p.r.total_rows + p.r.rows - 1) / p.r.rows;
-  if (tiles * chunks > 0x7fffffffLL - most) return cudaErrorInvalidValue;
-  p.items = static_cast<int>(tiles * chunks);
-  p.tiles = static_cast<int>(tiles);
-  p.div_tiles = make_fast_div(p.tiles);
-  p.r.div_n = make_fast_div(static_cast<int>(p.r.N > 0 ? p.r.N : 1));
-  const int grid = static_cast<int>(p.items < most ? p.items : most);
+  constexpr unsigned smem = kFeedBytes<T, D, W, 4 * fa2dev::NormShape<T, D, W, HALF>::NV>;
+  const int grid = norm_blocks<T, D, W, HALF>(&p, sms, kNormGradBlocksPerSm);
   const cudaError_t e = launch_behind(fa2dev::fa2_norm_rope_grad_kernel<T, D, W, HALF>, dim3(static_cast<unsigned>(grid)),
-                                      fa2dev::kRopeThreads, 0, s, p);
+                                      fa2dev::kRopeThreads, smem, s, p);
   if (e != cudaSuccess) return e;
   return launch_behind(fa2dev::fa2_norm_sum_kernel, dim3(D / 8), fa2dev::kRopeThreads, 0, s,
                        static_cast<const float*>(p.partial), grid, D, dweight);
@@ -502,15 +761,34 @@ cudaError_t by_shape(int dtype, int d, bool wide, bool interleaved, const F& f) 
   return size(float{});
 }
 
+// The gradient's ring takes more shared memory than a kernel may have unasked.
+template <typename T, int D, int W, bool HALF>
+cudaError_t prepare_grad() {
+  return cudaFuncSetAttribute(fa2dev::fa2_norm_rope_grad_kernel<T, D, W, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kFeedBytes<T, D, W, 4 * fa2dev::NormShape<T, D, W, HALF>::NV>);
+}
+
 }  // namespace
+
+cudaError_t prepare_norm() {
+  for (const int dtype : {FA2_DTYPE_BF16, FA2_DTYPE_FP16, FA2_DTYPE_FP32})
+    for (const int d : {64, 128, 256})
+      for (const bool interleaved : {false, true}) {
+        const cudaError_t e = by_shape(dtype, d, true, interleaved, [](auto t, auto dim, auto w, auto half) {
+          return prepare_grad<decltype(t), decltype(dim)::value, decltype(w)::value, decltype(half)::value>();
+        });
+        if (e != cudaSuccess) return e;
+      }
+  return cudaSuccess;
+}
 
 cudaError_t launch_norm_rope(NormParams p, bool append, int dtype, bool wide, int sms, cudaStream_t s) {
   return by_shape(dtype, p.r.d, wide, p.r.interleaved != 0, [&](auto t, auto dim, auto w, auto half) {
     using T = decltype(t);
     if constexpr (!std::is_same_v<T, float>) {   // (a cache holds 16-bit elements)
-      if (append) return run<T, decltype(dim)::value, decltype(w)::value, decltype(half)::value, true>(p, sms, s);
+      if (append) return run_append<T, decltype(dim)::value, decltype(w)::value, decltype(half)::value>(p, sms, s);
     }
-    return run<T, decltype(dim)::value, decltype(w)::value, decltype(half)::value, false>(p, sms, s);
+    return run<T, decltype(dim)::value, decltype(w)::value, decltype(half)::value>(p, sms, s);
   });
 }
 

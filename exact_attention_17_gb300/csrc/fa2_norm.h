@@ -15,9 +15,7 @@ struct NormParams {
   const void* dy;
   long long dy_batch, dy_token, dy_head;
   float* partial;          // [blocks][d]
-  int items;               // token tiles times head ranges
-  int tiles;
-  FastDiv div_tiles;
+  long long places;        // token tiles times heads (set by the launch)
 };
 
 }  // namespace fa2dev
@@ -27,6 +25,7 @@ namespace fa2host {
 // Most blocks that the gradient's first kernel has (each leaves d sums).
 constexpr int kNormGradBlocksPerSm = 2;
 
+cudaError_t prepare_norm();
 // wide: every row start, stride and weight allows 16-byte vectors, and whole vectors hold the rotated columns.
 cudaError_t launch_norm_rope(fa2dev::NormParams p, bool append, int dtype, bool wide, int sms, cudaStream_t s);
 cudaError_t launch_norm_rope_grad(fa2dev::NormParams p, float* dweight, int dtype, bool wide, int sms, cudaStream_t s);

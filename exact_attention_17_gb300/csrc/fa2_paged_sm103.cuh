@@ -1271,8 +1271,10 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
             }
           };
           // the row max, and the offset moved to it when it exceeds it by more than kRescaleLog2
-          float m_new = m;
+          float m_new = m, rs = 0.f;
           float alpha = 1.f;
+          const bool windows = EXT && p.role == kPagedPlain;
+          bool settle = windows && t_begin + j <= (w.sink_keys >> 7) + 1;
           auto decide = [&]() {
 #define FA2_S(f) __uint_as_float(s[(f) >> 5][(f) & 31])
             float mx8[8];
@@ -1288,12 +1290,13 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
             const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
                                    fmaxf(mx8[6], mx8[7]));
             const float m_cand = fmaxf(m, mx * sl2);
-            const bool move = m == -INFINITY || m_cand > m + kRescaleLog2;
+            // EXT: see the windows of the dense kernel
+            const bool move = m == -INFINITY || m_cand > m + kRescaleLog2 ||
+                              (EXT && settle && m_cand > m);
             m_new = move ? m_cand : m;
             alpha = !move ? 1.f : (m == -INFINITY ? 0.f : ex2_approx(m - m_new));
           };
           uint32_t pk[kChunks][16];
-          float rs;
           auto exps = [&]() {
             const float off = m_new == -INFINITY ? 0.f : m_new;
             const float2 c2 = make_float2(sl2, sl2);
@@ -1318,13 +1321,14 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
           // Once the offset is finite the exponentials come first, with the
           // offset as it stands (see the dense kernel); one loop, so that the
           // code, which every cold launch has to fetch, is there once.
-          bool decided = __any_sync(0xffffffffu, live && m == -INFINITY);   // take the row max first
+          bool decided = (EXT && settle) || __any_sync(0xffffffffu, live && m == -INFINITY);   // take the row max first
           for (;;) {
             load_s();
             if (decided) decide();
             exps();
             if (decided || !__any_sync(0xffffffffu, live && rs > kRescaleBound)) break;
             decided = true;
+            settle = windows;
           }
           if constexpr (NARROW) {
             // P: my keys, zeros for the other warps' (S covers all of P's columns);

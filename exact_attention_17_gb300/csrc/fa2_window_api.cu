@@ -72,9 +72,12 @@ BackwardPlan plan_backward(const Window& w, bool grad_half, int sms) {
   return q;
 }
 
-// Query sub-tiles per CTA, and the heads of a scheduling group, as for the forward pass without a window.
+// Query sub-tiles per CTA: as for the forward pass without a window, but one (two CTAs
+// per SM, whose starts and ends overlap the other's work) for short windows.  16384
+// positions, 32 heads sharing 8, two sub-tiles / one: d = 128, windows of 128, 1024 and 4096:
+// 146 / 114, 281 / 277 and 663 / 797 us; d = 64: 127 / 91, 254 / 214 and 592 / 590, 16384: 1197 / 1259.
 int sub_tiles(const Window& w, int sms) {
-  if (w.Nq <= 128 || w.d == 256) return 1;
+  if (w.Nq <= 128 || w.d == 256 || w.window <= (w.d == 64 ? 4096 : 1024)) return 1;
   return (static_cast<long long>(w.Nq) + 255) / 256 * w.BH < 2ll * sms ? 1 : 2;
 }
 
@@ -218,7 +221,7 @@ extern "C" int fa2_backward_window(const void* Q, const void* K, const void* V, 
   p.sink_chunk = plan.sink_chunk;
   p.part = reinterpret_cast<float*>(ws + plan.part_at);
   p.grad_half = half ? 1 : 0;
-  if (fa2host::launch_bwd_pre(d, f16, O, dO, LSE, dq, L2, Dr, w.BH * Nq, Nq, p.Nq_pad, s, o_half) != cudaSuccess ||
+  if (fa2host::launch_bwd_window_pre(d, f16, o_half, O, dO, LSE, dq, L2, Dr, w.BH * Nq, Nq, p.Nq_pad, s) != cudaSuccess ||
       fa2host::launch_bwd_window(d, f16, mq, mk, mv, mdo, mdq, p, static_cast<unsigned>(plan.items), s) != cudaSuccess ||
       fa2host::launch_bwd_window_end(d, f16, p, half ? dQ : nullptr, q_elems, s) != cudaSuccess)
     return FA2_ERR_LAUNCH;

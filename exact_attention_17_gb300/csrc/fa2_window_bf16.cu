@@ -16,9 +16,8 @@ cudaError_t set_limits() {
 template <int D, int SUBS>
 cudaError_t run(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mo,
                 const fa2dev::FwdParams& p, unsigned grid, cudaStream_t s) {
-  fa2dev::fa2_fwd_tc_kernel<D, true, kF16, SUBS, true>
-      <<<grid, fa2dev::FwdShape<SUBS>::kThreads, fa2dev::FwdConfig<D, SUBS>::kSmemBytes, s>>>(mq, mk, mv, mo, p);
-  return cudaGetLastError();
+  return launch_behind(fa2dev::fa2_fwd_tc_kernel<D, true, kF16, SUBS, true>, dim3(grid), fa2dev::FwdShape<SUBS>::kThreads,
+                       fa2dev::FwdConfig<D, SUBS>::kSmemBytes, s, mq, mk, mv, mo, p);
 }
 }  // namespace
 

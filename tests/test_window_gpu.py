@@ -143,9 +143,12 @@ def test_a_window_of_everything_is_causal_attention():
     q, k, v = inputs(BF, 2, 3, 3, 500, 500, 128)
     do = normal(q.shape, BF, 4)
     o, lse = fa2.forward(q, k, v, causal=True)
+    # both lie within their bounds of the 64-bit form, but not at the same place: the exponents' offsets differ
+    _, _, bO, bL, _, _ = forward(q, k, v, seen(500, 500, 500, 0), 1.0 / math.sqrt(128), EPS[F32])
     for window, sinks in ((500, 0), (1 << 40, 7), (1, 500)):
         ow, lw = fa2.forward_window(q, k, v, window, sinks)
-        assert torch.equal(ow, o) and torch.equal(lw, lse)
+        close(ow, o.double(), 2 * bO)
+        close(lw, lse.double(), 2 * bL)
     dk, dv = fa2.backward(q, k, v, o, lse, do, causal=True)[1:]
     got = fa2.backward_window(q, k, v, o, lse, do, 500)
     # the same tiles in the same order, but cut into items and added up in fp32
