@@ -397,7 +397,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // this tile's LSE log2(e) for the warpgroup's columns, fetched while S^T is computed
       float4 l4v[16];
 #pragma unroll
-      for (int e4 = 0; e4 < 16; ++e4) l4v[e4] = __ldg(reinterpret_cast<const float4*>(L2h + qcol0) + e4);
+      for (int e4 = 0; e4 < 16; ++e4) {
+        const float4* from = reinterpret_cast<const float4*>(L2h + qcol0) + e4;
+        l4v[e4] = WINDOW ? *from : __ldg(from);   // (WINDOW: this kernel may start while the pre-pass still writes them)
+      }
       if (!__all_sync(0xffffffffu, wait_bar(&bars->s_full, t & 1, abort, p.timeout_ns))) {
         ok = false;
         break;
@@ -443,7 +446,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // D for the same columns, fetched while the P^T store completes
       float4 d4v[16];
 #pragma unroll
-      for (int e4 = 0; e4 < 16; ++e4) d4v[e4] = __ldg(reinterpret_cast<const float4*>(Drh + qcol0) + e4);
+      for (int e4 = 0; e4 < 16; ++e4) {
+        const float4* from = reinterpret_cast<const float4*>(Drh + qcol0) + e4;
+        d4v[e4] = WINDOW ? *from : __ldg(from);
+      }
       tmem_st_wait();
       tc_fence_before_sync();
       bar_arrive(&bars->p_ready);

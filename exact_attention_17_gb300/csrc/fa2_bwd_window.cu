@@ -4,15 +4,15 @@
 
 namespace fa2dev {
 
+// (No pointer of these kernels is declared restricted: the compiler would read through the cache that is not
+// kept coherent, while the kernel before, behind which they are launched early, still writes.)
+
 // Pre-pass: D_i = dO_i . O_i, LSE_i log2(e), and the row of dQ set to zero, D / 8
 // lanes a query row.  Entries past Nq in each head's padded arrays are set to zero.
 // Bound: bytes (O and dO read, fp32 dQ written).
 template <int D, bool F16, bool O_HALF>
-__global__ void __launch_bounds__(256) fa2_bwd_window_pre_kernel(const void* __restrict__ O,
-                                                                 const uint16_t* __restrict__ dO,
-                                                                 const float* __restrict__ LSE,
-                                                                 float* __restrict__ dQ, float* __restrict__ L2,
-                                                                 float* __restrict__ Dr, long long rows, int Nq,
+__global__ void __launch_bounds__(256) fa2_bwd_window_pre_kernel(const void* O, const uint16_t* dO, const float* LSE,
+                                                                 float* dQ, float* L2, float* Dr, long long rows, int Nq,
                                                                  int Nq_pad) {
   constexpr int kLanes = D / 8;
   const long long r = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / kLanes;
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(256) fa2_bwd_window_pre_kernel(const void* __r
 // sums of the items of the key blocks that were cut: key row, four columns a thread.
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) fa2_bwd_window_end_kernel(const __grid_constant__ BwdParams p,
-                                                                 uint2* __restrict__ dq_out, long long q_quads,
+                                                                 uint2* dq_out, long long q_quads,
                                                                  int dq_blocks, long long sum_quads) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");

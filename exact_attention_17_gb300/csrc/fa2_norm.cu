@@ -661,8 +661,8 @@ __global__ void __launch_bounds__(kRopeThreads, fa2host::kNormGradBlocksPerSm)
 }
 
 // dweight: eight columns a block, the blocks' sums in 32 strips.
-__global__ void __launch_bounds__(kRopeThreads) fa2_norm_sum_kernel(const float* __restrict__ partial, int blocks, int d,
-                                                                    float* __restrict__ out) {
+__global__ void __launch_bounds__(kRopeThreads) fa2_norm_sum_kernel(const float* partial, int blocks, int d,
+                                                                    float* out) {   // (not restricted: see fa2_bwd_window.cu)
   __shared__ float sums[32][8];
   const int c = blockIdx.x * 8 + (threadIdx.x & 7), strip = threadIdx.x >> 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
