@@ -338,3 +338,28 @@ def test_other_streams_and_given_buffers():
             assert torch.equal(a, b)
     with pytest.raises(fa2.FA2Error):
         fa2.norm_rope_backward(dy, x, w, pos, freq, workspace=ws[:size // 2].clone())
+
+
+def test_rows_beyond_32_bits():
+    """More than 2^31 elements: the rows at both ends and around the border."""
+    H, N, d = 64, 270000, 128                     # 2.2e9 elements
+    x = torch.empty((1, H, N, d), dtype=BF, device="cuda")
+    y, freq, w = torch.empty_like(x), fa2.rope_inv_freq(d, device="cuda"), normal((d,), BF, 3, 0.3, 1.0)
+    x.view(torch.int16).zero_()
+    border = (1 << 31) // (N * d)
+    places = [(0, 0), (border, (1 << 31) // d - border * N), (H - 1, N - 1), (H - 1, 5)]
+    for i, (h, n) in enumerate(places):
+        x[0, h, n] = normal((d,), BF, 10 + i)
+    pos = torch.arange(N, device="cuda")
+    assert fa2.norm_rope(x, w, pos, freq, out=y) is y
+    for h, n in places:
+        ref, bound, size = forward_64(x[0, h, n:n + 1], w, pos[n:n + 1], freq, 1e-6, False, 1.0)
+        close(y[0, h, n:n + 1], ref, rounded(bound, size, BF))
+    dx, dw = fa2.norm_rope_backward(x, x, w, pos, freq, dx=y)
+    total, slacks = 0.0, 0.0
+    for h, n in places:
+        ref, bound, dw_, dw_bound = backward_64(x[0, h, n:n + 1], x[0, h, n:n + 1], w, pos[n:n + 1], freq, 1e-6, False,
+                                                1.0, chain=8)
+        close(dx[0, h, n:n + 1], ref, rounded(bound, ref, BF))
+        total, slacks = total + dw_, slacks + dw_bound
+    close(dw, total, slacks)                      # (all other rows are zeros)

@@ -312,3 +312,23 @@ def test_streams_and_given_buffers():
             assert torch.equal(a, b)
     with pytest.raises(fa2.FA2Error):
         fa2.forward_paged_prefix(*args, cu, lens, workspace=ws[:1024].clone())
+
+
+def test_a_cache_beyond_32_bits():
+    """Pages behind 2^31 elements, windows and shared prefixes."""
+    d, Hkv, S = 64, 4, 16
+    P = (1 << 31) // (Hkv * S * d) + 64
+    pages = [torch.empty((P, Hkv, S, d), dtype=BF, device="cuda") for _ in range(2)]
+    kv = [300, 320, 310]
+    small = Cache(kv, Hkv, S, d, BF, seed=5)
+    share(small, [0, 3], [288])
+    n = small.k.shape[0]
+    for big, own in zip(pages, (small.k, small.v)):
+        big[P - n:] = own
+    table = torch.where(small.table < n, small.table + (P - n), small.table)
+    q = normal((3, 8, d), BF, 1)
+    for call in (lambda k, v, t: fa2.forward_paged_window(q, k, v, t, small.lens, 100, 4),
+                 lambda k, v, t: fa2.forward_paged_prefix(q, k, v, t, small.lens, ints([0, 3]), ints([288]))):
+        a, b = call(*pages, table), call(small.k, small.v, small.table)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert status() == fa2.FA2_OK
