@@ -1,5 +1,6 @@
-"""GB300-native FlashAttention-2 forward pass (sm_103a), its backward pass, and
-attention over a paged key/value cache (``paged``).
+"""GB300-native FlashAttention-2 forward pass (sm_103a), its backward pass,
+attention over a paged key/value cache (``paged``), attention with a window
+(``window``), and heads normed and rotated in one pass (``norm``).
 
 Python binding of ``libfa2.so`` (C ABI in ``include/fa2.h``).  This module
 only marshals arguments: every step of the attention pass runs in the

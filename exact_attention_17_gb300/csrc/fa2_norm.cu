@@ -17,6 +17,11 @@
 // registers, add up their lanes in shared memory, and leave d numbers each; a
 // second kernel adds those up in one order, so that the result does not depend on
 // timing.
+//
+// Measured: 4 x 16 heads x 4096 rows of 128 columns in bf16: forward (134 MB) 28.7-29.4 us
+// a call, 4.6 TB/s; gradients (201 MB) 45-46 us, 4.4 TB/s; the warps' issue slots are 55 to
+// 60% busy, a third of that with the sines.  One token of 64 sequences appended (32 + 8
+// heads normed): 7.1-9 us, latency.
 #include "fa2_host.h"
 #include "fa2_launch.h"
 #include "fa2_norm.h"
@@ -334,8 +339,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) fa2_norm_append_kernel(const 
 }
 
 // Block b's places are norm_range(b) .. norm_range(b + 1) - 1: all (token tile, head)
-// places in equal shares, tiles outermost.  (A block for each tile with all its heads: 512 of them on 304 slots, 29
-// us instead of 27 for the 134 MB above.)
+// places in equal shares, tiles outermost.  (With a block for each tile and all its heads, 512 of them on 304
+// slots, the 134 MB took 32 us instead of 29.)
 __device__ __forceinline__ long long norm_range(long long places, long long b) { return places * b / gridDim.x; }
 
 // A block's walk over its places.
@@ -383,7 +388,8 @@ struct NormWalk {
 // its own slots of a ring in shared memory, kNormStages - 1 rows ahead of the one
 // that it works on, over the ends of tiles too.  Nothing there is another thread's, so
 // that waiting for one's own copies is all the order it takes.  (Rows ahead in
-// registers: two for y in 29 us and one of x and dy in 54, at the sizes above.)
+// registers: the gradients took 54 us instead of 45.5, the forward pass 29.2 as now.  Five
+// stages instead of three: 50 us and 28.7; three blocks per SM, which spill: 36 forward.)
 // Rows off 16-byte boundaries (W = 1) are loaded when it is their turn.
 constexpr int kNormStages = 3;
 constexpr int kNormBlocksPerSm = 2;

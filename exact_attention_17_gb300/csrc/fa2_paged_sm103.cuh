@@ -66,13 +66,20 @@
 //    token's window on (tiles, where pages are larger), one after the other: a list
 //    with one gap, whose tiles the schedule and the pipeline count in; only the
 //    copies and the masks look up which key it is.  Pages without a key that some row of
-//    the block sees are not in it.  (Whole tiles on both sides of the gap: 64 single
-//    tokens, window 2048 and 4 sinks in pages of 16, 101 us, see below.)  The cost of
+//    the block sees are not in it.  (Whole tiles on both sides of the gap: chunks of
+//    1-1024 tokens, window 1024 in pages of 32, 76 us instead of 62.)  The cost of
 //    a block is that of its keys, at most the longest list there can be, so that
 //    sums of costs stay closed forms.
 //    With a shared prefix one launch has the groups of sequences as its sequences (all
 //    their new tokens over the shared pages, without a mask) and the next the sequences
-//    over their own pages; see fa2_paged_api.cu.
+//    over their own pages; the CTAs note where they leave an item's parts, and a third
+//    kernel joins them row by row (fa2_paged_prefix.cu).
+//    Measured: 64 single tokens, window 2048: 99-100 us, 5.4 TB/s (the kernel alone 94, the
+//    merge 7); those chunks 61-66 us; 64 single tokens behind two prefixes of 13872 and 16384
+//    tokens, 20-2000 of their own: 93-96 us (45 for the groups, 37 for their own, 10 to join:
+//    each a start of 8 to 12 us and tiles at 2.9 us a CTA, 45 GB/s and SM); 8 single
+//    tokens behind 2000: 24-25 us; 24 chunks of 2-40 tokens behind 65536, d = 64: 158-163 us (131
+//    for the group, of which the exponentials alone are 86).
 //
 // Bound and measured.  Single tokens: bytes (64 sequences of 1000-8192 keys, 8
 // key/value heads of 128: 1.11 GB in 169.5-172 us, 6.48-6.57 TB/s; four of
