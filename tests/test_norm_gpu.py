@@ -363,3 +363,19 @@ def test_rows_beyond_32_bits():
         close(dx[0, h, n:n + 1], ref, rounded(bound, ref, BF))
         total, slacks = total + dw_, slacks + dw_bound
     close(dw, total, slacks)                      # (all other rows are zeros)
+
+
+def test_outputs_that_overlap_are_refused():
+    buffer = normal((2, 8, 65, 128), BF, 1)
+    w, pos, freq = normal((128,), BF, 3), torch.arange(64, device="cuda"), fa2.rope_inv_freq(128, device="cuda")
+    x, shifted = buffer[:, :, :64], buffer[:, :, 1:]
+    with pytest.raises(fa2.FA2Error):              # in place, but a row further
+        fa2.norm_rope(x, w, pos, freq, out=shifted)
+    with pytest.raises(fa2.FA2Error):
+        fa2.norm_rope_backward(x, x, w, pos, freq, dx=shifted)
+    with pytest.raises(fa2.FA2Error):              # rows of the output on one another
+        fa2.norm_rope(x, w, pos, freq, out=torch.zeros((2, 1, 64, 128), dtype=BF, device="cuda").expand(2, 8, 64, 128))
+    with pytest.raises(ValueError):
+        fa2.norm_rope(x, w[:64], pos, freq)
+    with pytest.raises(ValueError):
+        fa2.norm_rope(x, w.half(), pos, freq)
