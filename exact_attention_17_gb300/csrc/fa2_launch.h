@@ -18,10 +18,13 @@ namespace fa2host {
 // runs (when that one allows it, griddepcontrol.launch_dependents).  Every block
 // waits for the one before to end (griddepcontrol.wait) before it writes, and
 // before it reads what others may write, so that "complete" reaches back along the
-// stream.  One kernel reads earlier: the merge of the paged attention looks up
+// stream.  Kernels that read earlier: the merge of the paged attention looks up
 // lengths and offsets first.  They are complete by then, because the kernel before
 // it, which writes neither, lets it start only behind its own wait; a kernel that
-// is to do the same has to be behind one that keeps this order.
+// is to do the same has to be behind one that keeps this order.  With shared prefixes
+// the launch over the sequences' own pages runs beside the groups' (which starts it behind its
+// own wait, and whose results it does not touch) and waits for it at its end; the kernel that
+// joins them looks up offsets and groups first, as the merge does.
 template <typename... Params, typename... Args>
 cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int threads, unsigned smem, cudaStream_t s,
                           const Args&... args) {

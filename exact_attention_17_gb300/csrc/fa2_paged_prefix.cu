@@ -16,9 +16,9 @@ constexpr int kJoinRows = 8;   // rows of a block
 // A block has eight rows (token, query head) of one key/value head, a lane one row and
 // four of every 16 columns, so that reads are 128 neighbouring bytes at least; its
 // four warps take every fourth part each, in the order of the lists, and add up
-// through shared memory, always in the same order.  Whose token it is, its group
-// and the entries of its items are looked up by every lane for its row.  Bound: the
-// latency of those four dependent loads and of the parts'.
+// through shared memory, always in the same order.  Whose token it is and its group
+// are looked up by every lane for its row, while the launch before still runs; then
+// the entries of its items.  Bound: the latency of dependent loads, the parts' among them.
 template <int D, bool F16>
 __global__ void __launch_bounds__(kJoinWarps * 32) fa2_paged_join_kernel(const __grid_constant__ PagedParams pre,
                                                                          const __grid_constant__ PagedParams own,
@@ -26,8 +26,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) fa2_paged_join_kernel(const _
                                                                          float* LSE, int half_out) {
   __shared__ float4 sums[kJoinWarps - 1][D / 16][32];
   __shared__ float2 weights[kJoinWarps - 1][32];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = lane >> 3;
   const int head = blockIdx.y, G = own.G;
   const long long at = static_cast<long long>(blockIdx.x) * kJoinRows + (lane & 7);
@@ -49,6 +47,30 @@ __global__ void __launch_bounds__(kJoinWarps * 32) fa2_paged_join_kernel(const _
     q0 = max(0, own.cu_q[b]);
     live = live && q0 <= t && t < own.cu_q[b + 1];   // (else nobody's)
   }
+  // the group, as paged_shared finds it
+  int group_at = 0, group_begin = 0;
+  bool grouped = false;
+  if (live) {
+    int n = pre.groups;
+    while (n > 1) {
+      const int half = n / 2;
+      if (pre.cu_groups[group_at + half] <= b) {
+        group_at += half;
+        n -= half;
+      } else {
+        n = half;
+      }
+    }
+    const PagedGroup g = paged_group(pre, own.B, group_at);
+    if (g.prefix > 0 && g.first <= b && b < g.last) {
+      group_begin = own.cu_q != nullptr ? max(0, own.cu_q[g.first]) : g.first;
+      grouped = group_begin <= t;
+    }
+  }
+  // What was read above neither launch writes, and it was complete when they started; their
+  // results are complete from here on.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const long long row = static_cast<long long>(t) * own.Hq + head * G + h;
   struct List {
     int4 e;
@@ -71,21 +93,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) fa2_paged_join_kernel(const _
   List mine = {}, shared = {};
   if (live) {
     mine = look_up(own, q0, own_block, b);
-    int lo = 0, n = pre.groups;   // the group, as paged_shared finds it
-    while (n > 1) {
-      const int half = n / 2;
-      if (pre.cu_groups[lo + half] <= b) {
-        lo += half;
-        n -= half;
-      } else {
-        n = half;
-      }
-    }
-    const PagedGroup g = paged_group(pre, own.B, lo);
-    if (g.prefix > 0 && g.first <= b && b < g.last) {
-      const int begin = own.cu_q != nullptr ? max(0, own.cu_q[g.first]) : g.first;
-      if (begin <= t) shared = look_up(pre, begin, pre_block, lo);
-    }
+    if (grouped) shared = look_up(pre, group_begin, pre_block, group_at);
   }
   const int parts = mine.e.z + shared.e.z;
   float4 acc[D / 16];

@@ -79,7 +79,7 @@
 //    tokens, 20-2000 of their own: 93-96 us (45 for the groups, 37 for their own, 10 to join:
 //    each a start of 8 to 12 us and tiles at 2.9 us a CTA, 45 GB/s and SM); 8 single
 //    tokens behind 2000: 24-25 us; 24 chunks of 2-40 tokens behind 65536, d = 64: 158-163 us (131
-//    for the group, of which the exponentials alone are 86).
+//    for the group: 81 pairs of tiles a CTA at 1.6 us).
 //
 // Bound and measured.  Single tokens: bytes (64 sequences of 1000-8192 keys, 8
 // key/value heads of 128: 1.11 GB in 169.5-172 us, 6.48-6.57 TB/s; four of
@@ -894,8 +894,8 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
   // start (it finds its items and then waits for this grid to end).
   // EXT, a sequence's own pages: the kernel before is that of the shared prefix, whose
   // results this one does not read, and which started behind its own wait: the two
-  // run side by side, and this one waits for the other at its end (all of whose
-  // blocks are running by then).
+  // run side by side, and this one does not end before the other has (all of whose
+  // blocks are running by now): its first block waits for that.
   const bool beside = EXT && p.role == kPagedOwn;
   if (!beside) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1573,7 +1573,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
   }
 
   // ------------------------------------------------------------ teardown
-  if (beside) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (beside && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
   tc_fence_before_sync();
   __syncthreads();
   if (warp == kWarpMma) {
