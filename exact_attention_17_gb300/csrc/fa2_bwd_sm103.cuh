@@ -154,11 +154,11 @@ __global__ void __launch_bounds__(256) fa2_bwd_pre_kernel(const float* __restric
 // up in order.  Scores outside the mask are zeroed from one word of bits for
 // every 32 queries of a key, only in tiles that the mask cuts.
 // Bound as without a window (shared-memory bandwidth, tile by tile).  4 x 16 heads
-// sharing 4 x 4 over 4096 positions, window 1024, 4 sinks, d = 128, bf16 gradients: 525 us
-// a call, of which this kernel 445-450 for 19900 tiles (936 TFLOP/s of them, 678 of what is
+// sharing 4 x 4 over 4096 positions, window 1024, 4 sinks, d = 128, bf16 gradients: 507 us
+// a call, of which this kernel 430 for 19900 tiles (970 TFLOP/s of them, 700 of what is
 // seen: the tiles that the mask cuts, and the sinks' 2048 with 4 keys of 128); the pre-pass
 // 37 and the conversion behind it 35 move 268 and 201 MB.  (Items of 16 tiles instead of
-// 36: 595 us.  dQ over dP^T's columns, so that S^T(t+1) runs beside dS(t): 563.)
+// 36: 595 us to 542 then.  dQ over dP^T's columns, so that S^T(t+1) runs beside dS(t): 563 to 541.)
 template <int D, bool CAUSAL, bool F16, bool WINDOW = false>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     fa2_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -197,13 +197,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   int slot = -1;               // WINDOW: workspace slot, -1: the block's only item
   const int q_tiles = (p.Nq + 127) / 128;
   if constexpr (WINDOW) {
-    // blocks with sinks first (the longest lists); heads innermost but for a block's items
-    const int sink_items = p.BH * p.sink_blocks * p.sink_parts;
-    const bool with_sinks = static_cast<int>(blockIdx.x) < sink_items;
-    const int x = blockIdx.x - (with_sinks ? 0 : sink_items), n_parts = with_sinks ? p.sink_parts : p.parts;
+    // Groups of item_group heads, whose Q, dO and dQ then stay in L2 between the key blocks that use them; in a
+    // group blocks with sinks first (the longest lists), heads innermost but for a block's items.
+    const int per_head = p.sink_blocks * p.sink_parts + (p.key_blocks - p.sink_blocks) * p.parts;
+    const int g0 = static_cast<int>(blockIdx.x) / (p.item_group * per_head) * p.item_group;
+    const int heads = min(p.item_group, p.BH - g0);
+    const int in_group = blockIdx.x - g0 * per_head;
+    const int sink_items = heads * p.sink_blocks * p.sink_parts;
+    const bool with_sinks = in_group < sink_items;
+    const int x = in_group - (with_sinks ? 0 : sink_items), n_parts = with_sinks ? p.sink_parts : p.parts;
     const int part = x % n_parts, y = x / n_parts;
-    jb = y / p.BH;
-    bh = y - jb * p.BH;
+    jb = y / heads;
+    bh = g0 + (y - jb * heads);
+    if (n_parts > 1)
+      slot = (jb * p.BH + bh) * n_parts + part + (with_sinks ? 0 : p.BH * p.sink_blocks * p.sink_parts);
     if (!with_sinks) jb += p.sink_blocks;
     i0 = min(jb, q_tiles);
     const long long last = min(jb * 128 + 127, p.Nk - 1) + static_cast<long long>(p.window) - 1;   // query
@@ -213,7 +220,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     first = part * chunk;
     n_tiles = max(0, min(chunk, row_tiles * p.shared - first));
     head0 = bh * p.shared;
-    if (n_parts > 1) slot = blockIdx.x;
   } else {
     const int U = p.key_blocks;
     const int per_group = p.item_group * U;

@@ -34,6 +34,7 @@ int tiles_of(long long n) { return static_cast<int>((n + 127) / 128); }
 // How a backward call cuts its key blocks; depends on sizes and the number of SMs.
 struct BackwardPlan {
   int key_blocks, sink_blocks, parts, sink_parts, chunk, sink_chunk;
+  int group;                             // key/value heads whose blocks run together
   long long items;
   size_t dr_at, dq_at, part_at, bytes;   // workspace: LSE log2(e), D, dQ in fp32, parts
 };
@@ -43,6 +44,13 @@ struct BackwardPlan {
 // sinks sees every later tile of every head, so it is cut into many; the others
 // only where there are few.
 constexpr int kLeastChunk = 8;
+
+// Heads that run together: their query tiles in use (a window's, and one more for each
+// other key block of the heads that runs) have Q, dO and fp32 dQ in L2, four at least.  (4 x 4
+// key/value heads shared by 16, 4096 positions, window 1024, d = 128: 16 heads together
+// 525 us, 8 507, 4 519, 2 536; 8 of 16384 positions, window 4096: 2617, 4 2579, 2 2616.)
+constexpr long long kL2Bytes = 126ll << 20;
+constexpr long long kLeastGroup = 4;
 
 BackwardPlan plan_backward(const Window& w, bool grad_half, int sms) {
   BackwardPlan q;
@@ -61,6 +69,9 @@ BackwardPlan plan_backward(const Window& w, bool grad_half, int sms) {
   };
   cut(list, &q.parts, &q.chunk);
   cut(sink_list, &q.sink_parts, &q.sink_chunk);
+  const long long tile_bytes = shared * 128 * w.d * (2 + 2 + 4);
+  const long long g = (kL2Bytes / tile_bytes - sms) / (row < q_tiles ? row : q_tiles);
+  q.group = static_cast<int>(w.BHkv < kLeastGroup || g >= w.BHkv ? w.BHkv : g < kLeastGroup ? kLeastGroup : g);
   const long long sink_items = w.BHkv * q.sink_blocks * q.sink_parts;
   q.items = sink_items + w.BHkv * (q.key_blocks - q.sink_blocks) * q.parts;
   const size_t pad = static_cast<size_t>(q_tiles) * 128 * w.BH * 4;
@@ -206,6 +217,7 @@ extern "C" int fa2_backward_window(const void* Q, const void* K, const void* V, 
   p.Nq_pad = tiles_of(Nq) * 128;
   p.BH = bhkv;
   p.key_blocks = plan.key_blocks;
+  p.item_group = plan.group;
   p.scale = scale;
   p.scale_log2 = scale * kLog2e;
   p.status = fa2host::device_status_word();
