@@ -249,8 +249,8 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b, int b
     if (p.role == kPagedOwn && b < p.B) {
       bool bad = false;
       const int shared = paged_shared(p, p.B, b, &bad);
-      // the shared tokens lie before the new ones
-      if (blockIdx.x == 0 && (bad || shared > s.kv_len - s.q_len)) atomicOr(p.status, kDevErrPage);
+      // the shared tokens lie before the new ones (with nothing shared there may be more new tokens than positions)
+      if (blockIdx.x == 0 && (bad || (shared > 0 && shared > s.kv_len - s.q_len))) atomicOr(p.status, kDevErrPage);
       s.kv_len = max(0, s.kv_len - shared);
       s.page0 = shared >> p.page_log2;
     }

@@ -254,6 +254,20 @@ def test_groups_out_of_order_are_reported():
         assert status() == fa2.FA2_ERR_PAGE, (cu, lens)
 
 
+def test_more_new_tokens_than_positions_beside_groups():
+    """Sequences that share nothing (outside all groups, alone in one, or in one without a prefix) are plain attention's."""
+    q_lens, kv = [5, 3, 3, 9, 40, 2], [4, 100, 110, 2, 30, 1]
+    for cu_groups, prefix_lens in (([1, 3, 4], [96, 0]), ([1, 3, 3, 6], [96, 0, 0])):
+        cache = Cache(kv, 2, 16, 64, BF, seed=5)
+        share(cache, cu_groups, prefix_lens)
+        q = normal((sum(q_lens), 8, 64), BF, 1)
+        got = fa2.forward_paged_prefix(q, cache.k, cache.v, cache.table, cache.lens, ints(cu_groups), ints(prefix_lens),
+                                       cu_q=offsets(q_lens), out_dtype=F32)
+        masks = [sees(n, length, 1 << 30, 0) for n, length in zip(q_lens, kv)]
+        compare(got, paged(q, cache.keys, cache.values, q_lens, masks, 0.125, EPS[F32], parts=2), sum(q_lens))
+        assert status() == fa2.FA2_OK
+
+
 def test_samples_of_one_prompt():
     """A prompt, forked into samples (pages_fork), then steps of append and attention with the prompt shared, captured
     and replayed: as attention without sharing."""
