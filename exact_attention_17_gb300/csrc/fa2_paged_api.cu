@@ -1,5 +1,7 @@
 // Host side of the paged-cache entry points (include/fa2.h): argument
 // validation, tensor maps, launch plans.
+#include <algorithm>
+
 #include "fa2_checks.h"
 #include "fa2_launch.h"
 #include "fa2_norm.h"
@@ -28,6 +30,15 @@ int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 // mean 1.1; above 0.77 to 1.07, mean 0.9.
 constexpr int kItemWaves = 4;
 constexpr int kItemWaves256 = 2;
+// With a window items cost nearly the same, so that their last wave is short; what it
+// loses grows with the keys that an item sees (window and sinks), and so do the waves from
+// which items are whole: 1 + (keys / 2048)^2, at most those above.  60000 random ragged
+// batches (2 to 60 sequences, groups of 1 to 8, windows of 128 to 4096), equal ranges / whole
+// at 1-1.25, 1.25-1.5, 1.5-2, 2-3 and 3-4 waves, geometric means: d = 128, windows to
+// 256 1.04, 1.06, 1.08, 1.06, 1.05; 512 and 1024 1.00, 1.04, 1.09, 1.09, 1.08; 1536 and 2048
+// 0.93, 0.96, 1.01, 1.06, 1.07; above 0.89, 0.92, 0.94, 0.98, 1.02.  d = 64 0.02 less, d =
+// 256 0.03 to 0.1 more.
+constexpr long long kItemReach = 2048;
 // The three below from 40 random batches each (1 to 300 sequences of 20 to 60000
 // keys, every head size, groups of 1 to 8; geometric mean of the times against the
 // value taken, worst and best batch).
@@ -48,7 +59,8 @@ constexpr int kItemKeysNarrow = 256;
 // take 149 us together, 109 and 58 apart, but a chunk that is long for the average
 // is cut into blocks of 32 rows (1024 single tokens over 100-500 keys and a chunk of
 // 7000: 1497 us, 252 and 319 apart).
-PagedPlan plan_paged(int B, int T, int Hq, int Hkv, int d, bool has_cu, int sms) {
+// reach: keys that a query of a windowed call may see (0: no window); decides `even` alone.
+PagedPlan plan_paged(int B, int T, int Hq, int Hkv, int d, bool has_cu, int sms, long long reach = 0) {
   PagedPlan q;
   q.G = Hq / Hkv;
   q.subs = has_cu && d != 256 && static_cast<long long>(T) * q.G > 128ll * B ? 2 : 1;
@@ -62,7 +74,9 @@ PagedPlan plan_paged(int B, int T, int Hq, int Hkv, int d, bool has_cu, int sms)
   q.items = (has_cu ? T / block + static_cast<long long>(B < T ? B : T) : B) * Hkv;
   q.ctas = sms * (q.subs == 2 || d == 256 ? 1 : 2);
   const long long waves = d == 256 ? kItemWaves256 : kItemWaves;
-  q.even = q.narrow || !has_cu || T / block * static_cast<long long>(Hkv) < waves * q.ctas;
+  const long long whole = T / block * static_cast<long long>(Hkv);
+  const bool short_items = reach > 0 && (whole - q.ctas) * kItemReach * kItemReach >= reach * reach * q.ctas;
+  q.even = q.narrow || !has_cu || (whole < waves * q.ctas && !short_items);
   q.slots = 2 * q.ctas;
   const long long rows = static_cast<long long>(has_cu ? (T < block ? T : block) : 1) * q.G;
   q.part_rows = static_cast<int>(rows);
@@ -210,7 +224,10 @@ int forward_paged(const PagedCall& a, int window, int sinks, cudaStream_t s) {
   int rc;
   if ((rc = fa2host::require_device()) != FA2_OK) return rc;
   const fa2_paged_cache& c = *a.cache;
-  const PagedPlan plan = plan_paged(c.B, a.T, a.Hq, c.kv_heads, c.d, a.cu_q != nullptr, fa2host::device_sms());
+  const long long longest = static_cast<long long>(c.table_width) * c.page_size;
+  const long long keys = std::min<long long>(window, longest) + std::min<long long>(sinks, longest);
+  const PagedPlan plan = plan_paged(c.B, a.T, a.Hq, c.kv_heads, c.d, a.cu_q != nullptr, fa2host::device_sms(),
+                                    window > 0 ? std::min(keys, 1ll << 20) : 0);
   if ((rc = check_call_memory(a, plan.bytes)) != FA2_OK) return rc;
   PagedMaps maps;
   fa2dev::PagedParams p;

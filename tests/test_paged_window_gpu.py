@@ -124,6 +124,22 @@ def test_many_items():
     assert status() == fa2.FA2_OK
 
 
+@pytest.mark.parametrize("d, Hkv", [(64, 8), (128, 8), (256, 4)])
+def test_few_waves_of_short_windows(d, Hkv):
+    """Between one and two waves of ragged blocks, sequences without new tokens and short ones among them."""
+    q_lens = [700, 0, 1, 1500, 256, 257, 900, 33, 2100, 0, 640, 5]
+    kv = [n + 97 * i for i, n in enumerate(q_lens)]
+    cache = Cache(kv, Hkv, 16, d, BF, seed=7)
+    assert forget(cache, q_lens, 100, 4) > 0
+    q = normal((sum(q_lens) + 2, Hkv, d), BF, 1)
+    out = torch.full(q.shape, 7.0, dtype=BF, device="cuda")
+    got = fa2.forward_paged_window(q, cache.k, cache.v, cache.table, cache.lens, 100, 4, cu_q=offsets(q_lens), out=out,
+                                   out_dtype=BF)
+    masks = [sees(n, length, 100, 4) for n, length in zip(q_lens, kv)]
+    compare(got, paged(q, cache.keys, cache.values, q_lens, masks, 1.0 / math.sqrt(d), EPS[BF]), sum(q_lens))
+    assert (out[sum(q_lens):] == 7.0).all() and status() == fa2.FA2_OK
+
+
 def test_a_window_of_everything_is_plain_attention():
     q_lens, kv = [70, 1, 300], [500, 900, 300]
     cache = Cache(kv, 2, 16, 128, BF, seed=4)
