@@ -288,7 +288,7 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 
 // stream the tiles of the first one's list and what the second needs behind it; scores outside a row's keys
 // are masked from one word of bits for every 32 keys.  Every sub-tile with rows visits a tile, so that rows without
 // a key (far behind the last one) get their O = 0 and LSE = -inf on the ordinary way.
-// 32 heads sharing 8 over 16384 positions, d = 128, window 4096, 4 sinks: 674-711 us, 1350-1430
+// 32 heads sharing 8 over 16384 positions, d = 128, window 4096, 4 sinks: 674-716 us, 1340-1430
 // TFLOP/s of what is seen (a CTA visits 69 tiles for 64.5, and starts and ends alone on its SM:
 // without a window 1720).  1000 positions of 64 columns, 16 heads: 9.4-11 us, latency.
 template <int D, bool CAUSAL, bool F16, int SUBS, bool WINDOW = false>

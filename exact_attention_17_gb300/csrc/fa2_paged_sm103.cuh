@@ -74,11 +74,11 @@
 //    their new tokens over the shared pages, without a mask) and the next the sequences
 //    over their own pages; the CTAs note where they leave an item's parts, and a third
 //    kernel joins them row by row (fa2_paged_prefix.cu).
-//    Measured: 64 single tokens, window 2048: 99-100 us, 5.4 TB/s (the kernel alone 94, the
-//    merge 7); those chunks 61-66 us; 64 single tokens behind two prefixes of 13872 and 16384
+//    Measured: 64 single tokens, window 2048: 97-100 us, 5.4 TB/s (the kernel alone 94, the
+//    merge 7); those chunks 62-63 us; 64 single tokens behind two prefixes of 13872 and 16384
 //    tokens, 20-2000 of their own: 91-95 us (45 for the groups, 37 for their own, 10 to join:
 //    each a start of 8 to 12 us and tiles at 2.9 us a CTA, 45 GB/s and SM); 8 single
-//    tokens behind 2000: 22.7-24 us; 24 chunks of 2-40 tokens behind 65536, d = 64: 158-163 us (131
+//    tokens behind 2000: 21.3-24 us; 24 chunks of 2-40 tokens behind 65536, d = 64: 158-163 us (131
 //    for the group: 81 pairs of tiles a CTA at 1.6 us).
 //
 // Bound and measured.  Single tokens: bytes (64 sequences of 1000-8192 keys, 8
