@@ -542,10 +542,15 @@ __global__ void __launch_bounds__(kRopeThreads, fa2host::kNormGradBlocksPerSm)
   constexpr int C = kOther ? E2 / 2 : E2;
   float2 own[C], cross[C];
   unsigned turned = 0;
+  // A row that is not there is zeros, whose r would be infinite with eps = 0, and 0 r no number: 1 takes the place of
+  // eps.  (W = 1 keeps it for a tile: with the choice at every row the compiler orders the loads so that rows off
+  // 16-byte boundaries take 150 us instead of 125.  The vectors' kernel has no register left for it.)
+  float eps = np.eps;
   bool fresh = true;
   int stage = 0;
   while (work.more()) {
     if (fresh) {
+      eps = work.live ? np.eps : 1.f;
       float2 turns[S::PAIRS];
       const long long i = work.batch * p.pos_batch + work.n;
       const long long pos = p.pos64 ? static_cast<const long long*>(p.positions)[i] : static_cast<const int*>(p.positions)[i];
@@ -623,12 +628,12 @@ __global__ void __launch_bounds__(kRopeThreads, fa2host::kNormGradBlocksPerSm)
       square += __shfl_xor_sync(0xffffffffu, square, o);
       dot += __shfl_xor_sync(0xffffffffu, dot, o);
     }
-    const float r = rsqrtf(fmaf(square, 1.f / D, np.eps));
+    const float r = rsqrtf(fmaf(square, 1.f / D, Feed::kAsync ? (work.live ? np.eps : 1.f) : eps));
     const float along = -dot * (1.f / D) * r * r * r;
     const float2 r2 = make_float2(r, r), along2 = make_float2(along, along);
 #pragma unroll
     for (int i = 0; i < E2; ++i) {
-      dw[i] = fma2(fg[i], mul2(fx[i], r2), dw[i]);   // (rows that are not there are zeros)
+      dw[i] = fma2(fg[i], mul2(fx[i], r2), dw[i]);   // (a row that is not there adds 0)
       h[i] = fma2(h[i], r2, mul2(fx[i], along2));
     }
     if (work.live) {

@@ -496,10 +496,10 @@ int fa2_append_paged(const fa2_paged_cache *cache, const void *K, const long lon
  *     y = R(t) (w x r),  r = 1 / sqrt(sum_c x_c^2 / d + eps),
  * R(t) being the rotation of fa2_rope (mscale and columns beyond rotary_dim as
  * there).  Sums are fp32 (of squares too: rows of elements beyond 1e18 overflow
- * it), products are fp32 and rounded once.
+ * it, and rows below 1e-19 count as zeros), products are fp32 and rounded once.
  *   X, Y       as fa2_rope, but d = 64, 128 or 256 and pairs without an alignment of their own
  *   weight     [d] of the rows' type or fp32 (weight_dtype)
- *   eps        finite, not negative
+ *   eps        finite, not negative; with 0 a row of zeros is NaN, and so are its gradients and dweight
  * Rows whose starts and strides are multiples of 16 bytes, with whole 16-byte
  * vectors of rotated columns (rotary_dim a multiple of 16 elements of 16 bits, of
  * 8 interleaved or in fp32, of 4 in fp32 interleaved), take the fast way.
