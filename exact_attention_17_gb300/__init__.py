@@ -73,6 +73,7 @@ SIGNATURES = {
     "fa2_status_string": (ctypes.c_char_p, [_I]),
     "fa2_device_status": (_I, [_P, _I]),
     "fa2_check_wait_timeout": (_I, [ctypes.c_ulonglong, _P]),
+    "fa2_check_window_plan": (_I, [_I] * 9 + [_P]),
 }
 
 

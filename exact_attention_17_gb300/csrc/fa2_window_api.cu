@@ -239,3 +239,18 @@ extern "C" int fa2_backward_window(const void* Q, const void* K, const void* V, 
     return FA2_ERR_LAUNCH;
   return FA2_OK;
 }
+
+extern "C" int fa2_check_window_plan(int B, int H, int Hkv, int Nq, int Nk, int d, int window, int sinks, int sm_count,
+                                     int* plan) {
+  Window w;
+  const int rc = check_window(B, H, Hkv, Nq, Nk, d, window, sinks, 1.f, FA2_DTYPE_BF16, false, &w);
+  if (rc != FA2_OK) return rc;
+  if (w.BH == 0 || Nq == 0 || sm_count < 1) return FA2_ERR_SHAPE;
+  if (!plan) return FA2_ERR_NULL;
+  const BackwardPlan q = plan_backward(w, false, sm_count);
+  plan[0] = sub_tiles(w, sm_count);
+  plan[1] = q.group;
+  plan[2] = q.parts;
+  plan[3] = q.sink_parts;
+  return FA2_OK;
+}

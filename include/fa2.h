@@ -642,6 +642,16 @@ int fa2_device_status(fa2_stream_t stream, int reset);
  */
 int fa2_check_wait_timeout(unsigned long long timeout_ns, fa2_stream_t stream);
 
+/*
+ * The form that fa2_forward_window and fa2_backward_window take for these sizes (not empty)
+ * on a device of sm_count SMs, for tests that must reach a certain one.  Host only.
+ *   plan   [4] on the host: query sub-tiles of a CTA of the forward pass; of the gradients
+ *          key/value heads that run together, items of a key block without sinks, and of one
+ *          with sinks
+ */
+int fa2_check_window_plan(int B, int H, int Hkv, int Nq, int Nk, int d, int window, int sinks,
+                          int sm_count, int *plan);
+
 #ifdef __cplusplus
 }
 #endif
