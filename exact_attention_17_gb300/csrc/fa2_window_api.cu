@@ -46,9 +46,12 @@ struct BackwardPlan {
 constexpr int kLeastChunk = 8;
 
 // Heads that run together: their query tiles in use (a window's, and one more for each
-// other key block of the heads that runs) have Q, dO and fp32 dQ in L2, four at least.  (4 x 4
-// key/value heads shared by 16, 4096 positions, window 1024, d = 128: 16 heads together
-// 525 us, 8 507, 4 519, 2 536; 8 of 16384 positions, window 4096: 2617, 4 2579, 2 2616.)
+// other key block of the heads that runs) have Q, dO and fp32 dQ in L2, four at least;
+// groups of one size, unless that is less than four.  (Window 1024, d = 128, 4096 positions,
+// 16 key/value heads shared by 4 each, of which 11 fit: 16 heads together 525 us, 11 and 5
+// 511, twice 8 507, 4 519, 2 536; 12 heads: 11 and 1 455, twice 6 439.5; 5 heads shared by 8:
+// 4 and 1 373, 3 and 2 374.  6 heads of 8192 positions, window 2048: 5 and 1 652, 4 and 2
+// 657, twice 3 666; 8 of 16384, window 4096: all 2617, 4 2579, 2 2616.)
 constexpr long long kL2Bytes = 126ll << 20;
 constexpr long long kLeastGroup = 4;
 
@@ -71,7 +74,9 @@ BackwardPlan plan_backward(const Window& w, bool grad_half, int sms) {
   cut(sink_list, &q.sink_parts, &q.sink_chunk);
   const long long tile_bytes = shared * 128 * w.d * (2 + 2 + 4);
   const long long g = (kL2Bytes / tile_bytes - sms) / (row < q_tiles ? row : q_tiles);
-  q.group = static_cast<int>(w.BHkv < kLeastGroup || g >= w.BHkv ? w.BHkv : g < kLeastGroup ? kLeastGroup : g);
+  const long long fit = g < kLeastGroup ? kLeastGroup : g, groups = (w.BHkv + fit - 1) / fit;
+  const long long equal = (w.BHkv + groups - 1) / groups;
+  q.group = static_cast<int>(groups == 1 || equal >= kLeastGroup ? equal : fit);
   const long long sink_items = w.BHkv * q.sink_blocks * q.sink_parts;
   q.items = sink_items + w.BHkv * (q.key_blocks - q.sink_blocks) * q.parts;
   const size_t pad = static_cast<size_t>(q_tiles) * 128 * w.BH * 4;
