@@ -59,8 +59,8 @@ __global__ void __launch_bounds__(256) fa2_bwd_window_pre_kernel(const void* O, 
   }
 }
 
-// dQ from fp32 to the input type (blocks from `key_blocks_from` on: see the launch), and
-// sums of the items of the key blocks that were cut: key row, four columns a thread.
+// dQ from fp32 to the input type (the first `dq_blocks` blocks of the grid), and sums of the
+// items of the key blocks that were cut: key row, four columns a thread.
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) fa2_bwd_window_end_kernel(const __grid_constant__ BwdParams p,
                                                                  uint2* dq_out, long long q_quads,
