@@ -20,8 +20,10 @@
 //
 // Measured: 4 x 16 heads x 4096 rows of 128 columns in bf16: forward (134 MB) 28.7-29.4 us
 // a call, 4.6 TB/s; gradients (201 MB) 45-46 us, 4.4 TB/s; the warps' issue slots are 55 to
-// 60% busy, a third of that with the sines.  One token of 64 sequences appended (32 + 8
-// heads normed): 7.1-9 us, latency.
+// 60% busy, a third of that with the sines.  The same rows in fp32 (twice the bytes): 45.7 and
+// 67.4 us, 5.9 and 6.0 TB/s.  Rows off 16-byte boundaries, or 20 rotated columns (W = 1, an element a
+// load): 99 and 125 us, in fp32 103 and 127.  One token of 64 sequences appended (32 + 8
+// heads normed): 7.1-9 us, latency; 8192 tokens of a prompt (201 MB): 43.4 us, 41.1 without the norm.
 #include "fa2_host.h"
 #include "fa2_launch.h"
 #include "fa2_norm.h"

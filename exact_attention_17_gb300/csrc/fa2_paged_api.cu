@@ -294,7 +294,9 @@ PrefixPlan plan_prefix(int B, int groups, int T, int Hq, int Hkv, int d, bool ha
   PrefixPlan q;
   q.prefix = plan_paged(groups, T, Hq, Hkv, d, true, sms);
   q.own = plan_paged(B, T, Hq, Hkv, d, has_cu, sms);
-  q.prefix.even = q.own.even = true;   // (a counter would need clearing between two launches that run side by side)
+  // Equal ranges at any size: whole items win from four waves of blocks on, where the products take the time and
+  // a call without sharing is faster anyway (16 chunks of 512 behind 8192: 1055 us, 776 without).
+  q.prefix.even = q.own.even = true;
   q.own_at = align256(q.prefix.bytes);
   size_t at = q.own_at + align256(q.own.bytes);
   const size_t rows = static_cast<size_t>(T) * Hq;

@@ -92,6 +92,7 @@ BackwardPlan plan_backward(const Window& w, bool grad_half, int sms) {
 // per SM, whose starts and ends overlap the other's work) for short windows.  16384
 // positions, 32 heads sharing 8, two sub-tiles / one: d = 128, windows of 128, 1024 and 4096:
 // 146 / 114, 281 / 277 and 663 / 797 us; d = 64: 127 / 91, 254 / 214 and 592 / 590, 16384: 1197 / 1259.
+// d = 256 has TMEM for one: windows of 1024 and 4096 610 and 1815 us (870 and 1063 TFLOP/s of what is seen).
 int sub_tiles(const Window& w, int sms) {
   if (w.Nq <= 128 || w.d == 256 || w.window <= (w.d == 64 ? 4096 : 1024)) return 1;
   return (static_cast<long long>(w.Nq) + 255) / 256 * w.BH < 2ll * sms ? 1 : 2;

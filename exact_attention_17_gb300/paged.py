@@ -288,6 +288,12 @@ def forward_paged_prefix(q, k_pages, v_pages, page_table, kv_lens, cu_groups, pr
     are read once for the group.  The part of a prefix behind its last whole
     page is read from each sequence's own pages.  The other arguments are
     ``forward_paged``'s; so are the results, but for the order of the sums.
+
+    It pays for single tokens and short chunks (up to about 80 rows a sequence: new
+    tokens times the query heads of a key/value head) where ``forward_paged`` on the same
+    table would read more than 200 MB of a group's keys and values again (32 single tokens behind
+    8192 with 8 key/value heads of 128: 36 us instead of 110; 8 behind 2000: 22 instead of 19).
+    Longer chunks, a prompt's among them, are faster in ``forward_paged``.
     """
     if torch is None:
         _load()

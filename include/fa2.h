@@ -434,6 +434,10 @@ int fa2_forward_paged_window(const fa2_paged_cache *cache, const void *Q, long l
  *   cu_groups    device int32 [groups + 1], ascending, within 0 .. B
  *   prefix_lens  device int32 [groups]
  *   groups       0 .. B (0: fa2_forward_paged)
+ * When it pays against fa2_forward_paged on the same table (which gives the same results and reads
+ * shared pages again for every sequence, from L2 where they fit): with up to about 80 rows (new
+ * tokens times heads of a group) a sequence, once a group would read more than 200 MB of keys
+ * and values again.  With longer chunks the products, not the bytes, take the time, and it is slower.
  *   workspace    at least fa2_forward_paged_prefix_workspace_bytes
  * Groups out of order, lengths outside the table and prefixes that reach into a
  * sequence's new tokens are reported (FA2_ERR_PAGE); the rows concerned are undefined.
