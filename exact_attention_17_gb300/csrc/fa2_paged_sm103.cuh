@@ -149,8 +149,20 @@ constexpr int kPagedPlain = 0;
 constexpr int kPagedPrefix = 1;   // the new tokens of groups of sequences over the groups' shared pages
 constexpr int kPagedOwn = 2;      // the new tokens of each sequence over its pages behind the shared ones
 
+// EXT: key x of the list is key x (x < sink_keys) or x + skip.  (The other kernels keep no such fields: with them
+// two tokens over 1000 keys took 14.4 us instead of 14.3, 8192 over 16384 keys 1071 instead of 1067.)
+template <bool EXT>
+struct PagedGap {
+  int sink_keys, skip;
+};
+template <>
+struct PagedGap<false> {
+  static constexpr int sink_keys = 0, skip = 0;
+};
+
 // Key tiles [t_begin, t_end) of an item; EXT: of its list.
-struct PagedUnit {
+template <bool EXT>
+struct PagedUnit : PagedGap<EXT> {
   int valid;
   int head;
   int row0;       // first token of the block in the packed queries
@@ -160,7 +172,6 @@ struct PagedUnit {
   int t_begin, t_end;
   int slot;       // workspace slot of this part, -1: the whole item
   long long table;   // offset of the sequence's row in the page table
-  int sink_keys, skip;   // EXT: key x of the list is key x (x < sink_keys) or x + skip
 };
 
 // Keys that the token `tok` of a sequence keeps: [0, kept).
@@ -297,14 +308,14 @@ __device__ __forceinline__ long long cost_before(const PagedParams& p, const Pag
     const long long lead = static_cast<long long>(s.kv_len) - s.q_len;
     const int none = lead >= 0 ? 0 : min(full, static_cast<int>(-lead) / block);   // blocks without a key count one
     long long n = full - none;
-    keys = none;
+    keys = 0;
     if constexpr (EXT) {   // blocks whose keys are as many as any block's (lead + (k + 1) block > most_keys)
       const long long below = lead > p.most_keys ? 0 : (p.most_keys - lead) / block;
       const long long most = max(0ll, min(n, full - below));
       keys += most * p.most_keys;
       n -= most;
     }
-    keys += n * (lead + none * static_cast<long long>(block)) + block * (n * (n + 1) / 2);
+    keys += none + n * (lead + none * static_cast<long long>(block)) + block * (n * (n + 1) / 2);
   } else {
     keys = static_cast<long long>(full) * max(1, EXT ? min(s.kv_len, p.most_keys) : s.kv_len);
   }
@@ -473,9 +484,9 @@ __device__ __forceinline__ PagedPlace paged_find(const PagedParams& p, const Pag
 }
 
 template <bool EXT>
-__device__ __forceinline__ PagedUnit paged_unit(const PagedParams& p, const PagedSeq& s, int b, int head, int block,
-                                                int i) {
-  PagedUnit u;
+__device__ __forceinline__ PagedUnit<EXT> paged_unit(const PagedParams& p, const PagedSeq& s, int b, int head,
+                                                     int block, int i) {
+  PagedUnit<EXT> u;
   u.valid = 1;
   u.head = head;
   u.q_len = s.q_len;
@@ -496,16 +507,17 @@ __device__ __forceinline__ PagedUnit paged_unit(const PagedParams& p, const Page
 // Whole warp: walks the segments of range `cta` (even).  A part that begins inside an
 // item goes to slot 2 cta, one that begins it and does not end it to slot 2 cta
 // + 1: a range has at most one of each.
+template <bool EXT>
 struct PagedWalk {
   PagedPlace at;
   long long lo, hi;   // the range
   int cta;
   long long share, total;   // EXT: of a range, of the list
 
-  template <int SUBS, bool EXT>
-  __device__ __forceinline__ PagedUnit next(const PagedParams& p) {
+  template <int SUBS>
+  __device__ __forceinline__ PagedUnit<EXT> next(const PagedParams& p) {
     const int lane = threadIdx.x & 31;
-    PagedUnit u;
+    PagedUnit<EXT> u;
     u.valid = 0;
     while (lo < hi && !u.valid) {
       const int from = at.tile(p, lo), to = at.tile(p, hi);
@@ -559,8 +571,8 @@ struct PagedWalk {
 };
 
 template <int SUBS, bool EXT>
-__device__ __forceinline__ PagedWalk paged_walk(const PagedParams& p, int cta) {
-  PagedWalk w;
+__device__ __forceinline__ PagedWalk<EXT> paged_walk(const PagedParams& p, int cta) {
+  PagedWalk<EXT> w;
   long long total;
   const PagedStrips f = paged_strips<SUBS, EXT>(p);
   const long long share = paged_share<SUBS, EXT>(p, f, &total);
@@ -575,16 +587,17 @@ __device__ __forceinline__ PagedWalk paged_walk(const PagedParams& p, int cta) {
 
 // Parts of an item that the merge reads: the first in slot `first`, the others
 // in `rest`, `rest` + step, ...
+template <bool EXT>
 struct PagedParts {
-  PagedUnit u;
+  PagedUnit<EXT> u;
   int parts, first, rest, step;
 };
 
 // Whole warp: the item that the boundary between the ranges `index` and `index`
 // + 1 cuts, when it is the first boundary to do so; otherwise u.valid = 0.
 template <int SUBS, bool EXT>
-__device__ __forceinline__ PagedParts paged_parts_even(const PagedParams& p, int index) {
-  PagedParts r;
+__device__ __forceinline__ PagedParts<EXT> paged_parts_even(const PagedParams& p, int index) {
+  PagedParts<EXT> r;
   r.u.valid = 0;
   long long total;
   const PagedStrips f = paged_strips<SUBS, EXT>(p);
@@ -615,7 +628,7 @@ struct PageCursor {
   int log2_tile;   // EXT: log2 of a tile's entries
   int sinks, skip; // EXT: the list's gap, in entries
 
-  __device__ __forceinline__ PageCursor(const PagedParams& p, const PagedUnit& w, int tiles) {
+  __device__ __forceinline__ PageCursor(const PagedParams& p, const PagedUnit<EXT>& w, int tiles) {
     table = p.page_table + (tiles > 0 ? w.table : 0);
     live = tiles > 0 ? (w.kv_len + (1 << p.page_log2) - 1) >> p.page_log2 : 0;
     if constexpr (EXT) {
@@ -666,7 +679,7 @@ constexpr long long kPagedL2Bytes = 64ll << 20;
 // rank `index` among those cut into several units (items = true; its parts are
 // in slots first, first + 1, ...).
 template <int SUBS, bool EXT>
-__device__ __forceinline__ PagedParts paged_item(const PagedParams& p, int index, bool items, int D) {
+__device__ __forceinline__ PagedParts<EXT> paged_item(const PagedParams& p, int index, bool items, int D) {
   const int lane = threadIdx.x & 31;
   const int block = p.sub_tokens * SUBS;
   long long total = 0;
@@ -678,7 +691,7 @@ __device__ __forceinline__ PagedParts paged_item(const PagedParams& p, int index
   const int per_unit = static_cast<int>(
       min(max((total + p.ctas - 1) / p.ctas, static_cast<long long>(p.min_tiles)), 1ll << 24));   // more than any length
 
-  PagedParts r;
+  PagedParts<EXT> r;
   r.u.valid = 0;
   r.step = 1;
   int before = 0, slots_before = 0;
@@ -759,11 +772,11 @@ struct PagedConfig : FwdConfig<D, SUBS> {
   static constexpr int kSegmentThreads = SUBS * 128 + 64 + (Base::kNamedP ? 32 : 0);
 };
 
-template <int STAGES>
+template <int STAGES, bool EXT>
 struct alignas(8) PagedShared {
   FwdBarriers<STAGES> bars;
   uint64_t q_empty;
-  PagedUnit unit[2];   // segment k in unit[k % 2]
+  PagedUnit<EXT> unit[2];   // segment k in unit[k % 2]
   float2 shares[4][32];   // NARROW: (m, l) of the warps' rows
 };
 
@@ -785,7 +798,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
   constexpr uint32_t TILE = Cfg::kTileBytes;
   constexpr int NCH = Cfg::kChunks;
   constexpr uint32_t kChunkBytes = kRowsPerSub * 128;  // one 64-column chunk of a 128-row tile
-  static_assert(sizeof(PagedShared<STAGES>) <= 2048, "barrier page");
+  static_assert(sizeof(PagedShared<STAGES, EXT>) <= 2048, "barrier page");
   static_assert(!NARROW || SUBS == 1, "narrow blocks have one sub-tile");
 
   extern __shared__ uint8_t smem_raw[];
@@ -793,7 +806,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sQ = smem;                  // SUBS sub-tiles
   uint8_t* sKV = smem + SUBS * TILE;   // STAGES tiles
-  auto* shared = reinterpret_cast<PagedShared<STAGES>*>(smem + Cfg::kSmemBars);
+  auto* shared = reinterpret_cast<PagedShared<STAGES, EXT>*>(smem + Cfg::kSmemBars);
   auto* bars = &shared->bars;
   volatile int* abort = &bars->abort;
 
@@ -801,7 +814,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
   const int lane = threadIdx.x & 31;
 
   // key tiles that sub-tile `sub` of unit w visits
-  auto tiles_for = [&](const PagedUnit& w, int sub) {
+  auto tiles_for = [&](const PagedUnit<EXT>& w, int sub) {
     const int first = sub * p.sub_tokens;
     if (first >= w.ntok) return 0;
     const int last = min(first + p.sub_tokens, w.ntok) - 1;
@@ -819,14 +832,14 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
   // key tile `tile`, which lies at or behind the cursor.  Everything is ready
   // before the wait for the slot: instructions after it delay every tile.
   int last[2] = {-1, -1};   // this warp's last copies of K and of V
-  auto copy = [&](auto C0, auto C1, const PagedUnit& w, PageCursor<EXT>& pages, int tile, int index, bool& ok) {
+  auto copy = [&](auto C0, auto C1, const PagedUnit<EXT>& w, PageCursor<EXT>& pages, int tile, int index, bool& ok) {
     constexpr int kFirst = decltype(C0)::value, kEnd = decltype(C1)::value;
     const int slot = index % STAGES, lap = index / STAGES;
     const int slots_log2 = min(p.page_log2, 7);   // slots of a page that the tile reads
     int count;
     const int id = pages.tile(p, tile, &count);
     const CUtensorMap* map = (index & 1) == 0 ? &tm_k : &tm_v;
-    const int row = pages.row(p, tile);
+    const int row = EXT ? pages.row(p, tile) : (tile << 7) & ((1 << p.page_log2) - 1);
     uint8_t* dst = sKV + slot * TILE + (static_cast<uint32_t>(lane) << slots_log2) * 128;
     const uint32_t bytes = static_cast<uint32_t>(count * (kEnd - kFirst)) * (128u << slots_log2);
     if (lap > 0) warp_wait(&bars->kv_empty[slot], (lap - 1) & 1, ok);
@@ -843,8 +856,8 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
   };
   // Three producers: their chunks of K and of V.  In the order of the MMAs: K(j+1),
   // whose slot S(j) frees, then V(j), whose slot P(j-1) V frees.
-  auto copy_three = [&](auto K0, auto K1, auto V0, auto V1, const PagedUnit& w, int n, int tiles, PageCursor<EXT>& k_pages,
-                        PageCursor<EXT>& v_pages, int first, bool& ok) {
+  auto copy_three = [&](auto K0, auto K1, auto V0, auto V1, const PagedUnit<EXT>& w, int n, int tiles,
+                        PageCursor<EXT>& k_pages, PageCursor<EXT>& v_pages, int first, bool& ok) {
     for (int j = first; j <= n && ok; ++j) {
       if (j < n) copy(K0, K1, w, k_pages, w.t_begin + j, 2 * (tiles + j), ok);
       if (j > 0 && ok) copy(V0, V1, w, v_pages, w.t_begin + j - 1, 2 * (tiles + j) - 1, ok);
@@ -905,10 +918,10 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
     if (warp == kWarpProducer) {
       // ------------------------------------------------------------ schedule and copies
       constexpr int kMine = Cfg::kThree ? 2 : Cfg::kTwo ? 1 : NCH;   // chunks of K that this warp copies
-      PagedWalk walk;
+      PagedWalk<EXT> walk;
       bool begun = false;
       auto next_unit = [&]() {
-        if (NARROW || p.even) return walk.next<SUBS, EXT>(p);   // (narrow blocks always have equal ranges)
+        if (NARROW || p.even) return walk.template next<SUBS>(p);   // (narrow blocks always have equal ranges)
         int index = blockIdx.x;   // the first unit by number, the others as CTAs become free
         if (begun) {
           if (lane == 0) index = gridDim.x + atomicAdd(p.counter, 1);
@@ -918,7 +931,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
         return paged_item<SUBS, EXT>(p, index, false, D).u;
       };
       if (NARROW || p.even) walk = paged_walk<SUBS, EXT>(p, static_cast<int>(blockIdx.x));
-      PagedUnit w = next_unit();
+      PagedUnit<EXT> w = next_unit();
       int tiles = 0, loads = 0;   // tiles of the segments before; Q loads
       bool ok = true;
       for (int k = 0;; ++k) {
@@ -986,7 +999,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
       bool ok = true;
       for (int k = 0;; ++k) {
         named_sync(kBarProducers, Cfg::kProducers * 32);
-        const PagedUnit w = shared->unit[k & 1];
+        const PagedUnit<EXT> w = shared->unit[k & 1];
         if (!w.valid) break;
         int n = tiles_for(w, 0);
         if (SUBS == 2) n = max(n, tiles_for(w, 1));
@@ -1012,7 +1025,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
       int base = 0;
       for (int k = 0;; ++k) {
         named_sync(kBarSegment, Cfg::kSegmentThreads);
-        const PagedUnit& w = shared->unit[k & 1];
+        const PagedUnit<EXT>& w = shared->unit[k & 1];
         if (!w.valid) break;
         const int n0 = tiles_for(w, 0), nmax = SUBS == 2 ? max(n0, tiles_for(w, 1)) : n0;
         for (int j = 0; j < nmax; ++j) {
@@ -1067,7 +1080,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
       int base = 0, done0 = 0, loads = 0;
       for (int k = 0;; ++k) {
         named_sync(kBarSegment, Cfg::kSegmentThreads);
-        const PagedUnit& w = shared->unit[k & 1];
+        const PagedUnit<EXT>& w = shared->unit[k & 1];
         if (!w.valid) break;
         const int n0 = tiles_for(w, 0), n1 = SUBS == 2 ? tiles_for(w, 1) : 0, nmax = max(n0, n1);
         if (nmax == 0) continue;
@@ -1177,18 +1190,19 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
     int base = 0, done = 0, outs = 0;   // outs: segments in which this sub-tile had tiles
     for (int k = 0;; ++k) {
       named_sync(kBarSegment, Cfg::kSegmentThreads);
-      const PagedUnit& w = shared->unit[k & 1];
+      const PagedUnit<EXT>& w = shared->unit[k & 1];
       if (!w.valid) break;
       const int n0 = tiles_for(w, 0), n1 = SUBS == 2 ? tiles_for(w, 1) : 0, nmax = max(n0, n1);
       const int n_tiles = sub == 0 ? n0 : n1;
       const int rows = max(0, min(p.sub_tokens, w.ntok - sub_tok0)) * p.G;   // live rows
       const bool live = row < rows;
       const bool warp_live = NARROW || wq * 32 < rows;
+      int kv_len = w.kv_len;
       const int t_begin = w.t_begin;
-      const int lim = live ? paged_kept(p.causal, w.kv_len, w.q_len, w.tok0 + sub_tok0 + tok) : 0;
+      const int lim = live ? paged_kept(p.causal, kv_len, w.q_len, w.tok0 + sub_tok0 + tok) : 0;
       // every live row keeps at least the first token's keys
-      int lim_min = paged_kept(p.causal, w.kv_len, w.q_len, w.tok0 + sub_tok0);
-      int kv_len = w.kv_len, low_max = 0;
+      int lim_min = paged_kept(p.causal, kv_len, w.q_len, w.tok0 + sub_tok0);
+      int low_max = 0;
       if constexpr (EXT) {   // numbers of the list from here on
         // keys below this one may lie outside some live row's window
         low_max = paged_kept(p.causal, kv_len, w.q_len, w.tok0 + min(sub_tok0 + p.sub_tokens, w.ntok) - 1) - p.window -
@@ -1278,7 +1292,7 @@ __global__ void __launch_bounds__(FwdShape<SUBS>::kThreads, FwdShape<SUBS>::kCta
             }
           };
           // the row max, and the offset moved to it when it exceeds it by more than kRescaleLog2
-          float m_new = m, rs = 0.f;
+          float m_new = m, rs;
           float alpha = 1.f;
           const bool windows = EXT && p.role == kPagedPlain;
           bool settle = windows && t_begin + j <= (w.sink_keys >> 7) + 1;
@@ -1598,7 +1612,7 @@ __global__ void __launch_bounds__(kPagedMergeWarps * 32) fa2_paged_merge_kernel(
   __shared__ float4 sums[kPagedMergeWarps - 1][D / 16][32];
   __shared__ float2 weights[kPagedMergeWarps - 1][32];
   const int index = static_cast<int>(blockIdx.x);
-  const PagedParts w = p.even ? paged_parts_even<SUBS, EXT>(p, index) : paged_item<SUBS, EXT>(p, index, true, D);
+  const PagedParts<EXT> w = p.even ? paged_parts_even<SUBS, EXT>(p, index) : paged_item<SUBS, EXT>(p, index, true, D);
   // launched while the partial results are computed: they are complete from here on
   // (what was read above the kernel before this one does not write, and that one lets
   // this one start behind its own wait for what came before it)
