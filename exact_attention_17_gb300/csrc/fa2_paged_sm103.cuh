@@ -83,12 +83,12 @@
 //
 // Bound and measured.  Single tokens: bytes (64 sequences of 1000-8192 keys, 8
 // key/value heads of 128: 1.11 GB in 169.5-172 us, 6.48-6.57 TB/s; four of
-// 100000-131072 keys, d = 64: 84.3-85.7 us, 5.6-5.7 TB/s).  Chunks: the tensor pipe,
+// 100000-131072 keys, d = 64: 84.3-86.5 us, 5.6-5.7 TB/s).  Chunks: the tensor pipe,
 // fed by one issuing thread per SM, and the K/V tiles that the SMs read from L2
 // (8192 tokens over 16384 keys, 32 heads of 128, causal: 1115-1150 us on different
 // GPUs, 1435-1480 TFLOP/s; d = 256: 159-160 us for 146 GFLOP, each SM reading 128 KB
 // a tile).  Small calls: latency, 4 us from the launch to the first S, 2 us a tile,
-// and the merge (two tokens over 1000 keys: 13.8-14.1 us, the merge's launch
+// and the merge (two tokens over 1000 keys: 13.8-14.4 us, the merge's launch
 // included).
 #pragma once
 
